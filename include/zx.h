@@ -354,6 +354,127 @@ zx_status zx_kv_slot_container(const zx_kv_pool *pool, uint32_t slot, zx_contain
 zx_status zx_kv_decode_slots(const zx_kv_pool *pool, const uint32_t *slot_ids, uint32_t count,
                              void *out, uint32_t *err, hipStream_t stream);
 
+/* ---- paged K/V cache --------------------------------------------------------------
+ * The uncompressed side of a K/V cache: new keys and values are appended token by
+ * token into pages, attention reads the pages, and full pages can be compressed into a
+ * slot pool (above) and brought back.  A page holds page_tokens tokens of every K/V
+ * head; with 512 tokens of 128 channels each head's part of a page is one
+ * 65536-element block.
+ *
+ * Sequence s of a batch has the packed rows q_start[s] .. q_start[s+1] - 1 as its new
+ * tokens and kv_len[s] tokens in all, the new ones included: its new token i stands at
+ * position kv_len[s] - nq + i.  Token t of it is token t % page_tokens of page
+ * page_table[s][t / page_tokens].
+ *
+ * Every array is read on the device when the work runs, so lengths and tables may be
+ * rewritten between the replays of a captured graph.  The device checks them: a sequence
+ * with decreasing or out-of-range q_start, more than max_q new tokens, a negative length
+ * or more than max_kv tokens is left out (nothing of it is read or written), and a page
+ * id outside [0, n_pages) stands for tokens that are not there; both set err to
+ * ZX_E_CORRUPT.  New tokens at negative positions (kv_len < nq) are not appended and
+ * attend to nothing.  Rows behind the last sequence are neither read nor written. */
+typedef struct zx_paged_cache {
+    int32_t dtype;                 /* ZX_BF16 or ZX_FP8_E4M3FN                          */
+    uint32_t n_pages;
+    uint32_t kv_heads;
+    uint32_t head_dim;             /* 64, 128 or 256                                    */
+    uint32_t page_tokens;          /* a power of two, 16..4096                          */
+    uint32_t block_tokens;         /* tokens a bound covers: a power of two, 16..256,
+                                      at most page_tokens; 0: no bounds                 */
+    void *k, *v;                   /* element (page, head, token, c) of k at
+                                      page * k_page_stride + head * k_head_stride
+                                      + token * k_token_stride + c; v the same way      */
+    uint64_t k_page_stride, k_head_stride, k_token_stride;   /* in elements, each a     */
+    uint64_t v_page_stride, v_head_stride, v_token_stride;   /* multiple of 16 bytes    */
+    const float *k_scale, *v_scale; /* FP8: [kv_heads], positive; a stored value x stands
+                                      for x * scale[head]; NULL: 1.  BF16: NULL         */
+    uint16_t *bounds;              /* BF16 [n_pages][kv_heads][page_tokens /
+                                      block_tokens][2][head_dim]: the smallest and the
+                                      largest stored key of each channel (before
+                                      k_scale); NULL: none                              */
+} zx_paged_cache;
+
+typedef struct zx_paged_batch {
+    uint32_t n_seqs;
+    uint32_t table_width;          /* page_table: [n_seqs][table_width]                 */
+    uint32_t max_q;                /* no sequence has more new tokens than this         */
+    uint32_t max_kv;               /* no sequence has more tokens than this (at most
+                                      table_width * page_tokens is used)                */
+    const int32_t *q_start;        /* [n_seqs + 1]                                      */
+    const int32_t *kv_len;         /* [n_seqs]                                          */
+    const int32_t *page_table;
+} zx_paged_batch;
+
+/* BF16 rows [token][head][head_dim] (a host struct): strides in elements, multiples of 8. */
+typedef struct zx_rows {
+    void *p;
+    uint64_t token_stride, head_stride;
+} zx_rows;
+
+/* Rotary positions: channel pairs j < dims / 2 are turned by angle position *
+ * inv_freq[j] and scaled by `magnitude`; a pair is channels (j, j + dims / 2), or
+ * (2 j, 2 j + 1) when interleaved.  Channels from dims on are left alone. */
+typedef struct zx_rotary {
+    const double *inv_freq;        /* device, [dims / 2]                                */
+    uint32_t dims;                 /* a multiple of 16, at most head_dim                */
+    int32_t interleaved;
+    float magnitude;
+    uint32_t reserved_;
+} zx_rotary;
+
+/* Append the new tokens' keys and values to the cache, rotated on the way (`rot` not
+ * NULL), and write the queries rotated the same way to q_out (q not NULL; q_out may be
+ * q itself).  Keys are rotated in 32 bits and rounded once, to BF16 or, divided by the
+ * head's scale, to E4M3 (saturating; NaN stays NaN); angles are taken in 64 bits.
+ *   n_tokens    packed rows of k, v and q
+ *   positions   int32[n_tokens] for the rotation, or NULL: the tokens' places
+ * Bounds, where the cache has them: a block's first token starts its bounds anew, later
+ * ones widen them (a token written again at its place widens them too: they stay
+ * bounds, not the tightest ones); NaN keys are left out.  Each page that is written must
+ * belong to one sequence only. */
+zx_status zx_paged_append(const zx_paged_cache *cache, const zx_paged_batch *batch, uint32_t n_tokens,
+                          const zx_rows *k, const zx_rows *v, const zx_rotary *rot, const int32_t *positions,
+                          const zx_rows *q, uint32_t q_heads, const zx_rows *q_out, uint32_t *err,
+                          hipStream_t stream);
+
+/* Attention of the new tokens over the cache: softmax(scale * q . k) v for each of
+ * q_heads query heads (a multiple of kv_heads; query head i reads K/V head
+ * i / (q_heads / kv_heads)), over the tokens of its sequence up to its own position
+ * (causal) or all of them, and, with window > 0, only those less than `window` places
+ * before its own.  A row that sees no token is zero, its lse -inf.
+ *   out     BF16 rows [n_tokens][q_heads][head_dim]
+ *   lse     float[n_tokens][q_heads]: ln of the sum of exp(scaled scores), or NULL
+ *   scale   positive
+ *   blocks  int32[n_tokens][kv_heads][n_blocks] or NULL: only these blocks of
+ *           block_tokens tokens are read, counted from the sequence's start; the list of a
+ *           row ends at its first negative entry, and a block entered twice counts
+ *           twice.  Needs causal != 0 and window 0.
+ *   workspace  zx_paged_attend_workspace_bytes(...) bytes, 16-byte aligned; its contents
+ *           do not matter before the call or after it
+ * Scores, the softmax's sums and the output are accumulated in 32 bits; weights are
+ * rounded to BF16 before they meet the values.  Equal inputs give equal bits. */
+size_t zx_paged_attend_workspace_bytes(const zx_paged_cache *cache, const zx_paged_batch *batch,
+                                       uint32_t n_tokens, uint32_t q_heads, uint32_t n_blocks);
+zx_status zx_paged_attend(const zx_paged_cache *cache, const zx_paged_batch *batch, uint32_t n_tokens,
+                          const zx_rows *q, uint32_t q_heads, const zx_rows *out, float *lse, float scale,
+                          int causal, uint32_t window, const int32_t *blocks, uint32_t n_blocks, void *workspace,
+                          size_t ws_bytes, uint32_t *err, hipStream_t stream);
+
+/* For each new token and K/V head, the blocks worth reading: an upper bound of the group's
+ * summed scores with any key of a block, sum over query heads g and channels d of
+ * max(q_gd min_d, q_gd max_d) from the cache's bounds, is taken for every block up to the
+ * token's own; the first keep_first blocks, the newest keep_last and then those of the
+ * largest bounds are entered, top_k in all, in ascending order, -1 behind them.  Bounds
+ * are summed in 64 bits; of equal ones the earlier block goes first; NaN comes last.
+ *   top_k      1..1024, at least keep_first + keep_last
+ *   blocks     out, int32[n_tokens][kv_heads][top_k]
+ *   workspace  zx_paged_select_workspace_bytes(...) bytes, 16-byte aligned */
+size_t zx_paged_select_workspace_bytes(const zx_paged_cache *cache, const zx_paged_batch *batch, uint32_t n_tokens);
+zx_status zx_paged_select(const zx_paged_cache *cache, const zx_paged_batch *batch, uint32_t n_tokens,
+                          const zx_rows *q, uint32_t q_heads, uint32_t top_k, uint32_t keep_first,
+                          uint32_t keep_last, int32_t *blocks, void *workspace, size_t ws_bytes, uint32_t *err,
+                          hipStream_t stream);
+
 /* ---- dominant-range codec ---------------------------------------------------------
  * A second codec behind the same conventions (ZipFloat page, sections 3.1-3.3): blocks
  * of 2048 elements; per block, MD is the most frequent exponent (ties to the smallest)

@@ -12,3 +12,4 @@ from .zx import (  # noqa: F401
 )
 from .kvslots import KVSlotPool  # noqa: F401,E402
 from .pipeline import LayerPipeline  # noqa: F401,E402
+from .paged import PagedBatch, PagedKVCache, Rotary  # noqa: F401,E402

@@ -1,0 +1,646 @@
+// zx_paged_attend.hip -- attention of new tokens over a paged K/V cache.
+//
+// For query row r and the tokens t it sees: s_t = scale q.k_t, o = sum e^(s_t - m) v_t /
+// sum e^(s_t - m).  Both kernels go over the tokens once, with the running maximum m and
+// sum l of a softmax, in powers of two (s_t log2 e).  The rows of one K/V head are its
+// group's query heads for each new token, r = token * group + head, so a token's keys and
+// values are read once for the whole group.
+//
+// Scores are computed transposed, S^T = K Q^T, and the output too, O^T = V^T P^T: in the
+// matrix instruction's result layout a lane then holds one query row, so the row's
+// statistics are lane-local values, and a lane's scores are, in their order, the operand
+// that the second product wants (any order of tokens will do there, if the values' order
+// is the same).
+//
+//   k_rows   few rows (single tokens, groups of a few): bound by the bytes of K and V.
+//            Every wave reads its own tokens straight into the operand registers, with no
+//            LDS in the loop; the waves and the workgroups that share a row are joined at the end.
+//   k_chunk  many rows: bound by the matrix units.  Tiles of K and V in LDS serve 32 rows a wave.
+//   k_join   adds up what the workgroups of one row left.
+#include "zx_paged_attend.h"
+
+namespace zxp {
+namespace {
+
+// ---------------------------------------------------------------- few rows
+
+// The 16-token pieces a workgroup reads: consecutive ones of the sequence, or those of
+// the listed blocks.
+struct Place {
+    int32_t token;       // first token of the piece
+    uint32_t page;       // its page: 0 where there is none
+    bool there;
+};
+
+template <int DT, int D, int MT, bool LIST>
+__global__ __launch_bounds__(kRowsThreads) void k_rows(AttendArgs g)
+{
+    constexpr int ROWS = 16 * MT;
+    constexpr int ES = DT == ZX_BF16 ? 2 : 1;
+    constexpr int NK = D / 32;                       // matrix steps over the channels
+    constexpr int VW = D < 128 ? D / 16 : 8;         // value channels a lane reads of one token
+    constexpr int NP = D / (16 * VW);                // such pieces of a row
+    constexpr int VD = VW * ES / 4;                  // dwords of one
+    constexpr int KL = D * 16 * ES / 64 / 16;        // 16-byte loads a lane makes of 16 keys
+    constexpr int OS = D + 4;                        // LDS row of the join, in floats
+    __shared__ __align__(16) float ods[4 * 16 * OS];
+    __shared__ float mls[2][4][16];
+
+    const uint32_t lane = threadIdx.x & 63u;
+    const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const uint32_t lr = lane & 15u, lq = lane >> 4;
+    const uint32_t h = blockIdx.x % g.c.heads, item = blockIdx.x / g.c.heads;
+    const uint32_t G = g.group;
+
+    // which rows, which tokens
+    uint32_t seq, local, before, nch, chunk = 1, rt;
+    Seq sv;
+    if constexpr (LIST) {
+        const uint32_t tiles = div_up(G, ROWS);
+        nch = g.target;
+        if (!find_item(g.b, item, [&](const Seq &v) { return (uint32_t)v.nq * tiles * nch; }, [](const Seq &) { return 0u; }, seq, sv,
+                       local, before))
+            return;
+    } else {
+        chunk = chunk_steps<ROWS>(g);
+        if (!find_item(
+                g.b, item,
+                [&](const Seq &v) { return takes(g, v) ? div_up((uint32_t)v.nq * G, ROWS) * div_up(seq_steps(g, v), chunk) : 0u; },
+                [](const Seq &) { return 0u; }, seq, sv, local, before))
+            return;
+        nch = div_up(seq_steps(g, sv), chunk);
+    }
+    rt = local / nch;
+    const uint32_t part = local % nch;
+    uint32_t row0, nrows, tok0;                      // rows row0 .. of the token list starting at tok0
+    if constexpr (LIST) {
+        const uint32_t tiles = div_up(G, ROWS);
+        tok0 = rt / tiles;
+        row0 = (rt % tiles) * ROWS;
+        nrows = G - row0 < (uint32_t)ROWS ? G - row0 : (uint32_t)ROWS;
+    } else {
+        tok0 = 0;
+        row0 = rt * ROWS;
+        const uint32_t all = (uint32_t)sv.nq * G;
+        nrows = all - row0 < (uint32_t)ROWS ? all - row0 : (uint32_t)ROWS;
+    }
+
+    // each lane's rows: what they see, and their queries in the operand's layout.  Rows
+    // past the last one repeat it.
+    int32_t lo[MT], hi[MT];
+    u4 q[MT][NK];
+    const int32_t pos0 = sv.kv - sv.nq;
+    int32_t lo_min = 0x7FFFFFFF, lo_max = 0, hi_min = 0x7FFFFFFF, hi_max = 0;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        uint32_t r = t * 16 + lr;
+        r = row0 + (r < nrows ? r : nrows - 1);
+        const uint32_t tok = tok0 + r / G, gh = r % G;
+        const int32_t p = pos0 + (int32_t)tok;
+        lo[t] = first_seen(g, p);
+        hi[t] = end_seen(g, p, sv.kv);
+        const __bf16 *qp = g.q.p + (int64_t)(sv.q0 + (int32_t)tok) * g.q.token + (int64_t)(h * G + gh) * g.q.head;
+#pragma unroll
+        for (int s = 0; s < NK; ++s) {
+            // BF16 keys: step s, lane quarter lq holds channels 32 s + 8 lq ..; E4M3 keys come 16
+            // channels a load: 64 (s / 2) + 16 lq + 8 (s % 2) ..
+            const int ch = DT == ZX_BF16 ? 32 * s + 8 * (int)lq : 64 * (s / 2) + 16 * (int)lq + 8 * (s % 2);
+            q[t][s] = *reinterpret_cast<const u4 *>(qp + ch);
+        }
+    }
+    {
+        const uint32_t ta = tok0 + row0 / G, tb = tok0 + (row0 + nrows - 1) / G;   // first and last token of the rows
+        const int32_t pa = pos0 + (int32_t)ta, pb = pos0 + (int32_t)tb;
+        lo_min = first_seen(g, pa);
+        lo_max = first_seen(g, pb);
+        hi_min = end_seen(g, pa, sv.kv);
+        hi_max = end_seen(g, pb, sv.kv);
+    }
+
+    // the pieces of 16 tokens this workgroup reads: u0 .. u1 - 1
+    const int32_t *table = g.b.table + (uint64_t)seq * g.b.width;
+    const int32_t *list = nullptr;
+    uint32_t u0, u1;
+    const uint32_t lb = g.c.log_block;
+    if constexpr (LIST) {
+        list = g.blocks + ((uint64_t)(sv.q0 + (int32_t)tok0) * g.c.heads + h) * g.n_blocks;
+        uint32_t n = 0;
+        while (n < g.n_blocks) {
+            const uint64_t neg = __ballot(n + lane >= g.n_blocks || list[n + lane < g.n_blocks ? n + lane : 0] < 0);
+            if (neg) {
+                n += (uint32_t)__builtin_ctzll(neg);
+                break;
+            }
+            n += 64;
+        }
+        const uint32_t steps = div_up(n << (lb - 4), kStep / 16), per = div_up(steps, nch);
+        u0 = part * per * (kStep / 16);
+        u1 = u0 + per * (kStep / 16);
+        if (u1 > n << (lb - 4)) u1 = n << (lb - 4);
+    } else {
+        const uint32_t base = (uint32_t)(first_seen(g, pos0) >> 4);
+        u0 = base + part * chunk * (kStep / 16);
+        u1 = u0 + chunk * (kStep / 16);
+        if (u0 < (uint32_t)(lo_min >> 4)) u0 = (uint32_t)(lo_min >> 4);
+        if (u1 > (uint32_t)((hi_max + 15) >> 4)) u1 = (uint32_t)((hi_max + 15) >> 4);
+    }
+
+    auto place = [&](uint32_t u) {
+        Place p;
+        p.there = u < u1;
+        uint32_t t = 0;
+        if (p.there) {
+            if constexpr (LIST) {
+                const uint32_t e = (uint32_t)list[u >> (lb - 4)];
+                t = e << lb;
+                p.there = e <= (uint32_t)sv.kv >> lb;       // entries past the sequence see nothing
+                t += (u & ((1u << (lb - 4)) - 1u)) << 4;
+                p.there = p.there && t < (uint32_t)sv.kv;
+            } else {
+                t = u << 4;
+            }
+        }
+        uint32_t page = 0;
+        if (p.there) {
+            page = (uint32_t)table[t >> g.c.log_page];
+            if (page >= g.c.n_pages) {
+                report(g.b.err, ZX_E_CORRUPT);
+                page = 0;
+                p.there = false;
+            }
+        }
+        p.token = (int32_t)t;
+        p.page = page;
+        return p;
+    };
+    const uint32_t pmask = (1u << g.c.log_page) - 1u;
+    const uint32_t koff = lr * g.c.k_token + lq * 16u;
+    const uint32_t voff = lq * 4u * g.c.v_token + lr * (VW * ES);
+    auto kbase = [&](const Place &p) {
+        return g.c.k + (int64_t)p.page * g.c.k_page + (int64_t)h * g.c.k_head + (uint64_t)((uint32_t)p.token & pmask) * g.c.k_token;
+    };
+    auto vbase = [&](const Place &p) {
+        return g.c.v + (int64_t)p.page * g.c.v_page + (int64_t)h * g.c.v_head + (uint64_t)((uint32_t)p.token & pmask) * g.c.v_token;
+    };
+
+    u4 kreg[2][KL];
+    uint32_t vreg[8][NP][VD];
+    auto load_k = [&](const Place (&p)[2]) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            const uint8_t *b = kbase(p[a]);
+#pragma unroll
+            for (int i = 0; i < KL; ++i) kreg[a][i] = *reinterpret_cast<const u4 *>(b + koff + 64u * i);
+        }
+    };
+    auto load_v = [&](const Place (&p)[2]) {
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+            const uint8_t *b = vbase(p[a]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int n = 0; n < NP; ++n) {
+                    const uint8_t *s = b + voff + (uint32_t)i * g.c.v_token + n * (16 * VW * ES);
+                    if constexpr (VD == 4) {
+                        const u4 x = *reinterpret_cast<const u4 *>(s);
+#pragma unroll
+                        for (int w = 0; w < 4; ++w) vreg[4 * a + i][n][w] = x[w];
+                    } else if constexpr (VD == 2) {
+                        const u2 x = *reinterpret_cast<const u2 *>(s);
+                        vreg[4 * a + i][n][0] = x[0];
+                        vreg[4 * a + i][n][1] = x[1];
+                    } else {
+                        vreg[4 * a + i][n][0] = *reinterpret_cast<const uint32_t *>(s);
+                    }
+                }
+        }
+    };
+
+    float m[MT], l[MT];
+    f4 o[MT][NP][VW];
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        m[t] = -kInf;
+        l[t] = 0.0f;
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+#pragma unroll
+            for (int j = 0; j < VW; ++j) o[t][n][j] = f4{0, 0, 0, 0};
+    }
+    const float c = g.scale * (g.c.k_scale ? g.c.k_scale[h] : 1.0f);
+
+    uint32_t u = u0 + 2 * wave;
+    Place here[2], next[2];
+    if (u < u1) {
+        here[0] = place(u);
+        here[1] = place(u + 1);
+        load_k(here);
+        load_v(here);
+        next[0] = place(u + 8);
+        next[1] = place(u + 9);
+    }
+    for (; u < u1; u += 8) {
+        // scores: 16 tokens x 16 rows a tile; a lane has row lr, tokens 4 lq .. 4 lq + 3 of each piece
+        f4 s[MT][2];
+#pragma unroll
+        for (int a = 0; a < 2; ++a) {
+#pragma unroll
+            for (int t = 0; t < MT; ++t) s[t][a] = f4{0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < NK; ++i) {
+                u4 kk;
+                if constexpr (DT == ZX_BF16) {
+                    kk = kreg[a][i];
+                } else {
+                    const uint32_t w0 = kreg[a][i / 2][2 * (i % 2)], w1 = kreg[a][i / 2][2 * (i % 2) + 1];
+                    kk = u4{fp8_pair<false>(w0), fp8_pair<true>(w0), fp8_pair<false>(w1), fp8_pair<true>(w1)};
+                }
+#pragma unroll
+                for (int t = 0; t < MT; ++t)
+                    s[t][a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, kk), __builtin_bit_cast(bf8, q[t][i]), s[t][a], 0, 0, 0);
+            }
+        }
+        const bool more = u + 8 < u1;
+        if (more) load_k(next);
+
+        // does any row not see any of these tokens?
+        bool part_seen = false;
+#pragma unroll
+        for (int a = 0; a < 2; ++a)
+            part_seen = part_seen || !here[a].there || here[a].token < lo_max || here[a].token + 16 > hi_min;
+#pragma unroll
+        for (int t = 0; t < MT; ++t) {
+            float mx = -kInf;
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    float x = s[t][a][i] * c;
+                    if (part_seen) {
+                        const int32_t tk = here[a].token + 4 * (int32_t)lq + i;
+                        x = here[a].there && tk >= lo[t] && tk < hi[t] ? x : -kInf;
+                    }
+                    s[t][a][i] = x;
+                    mx = fmaxf(mx, x);
+                }
+            mx = max_quarters(mx);
+            if (__any(mx > m[t] + kSlack)) {
+                const float nm = fmaxf(m[t], mx), base = nm == -kInf ? 0.0f : nm;
+                const float f = __builtin_amdgcn_exp2f(m[t] - base);
+                m[t] = nm;
+                l[t] *= f;
+#pragma unroll
+                for (int n = 0; n < NP; ++n)
+#pragma unroll
+                    for (int j = 0; j < VW; ++j) o[t][n][j] *= f;
+            }
+            const float base = m[t] == -kInf ? 0.0f : m[t];
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    s[t][a][i] = __builtin_amdgcn_exp2f(s[t][a][i] - base);
+                    l[t] += s[t][a][i];
+                }
+        }
+        // weights as the second product's operand: tokens 4 lq .. + 3 of both pieces, as the values have them
+        u4 p[MT];
+#pragma unroll
+        for (int t = 0; t < MT; ++t)
+            p[t] = u4{pack2(s[t][0][0], s[t][0][1]), pack2(s[t][0][2], s[t][0][3]), pack2(s[t][1][0], s[t][1][1]), pack2(s[t][1][2], s[t][1][3])};
+
+        // values that no row sees are not there (pages hold anything behind a sequence's end)
+        bool odd = false;
+        if (part_seen) {
+#pragma unroll
+            for (int a = 0; a < 2; ++a)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int32_t tk = here[a].token + 4 * (int32_t)lq + i;
+                    const bool seen = here[a].there && tk >= lo_min && tk < hi_max;
+#pragma unroll
+                    for (int n = 0; n < NP; ++n)
+#pragma unroll
+                        for (int w = 0; w < VD; ++w) vreg[4 * a + i][n][w] = seen ? vreg[4 * a + i][n][w] : 0u;
+                }
+        }
+        const bool differ = part_seen && (lo_min != lo_max || hi_min != hi_max);
+#pragma unroll
+        for (int n = 0; n < NP; ++n) {
+#pragma unroll
+            for (int w = 0; w < VW / 2; ++w) {
+                // channel pair w of eight tokens, as BF16 pairs of channels ...
+                uint32_t x[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    if constexpr (DT == ZX_BF16) x[i] = vreg[i][n][w];
+                    else x[i] = w % 2 ? fp8_pair<true>(vreg[i][n][w / 2]) : fp8_pair<false>(vreg[i][n][w / 2]);
+                }
+                // ... and turned into pairs of tokens
+                u4 v0, v1;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    v0[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x05040100u);
+                    v1[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x07060302u);
+                }
+                if (differ) {
+                    // rows see different tokens here: an infinity or NaN may belong to some rows only
+                    bool any = false;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) any = any || odd_pair(v0[i]) || odd_pair(v1[i]);
+                    odd = __any(any);
+                    if (odd) {
+#pragma unroll
+                        for (int t = 0; t < MT; ++t) {
+                            u4 see;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const int a = k / 2, i = 2 * (k % 2);
+                                const int32_t tk = here[a].token + 4 * (int32_t)lq + i;
+                                see[k] = (here[a].there && tk >= lo[t] && tk < hi[t] ? 0x3F80u : 0u) |
+                                         (here[a].there && tk + 1 >= lo[t] && tk + 1 < hi[t] ? 0x3F800000u : 0u);
+                            }
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const u4 v = e ? v1 : v0;
+                                u4 wp, wn;
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) {
+                                    wp[k] = wild_pair<0>(v[k]);
+                                    wn[k] = wild_pair<1>(v[k]);
+                                }
+                                const f4 z = {0, 0, 0, 0};
+                                const f4 np = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, wp), __builtin_bit_cast(bf8, see), z, 0, 0, 0);
+                                const f4 nn = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, wn), __builtin_bit_cast(bf8, see), z, 0, 0, 0);
+#pragma unroll
+                                for (int i = 0; i < 4; ++i) {
+                                    if (np[i] > 0.0f) o[t][n][2 * w + e][i] += kInf;
+                                    if (nn[i] > 0.0f) o[t][n][2 * w + e][i] -= kInf;
+                                }
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            v0[k] = tame_pair(v0[k]);
+                            v1[k] = tame_pair(v1[k]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int t = 0; t < MT; ++t) {
+                    o[t][n][2 * w] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, v0), __builtin_bit_cast(bf8, p[t]), o[t][n][2 * w], 0, 0, 0);
+                    o[t][n][2 * w + 1] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, v1), __builtin_bit_cast(bf8, p[t]), o[t][n][2 * w + 1], 0, 0, 0);
+                }
+            }
+        }
+        if (more) {
+            load_v(next);
+            here[0] = next[0];
+            here[1] = next[1];
+            next[0] = place(u + 16);
+            next[1] = place(u + 17);
+        }
+    }
+
+    // join the four waves, 16 rows at a time
+    const float vs = g.c.v_scale ? g.c.v_scale[h] : 1.0f;
+    const uint64_t slot = ((uint64_t)item * g.c.heads + h) * ROWS;
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        if (t) __syncthreads();
+        l[t] = sum_quarters(l[t]);
+        if (lq == 0) {
+            mls[0][wave][lr] = m[t];
+            mls[1][wave][lr] = l[t];
+        }
+        // a lane has, of row lr, channels n * 16 VW + (4 lq + i) VW + j
+        float *dst = ods + (wave * 16 + lr) * OS;
+#pragma unroll
+        for (int n = 0; n < NP; ++n)
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < VW; j += 4)
+                    *reinterpret_cast<f4 *>(dst + n * 16 * VW + (4 * lq + i) * VW + j) = f4{o[t][n][j][i], o[t][n][j + 1][i], o[t][n][j + 2][i], o[t][n][j + 3][i]};
+        __syncthreads();
+        for (uint32_t e = threadIdx.x; e < 16 * (D / 8); e += kRowsThreads) {
+            const uint32_t r = e / (D / 8), ch = (e % (D / 8)) * 8;
+            const uint32_t row = t * 16 + r;
+            if (row >= nrows) continue;
+            float mm = -kInf;
+#pragma unroll
+            for (int w = 0; w < 4; ++w) mm = fmaxf(mm, mls[0][w][r]);
+            const float base = mm == -kInf ? 0.0f : mm;
+            float ll = 0.0f, x[8] = {};
+#pragma unroll
+            for (int w = 0; w < 4; ++w) {
+                const float f = __builtin_amdgcn_exp2f(mls[0][w][r] - base);
+                ll += mls[1][w][r] * f;
+                const float *src = ods + (w * 16 + r) * OS + ch;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] += src[i] * f;
+            }
+            if (nch == 1) {
+                const uint32_t tok = tok0 + (row0 + row) / G, gh = (row0 + row) % G;
+                const int64_t at = sv.q0 + (int32_t)tok;
+                const float inv = ll == 0.0f ? 0.0f : vs / ll;
+                bf8 y;
+#pragma unroll
+                for (int i = 0; i < 8; ++i) y[i] = (__bf16)(x[i] * inv);
+                *reinterpret_cast<bf8 *>(g.out.p + at * g.out.token + (int64_t)(h * G + gh) * g.out.head + ch) = y;
+                if (g.lse && ch == 0) g.lse[at * g.q_heads + h * G + gh] = ll == 0.0f ? -kInf : (mm + log2f(ll)) * kLn2;
+            } else {
+                float *dst2 = g.part + (slot + row) * D + ch;
+                reinterpret_cast<f4 *>(dst2)[0] = f4{x[0], x[1], x[2], x[3]};
+                reinterpret_cast<f4 *>(dst2)[1] = f4{x[4], x[5], x[6], x[7]};
+                if (ch == 0) {
+                    g.stat[(slot + row) * 2] = mm;
+                    g.stat[(slot + row) * 2 + 1] = ll;
+                }
+            }
+        }
+    }
+}
+
+// ---------------------------------------------------------------- host
+
+struct Plan {
+    bool rows, chunk;                // which kernels run
+    uint32_t mt, rows_items, rows_target, rows_slots, rows_max;
+    uint32_t waves, chunk_items, chunk_split;
+    bool rows_join, chunk_join;
+    uint64_t rows_part, rows_stat, chunk_part, chunk_stat, bytes;   // offsets into the workspace
+};
+
+constexpr uint32_t kFewRows = 32;    // rows of a sequence that k_rows takes
+constexpr uint32_t kRowsGroups = 768;
+
+inline uint32_t bound_tiles(uint64_t n, uint64_t seqs, uint64_t group, uint64_t rows)
+{
+    // sum over the sequences of ceil(nq * group / rows)
+    const uint64_t a = n * ceil_div(group, rows), b = n * group / rows + seqs;
+    return (uint32_t)(a < b ? a : b);
+}
+
+Plan make_plan(const zx_paged_cache *c, const zx_paged_batch *b, uint32_t n, uint32_t q_heads, uint32_t n_blocks)
+{
+    Plan p{};
+    const uint32_t G = q_heads / c->kv_heads, H = c->kv_heads, D = c->head_dim;
+    const uint64_t room = (uint64_t)b->table_width * c->page_tokens, cap = b->max_kv < room ? b->max_kv : room;
+    const uint32_t max_q = b->max_q < n ? b->max_q : n;
+    const uint32_t seqs = b->n_seqs < n ? b->n_seqs : n;      // sequences with new tokens
+    auto area = [&](uint64_t bytes) {
+        const uint64_t at = p.bytes;
+        p.bytes += (bytes + 255) & ~255ull;
+        return at;
+    };
+    if (n_blocks) {
+        p.rows = true;
+        p.mt = 1;
+        p.rows_items = n * ceil_div(G, 16);
+        const uint32_t steps = ceil_div((uint64_t)n_blocks * c->block_tokens, kStep);
+        uint32_t s = ceil_div(kRowsGroups, (uint64_t)p.rows_items * H);
+        if (s > steps) s = steps;
+        p.rows_target = s ? s : 1;
+        p.rows_slots = p.rows_items * p.rows_target;
+        p.rows_join = p.rows_target > 1;
+        p.rows_max = G < 16 ? G : 16;
+    } else {
+        p.chunk = (uint64_t)max_q * G > kFewRows;
+        p.rows = !p.chunk || seqs > 1;       // a batch may mix single tokens with long chunks
+        if (p.rows) {
+            p.mt = D <= 128 && (uint64_t)max_q * G > 16 ? 2 : 1;
+            const uint32_t R = 16 * p.mt, tiles = p.chunk ? seqs * (kFewRows / R) : bound_tiles(n, seqs, G, R);
+            p.rows_target = ceil_div(kRowsGroups, H);
+            p.rows_slots = p.rows_target + tiles;
+            p.rows_items = tiles;
+            p.rows_join = cap > kStep;
+            const uint64_t most = (uint64_t)max_q * G;
+            p.rows_max = most < 1 ? 1 : (uint32_t)(most < R ? most : R);
+        }
+        if (p.chunk) {
+            p.waves = chunk_waves((uint64_t)max_q * G, D);
+            const uint32_t R = 32 * p.waves;
+            p.chunk_items = bound_tiles(n, seqs, G, R);
+            // split the tokens of a row tile where the row tiles alone leave most of the card idle
+            uint32_t s = 512 / (p.chunk_items * H ? p.chunk_items * H : 1);
+            const uint32_t most = (uint32_t)(cap / 512);
+            if (s > most) s = most;
+            p.chunk_split = s < 1 ? 1 : s > 64 ? 64 : s;
+            p.chunk_join = p.chunk_split > 1;
+        }
+    }
+    if (p.rows_join) {
+        const uint64_t r = (uint64_t)p.rows_slots * H * 16 * p.mt;
+        p.rows_part = area(r * D * 4);
+        p.rows_stat = area(r * 8);
+    }
+    if (p.chunk_join) {
+        const uint64_t r = (uint64_t)p.chunk_items * p.chunk_split * H * 32 * p.waves;
+        p.chunk_part = area(r * D * 4);
+        p.chunk_stat = area(r * 8);
+    }
+    return p;
+}
+
+template <int DT, int D>
+void run_plan(const Plan &p, AttendArgs g, uint32_t n_blocks, uint8_t *ws, hipStream_t stream)
+{
+    const uint32_t H = g.c.heads;
+    if (p.rows) {
+        AttendArgs a = g;
+        a.part = reinterpret_cast<float *>(ws + p.rows_part);
+        a.stat = reinterpret_cast<float *>(ws + p.rows_stat);
+        a.target = p.rows_target;
+        a.slots = p.rows_slots;
+        a.lo_rows = 0;
+        a.hi_rows = p.chunk ? kFewRows : 0xFFFFFFFFu;
+        const dim3 grid(p.rows_slots * H), block(kRowsThreads);
+        const dim3 jgrid(p.rows_items * H, 1, p.rows_max);
+        if (n_blocks) {
+            hipLaunchKernelGGL((k_rows<DT, D, 1, true>), grid, block, 0, stream, a);
+            if (p.rows_join) hipLaunchKernelGGL((k_join<D, 16, JOIN_LIST>), jgrid, dim3(256), 0, stream, a);
+        } else if (p.mt == 1) {
+            hipLaunchKernelGGL((k_rows<DT, D, 1, false>), grid, block, 0, stream, a);
+            if (p.rows_join) hipLaunchKernelGGL((k_join<D, 16, JOIN_ROWS>), jgrid, dim3(256), 0, stream, a);
+        } else if constexpr (D <= 128) {
+            hipLaunchKernelGGL((k_rows<DT, D, 2, false>), grid, block, 0, stream, a);
+            if (p.rows_join) hipLaunchKernelGGL((k_join<D, 32, JOIN_ROWS>), jgrid, dim3(256), 0, stream, a);
+        }
+    }
+    if (p.chunk) {
+        AttendArgs a = g;
+        a.part = reinterpret_cast<float *>(ws + p.chunk_part);
+        a.stat = reinterpret_cast<float *>(ws + p.chunk_stat);
+        a.target = p.chunk_split;
+        a.slots = p.chunk_items * p.chunk_split;
+        a.lo_rows = p.rows ? kFewRows : 0;
+        a.hi_rows = 0xFFFFFFFFu;
+        run_chunk(DT, D, p.waves, p.chunk_items, p.chunk_split, a, stream);
+    }
+}
+
+zx_status checks(const zx_paged_cache *cache, const zx_paged_batch *batch, uint32_t n_tokens, uint32_t q_heads, uint32_t n_blocks, uint32_t *err,
+                 AttendArgs &g)
+{
+    zx_status st = make_cache(cache, g.c);
+    if (st == ZX_OK) st = make_batch(batch, cache, n_tokens, err, g.b);
+    if (st != ZX_OK) return st;
+    if (q_heads == 0 || q_heads % cache->kv_heads || q_heads > 65536 || n_blocks > 65536) return ZX_E_INVAL;
+    if (n_blocks && !cache->block_tokens) return ZX_E_INVAL;
+    const uint64_t work = (uint64_t)n_tokens * q_heads;
+    if (work > 0x3FFFFFFFull) return ZX_E_LIMIT;
+    // the kernels count steps and pieces in 32 bits
+    const uint64_t tiles = (uint64_t)n_tokens * ceil_div(q_heads / cache->kv_heads, 16);
+    if (tiles * ((uint64_t)g.b.cap / kStep + 1) > 0x7FFFFFFFull || tiles * cache->kv_heads * (n_blocks ? 64 : 1) > 0x7FFFFFFFull) return ZX_E_LIMIT;
+    return ZX_OK;
+}
+
+}  // namespace
+}  // namespace zxp
+
+extern "C" size_t zx_paged_attend_workspace_bytes(const zx_paged_cache *cache, const zx_paged_batch *batch, uint32_t n_tokens,
+                                                  uint32_t q_heads, uint32_t n_blocks)
+{
+    zxp::AttendArgs g{};
+    if (zxp::checks(cache, batch, n_tokens, q_heads, n_blocks, nullptr, g) != ZX_OK || n_tokens == 0 || batch->n_seqs == 0) return 0;
+    return (size_t)zxp::make_plan(cache, batch, n_tokens, q_heads, n_blocks).bytes;
+}
+
+extern "C" zx_status zx_paged_attend(const zx_paged_cache *cache, const zx_paged_batch *batch, uint32_t n_tokens, const zx_rows *q,
+                                     uint32_t q_heads, const zx_rows *out, float *lse, float scale, int causal, uint32_t window,
+                                     const int32_t *blocks, uint32_t n_blocks, void *workspace, size_t ws_bytes, uint32_t *err,
+                                     hipStream_t stream)
+{
+    using namespace zxp;
+    AttendArgs g{};
+    if ((blocks == nullptr) != (n_blocks == 0)) return ZX_E_INVAL;
+    zx_status st = checks(cache, batch, n_tokens, q_heads, n_blocks, err, g);
+    if (st != ZX_OK) return st;
+    if (!(scale > 0.0f) || scale > 1e30f || window > 0x3FFFFFFFu || (blocks && (!causal || window))) return ZX_E_INVAL;
+    if (n_tokens == 0 || batch->n_seqs == 0) return ZX_OK;
+    if ((st = make_rows(q, g.q)) != ZX_OK || (st = make_rows(out, g.out)) != ZX_OK) return st;
+    const Plan p = make_plan(cache, batch, n_tokens, q_heads, n_blocks);
+    if (p.bytes && (!workspace || ws_bytes < p.bytes || !al16(workspace))) return ZX_E_INVAL;
+    g.lse = lse;
+    g.blocks = blocks;
+    g.n_blocks = n_blocks;
+    g.scale = scale * kLog2e;
+    g.causal = causal;
+    g.window = (int32_t)window;
+    g.group = q_heads / cache->kv_heads;
+    g.q_heads = q_heads;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const uint32_t D = cache->head_dim;
+    if (cache->dtype == ZX_BF16) {
+        if (D == 64) run_plan<ZX_BF16, 64>(p, g, n_blocks, ws, stream);
+        else if (D == 128) run_plan<ZX_BF16, 128>(p, g, n_blocks, ws, stream);
+        else run_plan<ZX_BF16, 256>(p, g, n_blocks, ws, stream);
+    } else {
+        if (D == 64) run_plan<ZX_FP8_E4M3FN, 64>(p, g, n_blocks, ws, stream);
+        else if (D == 128) run_plan<ZX_FP8_E4M3FN, 128>(p, g, n_blocks, ws, stream);
+        else run_plan<ZX_FP8_E4M3FN, 256>(p, g, n_blocks, ws, stream);
+    }
+    return hipGetLastError() == hipSuccess ? ZX_OK : ZX_E_HIP;
+}

@@ -1,0 +1,329 @@
+// zx_paged_select.hip -- which blocks of a paged K/V cache a new token should read.
+//
+// For a group of G query heads and a block with smallest and largest keys lo, hi per
+// channel, no key of the block scores more than
+//   sum_g sum_d max(q_gd lo_d, q_gd hi_d) = sum_d up_d hi_d + dn_d lo_d,
+//   up_d = sum_g max(q_gd, 0), dn_d = sum_g min(q_gd, 0):
+// one dot product of 2 D terms a block, whatever the group's size, over 4 D bytes of
+// bounds: bound by those bytes.  Which blocks are taken is a yes or no, and two ways of
+// adding up in 32 bits would now and then say differently for blocks next to the border,
+// so the sums are taken in 64 bits (the vector units' 64-bit multiply-add has the rate of the 32-bit one).
+//
+//   k_score  one key (the sum, as an integer that orders like it) per token, head and block
+//   k_top    the top_k-th largest key by radix selection, then the taken blocks in ascending order
+#include "zx_paged.h"
+
+namespace zxp {
+namespace {
+
+constexpr uint32_t kThreads = 256;
+constexpr uint32_t kHeld = 4096;        // keys of a row that k_top holds in LDS (32 KB)
+
+struct SelectArgs {
+    Cache c;
+    Batch b;
+    Rows q;
+    int32_t *blocks;
+    uint64_t *keys;                     // [rows of the slab][heads][nb]
+    uint32_t group, top_k, keep_first, keep_last;
+    uint32_t nb;                        // blocks of the longest sequence
+    uint32_t slab0, slab;               // token groups of this launch: slab0 .. slab0 + slab - 1
+    uint32_t per;                       // blocks of a workgroup of k_score
+};
+
+// An integer that orders like the double; NaN below everything.
+__device__ __forceinline__ uint64_t order_key(double x)
+{
+    const int64_t b = __double_as_longlong(x);
+    if (x != x) return 0;
+    return b < 0 ? ~(uint64_t)b : (uint64_t)b | 0x8000000000000000ull;
+}
+
+// Tokens of a sequence come in groups of TT that share what is read of the bounds.
+template <int D, int TT>
+__global__ __launch_bounds__(kThreads) void k_score(SelectArgs g)
+{
+    constexpr uint32_t LB = D / 8;                       // lanes of a block
+    constexpr uint32_t PB = kThreads / LB;               // blocks at a time
+    const uint32_t h = blockIdx.x % g.c.heads, grp = blockIdx.x / g.c.heads;
+    uint32_t seq, local, unused;
+    Seq sv;
+    if (!find_item(g.b, g.slab0 + grp, [](const Seq &v) { return div_up((uint32_t)v.nq, TT); }, [](const Seq &) { return 0u; }, seq, sv, local, unused)) return;
+    const uint32_t tok = local * TT, nt = (uint32_t)sv.nq - tok < (uint32_t)TT ? (uint32_t)sv.nq - tok : (uint32_t)TT;
+    const int32_t p9 = sv.kv - sv.nq + (int32_t)(tok + nt - 1);      // position of the last token
+    if (p9 < 0) return;
+    const uint32_t lb = g.c.log_block, seen = ((uint32_t)p9 >> lb) + 1;
+    if (seen <= g.top_k) return;                                     // every block is taken
+    const uint32_t j0 = blockIdx.y * g.per, j1 = j0 + g.per < seen ? j0 + g.per : seen;
+    if (j0 >= j1) return;
+
+    const uint32_t ln = threadIdx.x % LB, slot = threadIdx.x / LB;
+    double up[TT][8], dn[TT][8];
+#pragma unroll
+    for (int t = 0; t < TT; ++t) {
+        const uint32_t tt = tok + ((uint32_t)t < nt ? (uint32_t)t : nt - 1);
+        const __bf16 *qp = g.q.p + (int64_t)(sv.q0 + (int32_t)tt) * g.q.token + (int64_t)(h * g.group) * g.q.head + 8 * ln;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) up[t][i] = dn[t][i] = 0.0;
+        for (uint32_t e = 0; e < g.group; ++e) {
+            const bf8 x = *reinterpret_cast<const bf8 *>(qp + (int64_t)e * g.q.head);
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float y = (float)x[i];
+                // a NaN stays one in both sums
+                up[t][i] += (double)(y < 0.0f ? 0.0f : y);
+                dn[t][i] += (double)(y > 0.0f ? 0.0f : y);
+            }
+        }
+    }
+    const int32_t *table = g.b.table + (uint64_t)seq * g.b.width;
+    const uint32_t lp = g.c.log_page - lb, nbp = 1u << lp;
+    for (uint32_t j = j0 + slot; j < j1; j += PB) {
+        uint32_t page = (uint32_t)table[j >> lp];
+        const bool there = page < g.c.n_pages;
+        if (!there) {
+            report(g.b.err, ZX_E_CORRUPT);
+            page = 0;
+        }
+        const __bf16 *bp = g.c.bounds + (((uint64_t)page * g.c.heads + h) * nbp + (j & (nbp - 1u))) * (2 * D) + 8 * ln;
+        const bf8 lo = *reinterpret_cast<const bf8 *>(bp), hi = *reinterpret_cast<const bf8 *>(bp + D);
+        double s[TT];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) s[t] = 0.0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const double a = (double)(float)lo[i], b = (double)(float)hi[i];
+#pragma unroll
+            for (int t = 0; t < TT; ++t) s[t] = __builtin_fma(up[t][i], b, __builtin_fma(dn[t][i], a, s[t]));
+        }
+#pragma unroll
+        for (uint32_t w = LB / 2; w >= 1; w >>= 1)
+#pragma unroll
+            for (int t = 0; t < TT; ++t) s[t] += __shfl_xor(s[t], (int)w, 64);
+        if (ln < nt) {
+            double x = s[0];
+#pragma unroll
+            for (int t = 1; t < TT; ++t) x = ln == (uint32_t)t ? s[t] : x;
+            g.keys[((uint64_t)(grp * TT + ln) * g.c.heads + h) * g.nb + j] = there ? order_key(x) : 0;
+        }
+    }
+}
+
+template <int TT>
+__global__ __launch_bounds__(kThreads) void k_top(SelectArgs g)
+{
+    __shared__ uint64_t held[kHeld];
+    __shared__ uint32_t hist[256];
+    __shared__ uint64_t wide[2][4];
+    __shared__ uint32_t pick[3];
+    __shared__ uint32_t sums[2][4];
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
+    const uint32_t h = blockIdx.x % g.c.heads, row = blockIdx.x / g.c.heads;
+    uint32_t seq, local, unused;
+    Seq sv;
+    if (!find_item(g.b, g.slab0 * TT + row, [](const Seq &v) { return div_up((uint32_t)v.nq, TT) * TT; }, [](const Seq &) { return 0u; }, seq, sv, local, unused))
+        return;
+    if (local >= (uint32_t)sv.nq) return;
+    const int32_t p = sv.kv - sv.nq + (int32_t)local;
+    const uint32_t seen = p < 0 ? 0u : ((uint32_t)p >> g.c.log_block) + 1;
+    const uint32_t K = g.top_k;
+    int32_t *out = g.blocks + ((uint64_t)(sv.q0 + (int32_t)local) * g.c.heads + h) * K;
+    if (seen <= K) {
+        for (uint32_t i = tid; i < K; i += kThreads) out[i] = i < seen ? (int32_t)i : -1;
+        return;
+    }
+    // blocks f0 .. f1 - 1 compete; those before and behind are taken anyway
+    const uint32_t f0 = g.keep_first, f1 = seen - g.keep_last, n = f1 - f0;
+    uint32_t want = K - g.keep_first - g.keep_last;      // of the n > want that compete
+    const uint64_t *src = g.keys + ((uint64_t)row * g.c.heads + h) * g.nb + f0;
+    const bool in_lds = n <= kHeld;
+    uint64_t least = ~0ull, most = 0;
+    for (uint32_t i = tid; i < n; i += kThreads) {
+        const uint64_t x = src[i];
+        if (in_lds) held[i] = x;
+        least = x < least ? x : least;
+        most = x > most ? x : most;
+    }
+    for (int w = 32; w >= 1; w >>= 1) {
+        const uint64_t a = __shfl_xor(least, w, 64), b = __shfl_xor(most, w, 64);
+        least = a < least ? a : least;
+        most = b > most ? b : most;
+    }
+    if (lane == 0) {
+        wide[0][wave] = least;
+        wide[1][wave] = most;
+    }
+    __syncthreads();
+    for (int w = 0; w < 4; ++w) {
+        least = wide[0][w] < least ? wide[0][w] : least;
+        most = wide[1][w] > most ? wide[1][w] : most;
+    }
+    auto key = [&](uint32_t i) { return in_lds ? held[i] : src[i]; };
+
+    // keys at or above `cut` in the bits of `mask` are taken, but of those equal to it in
+    // these bits only the first `want`
+    const uint64_t diff = least ^ most;
+    int top = diff ? 64 - __builtin_clzll(diff) : 0;     // bits that are not alike in all keys
+    uint64_t mask = top == 64 ? 0ull : ~0ull << top, cut = most & mask;
+    uint32_t same = n;                                   // keys equal to `cut` in the bits of `mask`
+    if (want == 0) {                                     // only the forced blocks
+        cut = ~0ull;
+        mask = ~0ull;
+        same = 0;
+        top = 0;
+    }
+    while (top > 0 && same != want) {
+        const int bits = top < 8 ? top : 8, sh = top - bits;
+        hist[tid] = 0;
+        __syncthreads();
+        for (uint32_t i = tid; i < n; i += kThreads) {
+            const uint64_t x = key(i);
+            if ((x & mask) == cut) atomicAdd(&hist[(uint32_t)(x >> sh) & ((1u << bits) - 1u)], 1u);
+        }
+        __syncthreads();
+        if (wave == 0) {
+            // lane l has digits 255 - 4 l downwards: the digit at which the count from above reaches `want`
+            uint32_t c[4], mine = 0, total;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                c[i] = hist[255u - 4u * lane - i];
+                mine += c[i];
+            }
+            uint32_t above = wave_excl_scan(mine, total);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                if (above < want && above + c[i] >= want) {
+                    pick[0] = 255u - 4u * lane - i;
+                    pick[1] = above;
+                    pick[2] = c[i];
+                }
+                above += c[i];
+            }
+        }
+        __syncthreads();
+        cut |= (uint64_t)pick[0] << sh;
+        mask |= (uint64_t)((1u << bits) - 1u) << sh;
+        want -= pick[1];
+        same = pick[2];
+        top = sh;
+        __syncthreads();
+    }
+
+    // every thread takes a run of neighbouring blocks, so that ranks come out of one scan
+    const uint32_t run = div_up(n, kThreads), i0 = tid * run < n ? tid * run : n, i1 = i0 + run < n ? i0 + run : n;
+    uint32_t over = 0, equal = 0;
+    for (uint32_t i = i0; i < i1; ++i) {
+        const uint64_t x = key(i) & mask;
+        over += x > cut;
+        equal += x == cut;
+    }
+    uint32_t ta, tb;
+    uint32_t ra = wave_excl_scan(over, ta), rb = wave_excl_scan(equal, tb);
+    if (lane == 0) {
+        sums[0][wave] = ta;
+        sums[1][wave] = tb;
+    }
+    __syncthreads();
+    for (uint32_t w = 0; w < wave; ++w) {
+        ra += sums[0][w];
+        rb += sums[1][w];
+    }
+    uint32_t at = g.keep_first + ra + (rb < want ? rb : want);
+    for (uint32_t i = i0; i < i1; ++i) {
+        const uint64_t x = key(i) & mask;
+        bool take = x > cut;
+        if (x == cut) take = rb++ < want;
+        if (take) out[at++] = (int32_t)(f0 + i);
+    }
+    for (uint32_t i = tid; i < g.keep_first; i += kThreads) out[i] = (int32_t)i;
+    for (uint32_t i = tid; i < g.keep_last; i += kThreads) out[K - g.keep_last + i] = (int32_t)(f1 + i);
+}
+
+// Tokens that share a read of the bounds: with one new token a sequence there is nothing to share.
+inline uint32_t sharing(const zx_paged_batch *b, uint32_t n) { return (b->max_q < n ? b->max_q : n) > 1 ? 4 : 1; }
+
+struct Slabs {
+    uint32_t tt, groups, slab, nb;
+    uint64_t bytes;
+};
+
+// The keys of all tokens at once, or of as many token groups as 256 MB hold.
+Slabs make_slabs(const zx_paged_cache *c, const zx_paged_batch *b, uint32_t n)
+{
+    Slabs s{};
+    const uint64_t room = (uint64_t)b->table_width * c->page_tokens, cap = b->max_kv < room ? b->max_kv : room;
+    s.nb = ceil_div(cap, c->block_tokens);
+    s.tt = sharing(b, n);
+    const uint32_t seqs = b->n_seqs < n ? b->n_seqs : n;
+    s.groups = s.tt == 1 ? n : n / s.tt + seqs < n ? n / s.tt + seqs : n;
+    const uint64_t each = (uint64_t)s.tt * c->kv_heads * s.nb * 8;
+    const uint64_t most = (256ull << 20) / (each ? each : 1);
+    s.slab = most < 1 ? 1 : most < s.groups ? (uint32_t)most : s.groups;
+    s.bytes = each * s.slab;
+    return s;
+}
+
+template <int TT>
+void launch(uint32_t D, const SelectArgs &g, uint32_t pieces, hipStream_t stream)
+{
+    const dim3 grid(g.slab * g.c.heads, pieces);
+    if (D == 64) hipLaunchKernelGGL((k_score<64, TT>), grid, dim3(kThreads), 0, stream, g);
+    else if (D == 128) hipLaunchKernelGGL((k_score<128, TT>), grid, dim3(kThreads), 0, stream, g);
+    else hipLaunchKernelGGL((k_score<256, TT>), grid, dim3(kThreads), 0, stream, g);
+    hipLaunchKernelGGL((k_top<TT>), dim3(g.slab * TT * g.c.heads), dim3(kThreads), 0, stream, g);
+}
+
+}  // namespace
+}  // namespace zxp
+
+extern "C" size_t zx_paged_select_workspace_bytes(const zx_paged_cache *cache, const zx_paged_batch *batch, uint32_t n_tokens)
+{
+    using namespace zxp;
+    SelectArgs g{};
+    if (make_cache(cache, g.c) != ZX_OK || make_batch(batch, cache, n_tokens, nullptr, g.b) != ZX_OK || !cache->block_tokens || n_tokens == 0 ||
+        batch->n_seqs == 0)
+        return 0;
+    return (size_t)make_slabs(cache, batch, n_tokens).bytes;
+}
+
+extern "C" zx_status zx_paged_select(const zx_paged_cache *cache, const zx_paged_batch *batch, uint32_t n_tokens, const zx_rows *q,
+                                     uint32_t q_heads, uint32_t top_k, uint32_t keep_first, uint32_t keep_last, int32_t *blocks,
+                                     void *workspace, size_t ws_bytes, uint32_t *err, hipStream_t stream)
+{
+    using namespace zxp;
+    SelectArgs g{};
+    zx_status st = make_cache(cache, g.c);
+    if (st == ZX_OK) st = make_batch(batch, cache, n_tokens, err, g.b);
+    if (st != ZX_OK) return st;
+    if (!cache->block_tokens || q_heads == 0 || q_heads % cache->kv_heads || q_heads > 65536 || top_k == 0 || top_k > 1024 ||
+        (uint64_t)keep_first + keep_last > top_k || !blocks)
+        return ZX_E_INVAL;
+    if (n_tokens == 0 || batch->n_seqs == 0) return ZX_OK;
+    if ((st = make_rows(q, g.q)) != ZX_OK) return st;
+    const Slabs s = make_slabs(cache, batch, n_tokens);
+    if (s.bytes && (!workspace || ws_bytes < s.bytes || !al16(workspace))) return ZX_E_INVAL;
+    if ((uint64_t)s.slab * s.tt * cache->kv_heads > 0x7FFFFFFFull || s.nb > (1u << 26)) return ZX_E_LIMIT;
+    g.blocks = blocks;
+    g.keys = static_cast<uint64_t *>(workspace);
+    g.group = q_heads / cache->kv_heads;
+    g.top_k = top_k;
+    g.keep_first = keep_first;
+    g.keep_last = keep_last;
+    g.nb = s.nb;
+    g.slab = s.slab;
+    // blocks of a workgroup: few enough to fill the card, many enough to be worth its start
+    const uint32_t at_once = kThreads / (cache->head_dim / 8);
+    const uint64_t want = ceil_div(2048, (uint64_t)s.slab * cache->kv_heads);
+    uint32_t per = ceil_div(s.nb ? s.nb : 1, want);
+    per = ceil_div(per, at_once) * at_once;
+    if (ceil_div(s.nb ? s.nb : 1, per) > 65535) per = ceil_div(ceil_div(s.nb, 65535), at_once) * at_once;
+    g.per = per;
+    const uint32_t pieces = ceil_div(s.nb ? s.nb : 1, per);
+    for (uint32_t at = 0; at < s.groups; at += s.slab) {
+        g.slab0 = at;
+        if (s.groups - at < g.slab) g.slab = s.groups - at;
+        if (s.tt == 1) launch<1>(cache->head_dim, g, pieces, stream);
+        else launch<4>(cache->head_dim, g, pieces, stream);
+    }
+    return hipGetLastError() == hipSuccess ? ZX_OK : ZX_E_HIP;
+}

@@ -82,7 +82,9 @@ EXPORTS = ("zx_histogram", "zx_build_codebook", "zx_encode_size", "zx_encode", "
            "zx_status_string", "zx_version", "zx_kv_slot_sizes", "zx_kv_workspace_bytes", "zx_kv_encode_slots",
            "zx_kv_slot_container", "zx_kv_decode_slots", "zx_zf_scan_workspace_bytes", "zx_zf_encode_size",
            "zx_zf_encode", "zx_zf_decode", "zx_histogram_accumulate", "zx_build_codebook_u64",
-           "zx_kv_encode_slots_noalloc", "zx_encode_plan", "zx_kv_encode_slots_fused", "zx_encode_coded")
+           "zx_kv_encode_slots_noalloc", "zx_encode_plan", "zx_kv_encode_slots_fused", "zx_encode_coded",
+           "zx_paged_append", "zx_paged_attend", "zx_paged_attend_workspace_bytes", "zx_paged_select",
+           "zx_paged_select_workspace_bytes")
 
 
 def lib():
