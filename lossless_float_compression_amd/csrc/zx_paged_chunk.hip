@@ -78,7 +78,8 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void k_chunk(AttendArgs g
     const int32_t *table = g.b.table + (uint64_t)seq * g.b.width;
     const uint32_t pmask = (1u << g.c.log_page) - 1u;
     // pages of a tile's four 16-token pieces: 0xFFFFFFFF where there is none
-    auto pages = [&](uint32_t tile, uint32_t (&id)[4]) {
+    auto pages = [&](uint32_t tile) {
+        u4 id;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const uint32_t t = tile * kTile + 16 * i;
@@ -91,9 +92,10 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void k_chunk(AttendArgs g
                 }
             }
         }
+        return id;
     };
     u4 kr[NL], vr[NL];
-    auto load = [&](uint32_t tile, const uint32_t (&id)[4]) {
+    auto load = [&](uint32_t tile, u4 id) {
 #pragma unroll
         for (int i = 0; i < NL; ++i) {
             const uint32_t w = i * NT + wave * 64;          // first piece of the wave: its rows lie in one 16-token piece
@@ -119,7 +121,7 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void k_chunk(AttendArgs g
             reinterpret_cast<u4 *>(dst)[1] = u4{fp8_pair<false>(x[2]), fp8_pair<true>(x[2]), fp8_pair<false>(x[3]), fp8_pair<true>(x[3])};
         }
     };
-    auto store = [&](uint32_t tile, uint32_t buf, const uint32_t (&id)[4]) {
+    auto store = [&](uint32_t tile, uint32_t buf, u4 id) {
         const int32_t a = (int32_t)(tile * kTile);
         const bool gone = id[0] == 0xFFFFFFFFu || id[1] == 0xFFFFFFFFu || id[2] == 0xFFFFFFFFu || id[3] == 0xFFFFFFFFu;
         const bool edge = gone || a < lo_min || a + kTile > hi_max;      // some token that no row sees
@@ -161,11 +163,11 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void k_chunk(AttendArgs g
 
     if (threadIdx.x < 2) flag[threadIdx.x] = 0;
     __syncthreads();
-    uint32_t here[4], next[4];
+    u4 here = {0, 0, 0, 0}, next = here;
     if (t0 < t1) {
-        pages(t0, here);
+        here = pages(t0);
         load(t0, here);
-        pages(t0 + 1, next);
+        next = pages(t0 + 1);
         store(t0, 0, here);
     }
     for (uint32_t tile = t0; tile < t1; ++tile) {
@@ -173,6 +175,22 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void k_chunk(AttendArgs g
         const bool more = tile + 1 < t1;
         __syncthreads();
         if (more) load(tile + 1, next);
+        __builtin_amdgcn_sched_barrier(0);
+        // An infinity or NaN in the values of a tile that only some rows see in full: zero
+        // times it would reach the others.  It is taken out of the tile, kept in the other half
+        // (free until this tile is done), and added afterwards to the rows that see it.
+        const bool odd = flag[buf] == tile + 1;
+        if (odd) {
+            for (uint32_t i = threadIdx.x; i < kTile * D / 8; i += NT) {
+                const uint32_t at8 = (i / (D / 8)) * VS + (i % (D / 8)) * 16;
+                u4 x = *reinterpret_cast<const u4 *>(vl[buf] + at8);
+                *reinterpret_cast<u4 *>(vl[buf ^ 1u] + at8) = x;
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = tame_pair(x[j]);
+                *reinterpret_cast<u4 *>(vl[buf] + at8) = x;
+            }
+            __syncthreads();
+        }
         const int32_t a = (int32_t)(tile * kTile);
         if (live && a < whi_max && a + kTile > wlo_min) {
             f16v s[2];
@@ -186,6 +204,7 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void k_chunk(AttendArgs g
                     s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, *reinterpret_cast<const u4 *>(kp + 32 * j)),
                                                                    __builtin_bit_cast(bf8, q[j]), s[t], 0, 0, 0);
             }
+            __builtin_amdgcn_sched_barrier(0);
             // register i of tile t: token 32 t + 8 (i / 4) + 4 lh + i % 4
             const bool gone = here[0] == 0xFFFFFFFFu || here[1] == 0xFFFFFFFFu || here[2] == 0xFFFFFFFFu || here[3] == 0xFFFFFFFFu;
             const bool mixed = gone || a < wlo_max || a + kTile > whi_min;
@@ -229,9 +248,10 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void k_chunk(AttendArgs g
 #pragma unroll
                 for (int i = 0; i < 4; ++i) p[k][i] = pack2(s[k / 2][8 * (k % 2) + 2 * i], s[k / 2][8 * (k % 2) + 2 * i + 1]);
 
-            const bool odd = mixed && flag[buf] == tile + 1;
-            const uint8_t *vp = vl[buf] + (4 * lh + (lane & 15u) / 4) * VS + ((lane >> 4) & 1u) * 32 + (lane & 3u) * 8;
-            auto value = [&](int k, int d) {
+            __builtin_amdgcn_sched_barrier(0);
+            typedef __attribute__((address_space(3))) const uint8_t *lds_ptr;
+            const lds_ptr vp = (lds_ptr)vl[buf] + (4 * lh + (lane & 15u) / 4) * VS + ((lane >> 4) & 1u) * 32 + (lane & 3u) * 8;
+            auto value = [](lds_ptr vp, int k, int d) {
                 typedef short s4 __attribute__((ext_vector_type(4)));
                 typedef __attribute__((address_space(3))) s4 *lp;
                 const s4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(vp + (16 * k) * VS + 64 * d));
@@ -239,47 +259,36 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void k_chunk(AttendArgs g
                 const u2 xu = __builtin_bit_cast(u2, x), yu = __builtin_bit_cast(u2, y);
                 return u4{xu[0], xu[1], yu[0], yu[1]};
             };
-            if (!odd) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k)
-#pragma unroll
-                    for (int d = 0; d < ND; ++d)
-                        o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, value(k, d)), __builtin_bit_cast(bf8, p[k]), o[d], 0, 0, 0);
-            } else {
-                // an infinity or NaN that some rows see and some do not: the finite values as
-                // above, and each infinity for the rows that see it
+            for (int k = 0; k < 4; ++k)
 #pragma unroll
                 for (int d = 0; d < ND; ++d)
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, value(vp, k, d)), __builtin_bit_cast(bf8, p[k]), o[d], 0, 0, 0);
+            if (odd) {
+                // the infinities and NaN that were taken out, for the rows that see them
+#pragma unroll 1
+                for (int t = 0; t < kTile; ++t) {
+                    const bool see = a + t >= lo && a + t < hi;
+                    const uint8_t *vo = vl[buf ^ 1u] + t * VS + 8 * lh;
 #pragma unroll
-                    for (int sign = 0; sign < 2; ++sign) {
-                        f16v n;
+                    for (int d = 0; d < ND; ++d)
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) n[i] = 0.0f;
+                        for (int i = 0; i < 4; ++i) {
+                            const u2 w = *reinterpret_cast<const u2 *>(vo + 64 * d + 16 * i);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            u4 v = value(k, d), see, wild;
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const int32_t tk = a + 16 * k + 8 * (i / 2) + 4 * (int32_t)lh + 2 * (i % 2);
-                                const bool there = here[k] != 0xFFFFFFFFu;
-                                see[i] = (there && tk >= lo && tk < hi ? 0x3F80u : 0u) | (there && tk + 1 >= lo && tk + 1 < hi ? 0x3F800000u : 0u);
-                                wild[i] = sign ? wild_pair<1>(v[i]) : wild_pair<0>(v[i]);
-                                v[i] = tame_pair(v[i]);
+                            for (int j = 0; j < 4; ++j) {
+                                const float x = __builtin_bit_cast(float, j % 2 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+                                o[d][4 * i + j] += see && !(__builtin_fabsf(x) < kInf) ? x : 0.0f;
                             }
-                            n = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, wild), __builtin_bit_cast(bf8, see), n, 0, 0, 0);
-                            if (sign == 0) o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, v), __builtin_bit_cast(bf8, p[k]), o[d], 0, 0, 0);
                         }
-#pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            if (n[i] > 0.0f) o[d][i] += sign ? -kInf : kInf;
-                    }
+                }
             }
         }
+        if (odd) __syncthreads();
         if (more) {
             store(tile + 1, buf ^ 1u, next);
-#pragma unroll
-            for (int i = 0; i < 4; ++i) here[i] = next[i];
-            pages(tile + 2, next);
+            here = next;
+            next = pages(tile + 2);
         }
     }
 
