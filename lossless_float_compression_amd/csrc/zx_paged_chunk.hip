@@ -19,7 +19,7 @@ namespace {
 constexpr int kTile = 64;
 
 template <int DT, int D, int NW>
-__global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void k_chunk(AttendArgs g)
+__global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_chunk(AttendArgs g)
 {
     constexpr int ROWS = 32 * NW, NT = 64 * NW;
     constexpr int ES = DT == ZX_BF16 ? 2 : 1;
@@ -77,21 +77,32 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void k_chunk(AttendArgs g
 
     const int32_t *table = g.b.table + (uint64_t)seq * g.b.width;
     const uint32_t pmask = (1u << g.c.log_page) - 1u;
-    // pages of a tile's four 16-token pieces: 0xFFFFFFFF where there is none
+    // Pages of the tiles' 16-token pieces, 0xFFFFFFFF where there is none: lane i has the
+    // piece i of the 16 tiles from `base` on (and, read ahead, of the 16 behind them), so a
+    // tile's pages are a lane read and not a trip to memory.
+    auto look = [&](uint32_t tile) {
+        const uint32_t t = tile * kTile + 16 * lane;
+        uint32_t id = 0xFFFFFFFFu;
+        if (t < (uint32_t)sv.kv) id = (uint32_t)table[t >> g.c.log_page];
+        return id;
+    };
+    auto vet = [&](uint32_t id, uint32_t tile) {
+        if (id >= g.c.n_pages) {
+            if (tile * kTile + 16 * lane < (uint32_t)sv.kv) report(g.b.err, ZX_E_CORRUPT);
+            id = 0xFFFFFFFFu;
+        }
+        return id;
+    };
+    uint32_t base = t0, ids = vet(look(t0), t0), ahead = look(t0 + 16);
     auto pages = [&](uint32_t tile) {
+        if (tile - base >= 16) {
+            base += 16;
+            ids = vet(ahead, base);
+            ahead = look(base + 16);
+        }
         u4 id;
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t t = tile * kTile + 16 * i;
-            id[i] = 0xFFFFFFFFu;
-            if (t < (uint32_t)sv.kv) {
-                id[i] = (uint32_t)table[t >> g.c.log_page];
-                if (id[i] >= g.c.n_pages) {
-                    report(g.b.err, ZX_E_CORRUPT);
-                    id[i] = 0xFFFFFFFFu;
-                }
-            }
-        }
+        for (int i = 0; i < 4; ++i) id[i] = (uint32_t)__builtin_amdgcn_readlane((int)ids, (int)(4 * (tile - base)) + i);
         return id;
     };
     u4 kr[NL], vr[NL];
