@@ -3,14 +3,20 @@
 //
 // A workgroup takes 32 rows a wave (rows: the group's query heads for each new token)
 // and goes over its tokens in tiles of 64.  K and V tiles are read from their pages into
-// registers while the tile before is worked on, written to the other half of LDS as BF16,
-// and shared by all waves: one barrier a tile.  With 32x32x16 products a lane has one query row;
-// K is the left operand as it lies, V is read transposed (ds_read_b64_tr_b16), four
-// tokens of 16 channels for 16 lanes at a time, in the order of tokens that the scores
-// come out in, so weights go from one product to the next without leaving their lane.
-// LDS rows are padded so that the 16 lanes of a read meet all 64 banks: keys by 16 bytes
-// (a row of 16-byte pieces moves four banks on), values by 64 bytes (four rows of 32
-// bytes, 16 banks apart).
+// registers two steps ahead, written to LDS as BF16 one step ahead, and shared by all waves.  With 32x32x16 products a lane has one query row; K is the left operand as it lies, V is
+// read transposed (ds_read_b64_tr_b16), four tokens of 16 channels for 16 lanes at a
+// time, in the order of tokens that the scores come out in, so weights go from one
+// product to the next without leaving their lane.  LDS rows are padded so that the 16
+// lanes of a read meet all 64 banks: keys by 16 bytes (a row of 16-byte pieces moves four
+// banks on), values by 64 bytes (four rows of 32 bytes, 16 banks apart).
+//
+// A step of a wave is a matrix phase (the second product of tile i, the first of tile i + 1)
+// and a vector phase (the softmax of tile i + 1), about 1000 cycles each.  Two waves share a
+// SIMD; in step with each other they would both want the matrix unit and then both the
+// vector unit, so the second half of the workgroup's waves runs one phase behind the
+// first, held there by a barrier after every phase.
+#include <type_traits>
+
 #include "zx_paged_attend.h"
 
 namespace zxp {
@@ -18,8 +24,12 @@ namespace {
 
 constexpr int kTile = 64;
 
+// global memory by name: an address put together from integers would else be read as one of any kind
+typedef __attribute__((address_space(1))) u4 global_u4;
+typedef __attribute__((address_space(1))) uint8_t global_u1;
+
 template <int DT, int D, int NW>
-__global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_chunk(AttendArgs g)
+__global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void k_chunk(AttendArgs g)
 {
     constexpr int ROWS = 32 * NW, NT = 64 * NW;
     constexpr int ES = DT == ZX_BF16 ? 2 : 1;
@@ -29,7 +39,7 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_chunk(AttendArgs 
     constexpr int NS = D / 16, ND = D / 32;
     __shared__ __align__(16) uint8_t kl[2][kTile * KS];
     __shared__ __align__(16) uint8_t vl[2][kTile * VS];
-    __shared__ uint32_t flag[2];                           // tile + 1 whose values hold an infinity or NaN
+    __shared__ uint32_t any_odd;                           // whether store_v left infinities or NaN out
 
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -52,12 +62,12 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_chunk(AttendArgs 
     const int32_t lo_min = first_seen(g, pa), lo_max = first_seen(g, pb), hi_min = end_seen(g, pa, sv.kv), hi_max = end_seen(g, pb, sv.kv);
 
     // this wave's rows (one lane's row past the last repeats it)
-    const uint32_t w0 = row0 + wave * 32;
-    const bool live = w0 < row9;
-    const uint32_t w9 = w0 + 32 < row9 ? w0 + 32 : row9;
-    const uint32_t row = live ? (w0 + lr < w9 ? w0 + lr : w9 - 1) : row9 - 1;
-    const int32_t wa = pos0 + (int32_t)((live ? w0 : row9 - 1) / G), wb = pos0 + (int32_t)((live ? w9 - 1 : row9 - 1) / G);
-    const int32_t wlo_min = first_seen(g, wa), wlo_max = first_seen(g, wb), whi_min = end_seen(g, wa, sv.kv), whi_max = end_seen(g, wb, sv.kv);
+    const uint32_t wr = row0 + wave * 32;
+    const bool live = wr < row9;
+    const uint32_t w9 = wr + 32 < row9 ? wr + 32 : row9;
+    const uint32_t row = live ? (wr + lr < w9 ? wr + lr : w9 - 1) : row9 - 1;
+    const int32_t wa = pos0 + (int32_t)((live ? wr : row9 - 1) / G), wb = pos0 + (int32_t)((live ? w9 - 1 : row9 - 1) / G);
+    const int32_t wlo_max = first_seen(g, wb), whi_min = end_seen(g, wa, sv.kv);
     const int32_t mypos = pos0 + (int32_t)(row / G), lo = first_seen(g, mypos), hi = end_seen(g, mypos, sv.kv);
     const int64_t at = sv.q0 + (int32_t)(row / G);
     const uint32_t qh = h * G + row % G;
@@ -77,233 +87,322 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_chunk(AttendArgs 
 
     const int32_t *table = g.b.table + (uint64_t)seq * g.b.width;
     const uint32_t pmask = (1u << g.c.log_page) - 1u;
-    // Pages of the tiles' 16-token pieces, 0xFFFFFFFF where there is none: lane i has the
-    // piece i of the 16 tiles from `base` on (and, read ahead, of the 16 behind them), so a
-    // tile's pages are a lane read and not a trip to memory.
+    const uint8_t *const kmem = g.c.k + (int64_t)h * g.c.k_head, *const vmem = g.c.v + (int64_t)h * g.c.v_head;
+    // Where the tiles' 16-token pieces lie: lane i has the addresses of piece i of the 16
+    // tiles from `base` on (page 0, and a bit in `gone`, where there is no page), and the page
+    // ids of the 16 tiles behind them are read ahead.  A tile's addresses are then lane
+    // reads, not a trip to memory and 64-bit products.
+    uint64_t kat, vat, gone;
+    uint32_t base = t0, ahead;
     auto look = [&](uint32_t tile) {
         const uint32_t t = tile * kTile + 16 * lane;
-        uint32_t id = 0xFFFFFFFFu;
-        if (t < (uint32_t)sv.kv) id = (uint32_t)table[t >> g.c.log_page];
-        return id;
+        return t < (uint32_t)sv.kv ? (uint32_t)table[t >> g.c.log_page] : 0xFFFFFFFFu;
     };
-    auto vet = [&](uint32_t id, uint32_t tile) {
-        if (id >= g.c.n_pages) {
-            if (tile * kTile + 16 * lane < (uint32_t)sv.kv) report(g.b.err, ZX_E_CORRUPT);
-            id = 0xFFFFFFFFu;
-        }
-        return id;
+    auto settle = [&](uint32_t id) {
+        const uint32_t t = base * kTile + 16 * lane;
+        const bool none = id >= g.c.n_pages;
+        if (none && t < (uint32_t)sv.kv) report(g.b.err, ZX_E_CORRUPT);
+        if (none) id = 0;
+        kat = (uint64_t)kmem + (uint64_t)((int64_t)id * g.c.k_page) + (uint64_t)(t & pmask) * g.c.k_token;
+        vat = (uint64_t)vmem + (uint64_t)((int64_t)id * g.c.v_page) + (uint64_t)(t & pmask) * g.c.v_token;
+        gone = __ballot(none);
+        ahead = look(base + 16);
     };
-    uint32_t base = t0, ids = vet(look(t0), t0), ahead = look(t0 + 16);
-    auto pages = [&](uint32_t tile) {
+    settle(look(t0));
+    // A thread's NL pieces of a tile lie in rows whose 16-token piece is the same for the whole wave.
+    struct Spot {
+        uint64_t at[NL];
+    };
+    struct Where {
+        Spot k, v;
+        uint32_t gone;               // pieces of the tile that have no page: four bits
+    };
+    auto lane64 = [](uint64_t x, uint32_t l) {
+        return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, (int)l) |
+               (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(x >> 32), (int)l) << 32;
+    };
+    auto where = [&](uint32_t tile) {
         if (tile - base >= 16) {
             base += 16;
-            ids = vet(ahead, base);
-            ahead = look(base + 16);
+            settle(ahead);
         }
-        u4 id;
+        Where r;
+        const uint32_t l = 4 * (tile - base);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) id[i] = (uint32_t)__builtin_amdgcn_readlane((int)ids, (int)(4 * (tile - base)) + i);
-        return id;
+        for (int i = 0; i < NL; ++i) {
+            uint32_t sub = (i * NT + wave * 64) / CPR / 16;
+            if (kTile * CPR % NT) sub &= 3u;            // waves that have no piece
+            r.k.at[i] = lane64(kat, l + sub);
+            r.v.at[i] = lane64(vat, l + sub);
+        }
+        r.gone = (uint32_t)(gone >> l) & 15u;
+        return r;
     };
     u4 kr[NL], vr[NL];
-    auto load = [&](uint32_t tile, u4 id) {
-#pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const uint32_t w = i * NT + wave * 64;          // first piece of the wave: its rows lie in one 16-token piece
-            if (kTile * CPR % NT && w >= (uint32_t)(kTile * CPR)) continue;
-            const uint32_t sub = w / CPR / 16;
-            uint32_t p = id[0];
-#pragma unroll
-            for (int j = 1; j < 4; ++j) p = sub == (uint32_t)j ? id[j] : p;
-            if (p == 0xFFFFFFFFu) p = 0;                    // any page: its tokens are not used
-            const uint32_t tok = (tile * kTile + 16 * sub) & pmask;
-            const uint32_t r = (w + lane) / CPR - 16 * sub, ch = ((w + lane) % CPR) * 16;
-            const uint8_t *kb = g.c.k + (int64_t)p * g.c.k_page + (int64_t)h * g.c.k_head + (uint64_t)tok * g.c.k_token;
-            const uint8_t *vb = g.c.v + (int64_t)p * g.c.v_page + (int64_t)h * g.c.v_head + (uint64_t)tok * g.c.v_token;
-            kr[i] = *reinterpret_cast<const u4 *>(kb + (r * g.c.k_token + ch));
-            vr[i] = *reinterpret_cast<const u4 *>(vb + (r * g.c.v_token + ch));
-        }
+    // piece i of this thread's part of a tile, keys or values, into a register
+    auto load = [&](u4 &r, const Spot &at, uint32_t token_stride, int i) {
+        const uint32_t w = i * NT + wave * 64;
+        if (kTile * CPR % NT && w >= (uint32_t)(kTile * CPR)) return;
+        const uint32_t row = (threadIdx.x + i * NT) / CPR % 16u, ch = (threadIdx.x + i * NT) % CPR * 16u;
+        r = *(const global_u4 *)((const global_u1 *)at.at[i] + (row * token_stride + ch));
     };
-    auto put = [](uint8_t *dst, u4 x) {                     // 16 bytes of the cache as BF16
+    auto load_k = [&](const Where &at, int i) { load(kr[i], at.k, g.c.k_token, i); };
+    auto load_v = [&](const Where &at, int i) { load(vr[i], at.v, g.c.v_token, i); };
+    // 16 bytes of the cache as BF16
+    auto widen = [](u4 x, u4 (&y)[2 / ES == 1 ? 1 : 2]) {
         if constexpr (DT == ZX_BF16) {
-            *reinterpret_cast<u4 *>(dst) = x;
+            y[0] = x;
         } else {
-            reinterpret_cast<u4 *>(dst)[0] = u4{fp8_pair<false>(x[0]), fp8_pair<true>(x[0]), fp8_pair<false>(x[1]), fp8_pair<true>(x[1])};
-            reinterpret_cast<u4 *>(dst)[1] = u4{fp8_pair<false>(x[2]), fp8_pair<true>(x[2]), fp8_pair<false>(x[3]), fp8_pair<true>(x[3])};
+            y[0] = u4{fp8_pair<false>(x[0]), fp8_pair<true>(x[0]), fp8_pair<false>(x[1]), fp8_pair<true>(x[1])};
+            y[1] = u4{fp8_pair<false>(x[2]), fp8_pair<true>(x[2]), fp8_pair<false>(x[3]), fp8_pair<true>(x[3])};
         }
     };
-    auto store = [&](uint32_t tile, uint32_t buf, u4 id) {
+    constexpr int NY = ES == 2 ? 1 : 2;
+    auto store_k = [&](uint32_t tile, int i) {
+        const uint32_t w = i * NT + wave * 64;
+        if (kTile * CPR % NT && w >= (uint32_t)(kTile * CPR)) return;
+        u4 y[NY];
+        widen(kr[i], y);
+        uint8_t *dst = kl[tile & 1u] + (w + lane) / CPR * KS + ((w + lane) % CPR) * (32 / ES);
+#pragma unroll
+        for (int j = 0; j < NY; ++j) reinterpret_cast<u4 *>(dst)[j] = y[j];
+    };
+    auto store_v = [&](uint32_t tile, uint32_t gone, int i) {
+        const uint32_t w = i * NT + wave * 64;
+        if (kTile * CPR % NT && w >= (uint32_t)(kTile * CPR)) return;
         const int32_t a = (int32_t)(tile * kTile);
-        const bool gone = id[0] == 0xFFFFFFFFu || id[1] == 0xFFFFFFFFu || id[2] == 0xFFFFFFFFu || id[3] == 0xFFFFFFFFu;
-        const bool edge = gone || a < lo_min || a + kTile > hi_max;      // some token that no row sees
-        const bool mixed = a < lo_max || a + kTile > hi_min;             // some token that some rows do not see
+        const bool edge = gone != 0 || a < lo_min || a + kTile > hi_max;      // some token that no row sees
+        const bool mixed = a < lo_max || a + kTile > hi_min;                  // some token that some rows do not see
+        u4 y[NY];
+        widen(vr[i], y);
+        if (edge) {
+            const int32_t t = a + (int32_t)((w + lane) / CPR);
+            const bool none = (gone >> (w / CPR / 16) & 1u) || t < lo_min || t >= hi_max;
 #pragma unroll
-        for (int i = 0; i < NL; ++i) {
-            const uint32_t w = i * NT + wave * 64;
-            if (kTile * CPR % NT && w >= (uint32_t)(kTile * CPR)) continue;
-            const uint32_t r = (w + lane) / CPR, ch = ((w + lane) % CPR) * (32 / ES);
-            if (edge) {
-                const uint32_t sub = w / CPR / 16;
-                uint32_t p = id[0];
-#pragma unroll
-                for (int j = 1; j < 4; ++j) p = sub == (uint32_t)j ? id[j] : p;
-                const int32_t t = a + (int32_t)r;
-                if (p == 0xFFFFFFFFu || t < lo_min || t >= hi_max) vr[i] = u4{0, 0, 0, 0};
-            }
-            put(kl[buf] + r * KS + ch, kr[i]);
-            put(vl[buf] + r * VS + ch, vr[i]);
-            if (mixed) {
-                bool odd = false;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    if constexpr (DT == ZX_BF16) odd = odd || odd_pair(vr[i][j]);
-                    else odd = odd || odd_pair(fp8_pair<false>(vr[i][j])) || odd_pair(fp8_pair<true>(vr[i][j]));
-                }
-                if (odd) flag[buf] = tile + 1;
-            }
+            for (int j = 0; j < NY; ++j) y[j] = none ? u4{0, 0, 0, 0} : y[j];
         }
+        if (mixed) {
+            // An infinity or NaN that only some rows see: zero times it would reach the
+            // others.  It is left out here and added at the end to the rows that see it.
+            bool odd = false;
+#pragma unroll
+            for (int j = 0; j < NY; ++j)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    odd = odd || odd_pair(y[j][e]);
+                    y[j][e] = tame_pair(y[j][e]);
+                }
+            if (odd) any_odd = 1;
+        }
+        uint8_t *dst = vl[tile & 1u] + (w + lane) / CPR * VS + ((w + lane) % CPR) * (32 / ES);
+#pragma unroll
+        for (int j = 0; j < NY; ++j) reinterpret_cast<u4 *>(dst)[j] = y[j];
     };
 
     float m = -kInf, l = 0.0f;
-    f16v o[ND];
+    f16v o[ND], s[2];
+    u4 p[4];
 #pragma unroll
     for (int d = 0; d < ND; ++d)
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
     const float c = g.scale * (g.c.k_scale ? g.c.k_scale[h] : 1.0f);
 
-    if (threadIdx.x < 2) flag[threadIdx.x] = 0;
-    __syncthreads();
-    u4 here = {0, 0, 0, 0}, next = here;
-    if (t0 < t1) {
-        here = pages(t0);
-        load(t0, here);
-        next = pages(t0 + 1);
-        store(t0, 0, here);
-    }
-    for (uint32_t tile = t0; tile < t1; ++tile) {
-        const uint32_t buf = (tile - t0) & 1u;
-        const bool more = tile + 1 < t1;
-        __syncthreads();
-        if (more) load(tile + 1, next);
-        __builtin_amdgcn_sched_barrier(0);
-        // An infinity or NaN in the values of a tile that only some rows see in full: zero
-        // times it would reach the others.  It is taken out of the tile, kept in the other half
-        // (free until this tile is done), and added afterwards to the rows that see it.
-        const bool odd = flag[buf] == tile + 1;
-        if (odd) {
-            for (uint32_t i = threadIdx.x; i < kTile * D / 8; i += NT) {
-                const uint32_t at8 = (i / (D / 8)) * VS + (i % (D / 8)) * 16;
-                u4 x = *reinterpret_cast<const u4 *>(vl[buf] + at8);
-                *reinterpret_cast<u4 *>(vl[buf ^ 1u] + at8) = x;
+    typedef __attribute__((address_space(3))) const uint8_t *lds_ptr;
+    const lds_ptr kp = (lds_ptr)&kl[0][0] + lr * KS + 16 * lh;
+    const lds_ptr vp = (lds_ptr)&vl[0][0] + (4 * lh + (lane & 15u) / 4) * VS + ((lane >> 4) & 1u) * 32 + (lane & 3u) * 8;
+    auto key = [](lds_ptr kp, int t, int j) { return *(__attribute__((address_space(3))) const u4 *)(kp + 32 * t * KS + 32 * j); };
+    auto value = [](lds_ptr vp, int k, int d) {
+        typedef short s4 __attribute__((ext_vector_type(4)));
+        typedef __attribute__((address_space(3))) s4 *lp;
+        const s4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(vp + (16 * k) * VS + 64 * d));
+        const s4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(vp + (16 * k + 8) * VS + 64 * d));
+        const u2 xu = __builtin_bit_cast(u2, x), yu = __builtin_bit_cast(u2, y);
+        return u4{xu[0], xu[1], yu[0], yu[1]};
+    };
+    // The products of a matrix phase: the second one of a tile (FIRST: none), then the first one
+    // of the tile behind it, whose register i of s[t] is token 32 t + 8 (i / 4) + 4 lh + i % 4.
+    // Reads and products stand in the order they are to run in, held there by scheduling
+    // barriers: values are read ND products ahead, keys kAhead products ahead.
+    constexpr int kAhead = D == 256 ? 4 : 8;
+    // `between(n)` is called after product n of the first one, to run beside the products.
+    auto products = [&](uint32_t tile, auto first, auto between) {
+        const lds_ptr vq = vp + (tile & 1u) * (kTile * VS), kq = kp + ((tile + 1) & 1u) * (kTile * KS);
+        u4 kf[kAhead];
+        auto next_key = [&](int n) { kf[n % kAhead] = key(kq, n % 2, n / 2); };
+        if constexpr (decltype(first)::value) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) x[j] = tame_pair(x[j]);
-                *reinterpret_cast<u4 *>(vl[buf] + at8) = x;
-            }
-            __syncthreads();
-        }
-        const int32_t a = (int32_t)(tile * kTile);
-        if (live && a < whi_max && a + kTile > wlo_min) {
-            f16v s[2];
+            for (int n = 0; n < kAhead; ++n) next_key(n);
+        } else {
+            u4 vf[2][ND];
 #pragma unroll
-            for (int t = 0; t < 2; ++t) {
-#pragma unroll
-                for (int i = 0; i < 16; ++i) s[t][i] = 0.0f;
-                const uint8_t *kp = kl[buf] + (32 * t + lr) * KS + 16 * lh;
-#pragma unroll
-                for (int j = 0; j < NS; ++j)
-                    s[t] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, *reinterpret_cast<const u4 *>(kp + 32 * j)),
-                                                                   __builtin_bit_cast(bf8, q[j]), s[t], 0, 0, 0);
-            }
+            for (int d = 0; d < ND; ++d) vf[0][d] = value(vq, 0, d);
             __builtin_amdgcn_sched_barrier(0);
-            // register i of tile t: token 32 t + 8 (i / 4) + 4 lh + i % 4
-            const bool gone = here[0] == 0xFFFFFFFFu || here[1] == 0xFFFFFFFFu || here[2] == 0xFFFFFFFFu || here[3] == 0xFFFFFFFFu;
-            const bool mixed = gone || a < wlo_max || a + kTile > whi_min;
-            float mx = -kInf;
-            if (mixed) {
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int d = 0; d < ND; ++d) {
+                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, vf[k % 2][d]), __builtin_bit_cast(bf8, p[k]), o[d], 0, 0, 0);
+                    if (k < 3) {
+                        vf[(k + 1) % 2][d] = value(vq, k + 1, d);
+                    } else {
+#pragma unroll
+                        for (int n = d * kAhead / ND; n < (d + 1) * kAhead / ND; ++n) next_key(n);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+        }
+        f16v zero;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) zero[i] = 0.0f;
+#pragma unroll
+        for (int n = 0; n < 2 * NS; ++n) {
+            s[n % 2] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, kf[n % kAhead]), __builtin_bit_cast(bf8, q[n / 2]),
+                                                               n < 2 ? zero : s[n % 2], 0, 0, 0);
+            if (n + kAhead < 2 * NS) next_key(n + kAhead);
+            between(n);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    };
+    // The weights of a tile whose scores are in s, and what they change in m, l and o.
+    auto soften = [&](uint32_t tile, uint32_t gone) {
+        const int32_t a = (int32_t)(tile * kTile);
+        if (gone || a < wlo_max || a + kTile > whi_min) {
+            // in terms of the tokens' constants, so that only two values are kept
+            const int32_t rl = lo - a - 4 * (int32_t)lh, rn = hi - lo;
+#pragma unroll
+            for (int t = 0; t < 2; ++t)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    s[t][i] = (uint32_t)(32 * t + 8 * (i / 4) + i % 4 - rl) < (uint32_t)rn ? s[t][i] : -kInf;
+            if (gone) {
 #pragma unroll
                 for (int t = 0; t < 2; ++t)
 #pragma unroll
-                    for (int i = 0; i < 16; ++i) {
-                        const int32_t tk = a + 32 * t + 8 * (i / 4) + 4 * (int32_t)lh + i % 4;
-                        const bool in = tk >= lo && tk < hi && here[2 * t + i / 8] != 0xFFFFFFFFu;
-                        s[t][i] = in ? s[t][i] : -kInf;
-                    }
-            }
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[t][i]);
-            mx = max_halves(mx) * c;
-            if (__any(mx > m + kSlack)) {
-                const float nm = fmaxf(m, mx), base = nm == -kInf ? 0.0f : nm;
-                const float f = __builtin_amdgcn_exp2f(m - base);
-                m = nm;
-                l *= f;
-#pragma unroll
-                for (int d = 0; d < ND; ++d)
-#pragma unroll
-                    for (int i = 0; i < 16; ++i) o[d][i] *= f;
-            }
-            const float base = m == -kInf ? 0.0f : m;
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-#pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    s[t][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], c, -base));
-                    l += s[t][i];
-                }
-            u4 p[4];
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int i = 0; i < 4; ++i) p[k][i] = pack2(s[k / 2][8 * (k % 2) + 2 * i], s[k / 2][8 * (k % 2) + 2 * i + 1]);
-
-            __builtin_amdgcn_sched_barrier(0);
-            typedef __attribute__((address_space(3))) const uint8_t *lds_ptr;
-            const lds_ptr vp = (lds_ptr)vl[buf] + (4 * lh + (lane & 15u) / 4) * VS + ((lane >> 4) & 1u) * 32 + (lane & 3u) * 8;
-            auto value = [](lds_ptr vp, int k, int d) {
-                typedef short s4 __attribute__((ext_vector_type(4)));
-                typedef __attribute__((address_space(3))) s4 *lp;
-                const s4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(vp + (16 * k) * VS + 64 * d));
-                const s4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lp)(vp + (16 * k + 8) * VS + 64 * d));
-                const u2 xu = __builtin_bit_cast(u2, x), yu = __builtin_bit_cast(u2, y);
-                return u4{xu[0], xu[1], yu[0], yu[1]};
-            };
-#pragma unroll
-            for (int k = 0; k < 4; ++k)
-#pragma unroll
-                for (int d = 0; d < ND; ++d)
-                    o[d] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf8, value(vp, k, d)), __builtin_bit_cast(bf8, p[k]), o[d], 0, 0, 0);
-            if (odd) {
-                // the infinities and NaN that were taken out, for the rows that see them
-#pragma unroll 1
-                for (int t = 0; t < kTile; ++t) {
-                    const bool see = a + t >= lo && a + t < hi;
-                    const uint8_t *vo = vl[buf ^ 1u] + t * VS + 8 * lh;
-#pragma unroll
-                    for (int d = 0; d < ND; ++d)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const u2 w = *reinterpret_cast<const u2 *>(vo + 64 * d + 16 * i);
-#pragma unroll
-                            for (int j = 0; j < 4; ++j) {
-                                const float x = __builtin_bit_cast(float, j % 2 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
-                                o[d][4 * i + j] += see && !(__builtin_fabsf(x) < kInf) ? x : 0.0f;
-                            }
-                        }
-                }
+                    for (int i = 0; i < 16; ++i) s[t][i] = gone >> (2 * t + i / 8) & 1u ? -kInf : s[t][i];
             }
         }
-        if (odd) __syncthreads();
-        if (more) {
-            store(tile + 1, buf ^ 1u, next);
-            here = next;
-            next = pages(tile + 2);
+        float mx = -kInf;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) mx = fmaxf(mx, s[t][i]);
+        mx = max_halves(mx) * c;
+        if (__any(mx > m + kSlack)) {
+            const float nm = fmaxf(m, mx), base = nm == -kInf ? 0.0f : nm;
+            const float f = __builtin_amdgcn_exp2f(m - base);
+            m = nm;
+            l *= f;
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) o[d][i] *= f;
+        }
+        const float base = m == -kInf ? 0.0f : m;
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) {
+                s[t][i] = __builtin_amdgcn_exp2f(__builtin_fmaf(s[t][i], c, -base));
+                l += s[t][i];
+            }
+        asm volatile("" : "+v"(l));      // here, not behind the matrix phase: s is to be free by then
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+#pragma unroll
+            for (int i = 0; i < 4; ++i) p[k][i] = pack2(s[k / 2][8 * (k % 2) + 2 * i], s[k / 2][8 * (k % 2) + 2 * i + 1]);
+    };
+    if (threadIdx.x == 0) any_odd = 0;
+    if (t0 < t1) {
+        __syncthreads();
+        // w1, w2: tiles i + 1, i + 2 (their loads are under way); the pieces of tile i without a page
+        const Where w0 = where(t0);
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            load_k(w0, i);
+            load_v(w0, i);
+        }
+        Where w1 = where(t0 + 1), w2 = where(t0 + 2);
+        uint32_t gone0 = w0.gone;
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            store_k(t0, i);
+            store_v(t0, w0.gone, i);
+            load_k(w1, i);
+        }
+#pragma unroll
+        for (int i = 0; i < NL; ++i) {
+            store_k(t0 + 1, i);
+            load_v(w1, i);
+            load_k(w2, i);
+        }
+        __syncthreads();
+        const bool behind = NW == 8 && wave >= NW / 2;
+        if (behind) __syncthreads();
+        products(t0 - 1, std::true_type{}, [](int) {});
+        __syncthreads();
+        for (uint32_t tile = t0; tile < t1; ++tile) {
+            __builtin_amdgcn_sched_barrier(0);
+            soften(tile, gone0);
+            __builtin_amdgcn_sched_barrier(0);
+            __syncthreads();
+            // Every wave works on every tile: one that its rows do not see has weights of zero.
+            // Behind the last tile, the scores are of whatever LDS holds and are not used.
+            __builtin_amdgcn_s_setprio(1);
+            // The tiles ahead, beside the products: what was read a step ago goes to LDS, where tile
+            // i - 1's values and tile i's keys were last read before the barrier above; then the
+            // next pieces are read.
+            products(tile, std::false_type{}, [&](int n) {
+                if (n < NL) {
+                    store_v(tile + 1, w1.gone, n);
+                    store_k(tile + 2, n);
+                }
+                if (n == NL) {
+                    gone0 = w1.gone;
+                    w1 = w2;
+                    w2 = where(tile + 3);
+                }
+                if (n > NL && n <= 2 * NL) {
+                    load_v(w1, n - NL - 1);
+                    load_k(w2, n - NL - 1);
+                }
+            });
+            __builtin_amdgcn_s_setprio(0);
+            __syncthreads();
+        }
+        if (NW == 8 && !behind) __syncthreads();
+        if (any_odd) {
+            // the infinities and NaN that store_v left out, for the rows that see them
+#pragma unroll 1
+            for (int32_t tk = (int32_t)(t0 * kTile); tk < (int32_t)(t1 * kTile); ++tk) {
+                const int32_t a = tk & ~(kTile - 1);
+                if (!(a < lo_max || a + kTile > hi_min) || tk < lo_min || tk >= hi_max) continue;
+                const uint32_t page = (uint32_t)table[tk >> g.c.log_page];
+                if (page >= g.c.n_pages) continue;
+                const bool see = tk >= lo && tk < hi;
+                const uint8_t *row = vmem + (int64_t)page * g.c.v_page + (uint64_t)((uint32_t)tk & pmask) * g.c.v_token + 4 * lh * ES;
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        u2 w;
+                        if constexpr (DT == ZX_BF16) {
+                            w = *reinterpret_cast<const u2 *>(row + 64 * d + 16 * i);
+                        } else {
+                            const uint32_t b = *reinterpret_cast<const uint32_t *>(row + 32 * d + 8 * i);
+                            w = u2{fp8_pair<false>(b), fp8_pair<true>(b)};
+                        }
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float x = __builtin_bit_cast(float, j % 2 ? w[j / 2] & 0xFFFF0000u : w[j / 2] << 16);
+                            o[d][4 * i + j] += see && !(__builtin_fabsf(x) < kInf) ? x : 0.0f;
+                        }
+                    }
+            }
         }
     }
 
-    if (!live || w0 + lr >= w9) return;
+    if (!live || wr + lr >= w9) return;
     l = sum_halves(l);
     if (g.target == 1) {
         const float inv = l == 0.0f ? 0.0f : (g.c.v_scale ? g.c.v_scale[h] : 1.0f) / l;
