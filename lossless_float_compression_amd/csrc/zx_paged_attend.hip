@@ -24,16 +24,25 @@ namespace {
 
 // ---------------------------------------------------------------- few rows
 
-// The 16-token pieces a workgroup reads: consecutive ones of the sequence, or those of
-// the listed blocks.
-struct Place {
-    int32_t token;       // first token of the piece
-    uint32_t page;       // its page: 0 where there is none
-    bool there;
-};
+// An infinity or NaN in a dword of values becomes zero; whether there was one.
+template <int DT>
+__device__ __forceinline__ bool tame(uint32_t &w)
+{
+    if constexpr (DT == ZX_BF16) {
+        const bool odd = odd_pair(w);
+        w = tame_pair(w);
+        return odd;
+    } else {                                     // E4M3 has no infinity; NaN is 0x7F in the low seven bits
+        const uint32_t m = ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+        w &= ~((m >> 7) * 0xFFu);
+        return m != 0;
+    }
+}
+
+constexpr int rows_waves(int d, int mt) { return d == 256 ? 1 : mt == 3 ? 2 : mt == 2 ? (d == 64 ? 3 : 2) : d == 64 ? 4 : 3; }
 
 template <int DT, int D, int MT, bool LIST>
-__global__ __launch_bounds__(kRowsThreads) void k_rows(AttendArgs g)
+__global__ __launch_bounds__(kRowsThreads, rows_waves(D, MT)) void k_rows(AttendArgs g)
 {
     constexpr int ROWS = 16 * MT;
     constexpr int ES = DT == ZX_BF16 ? 2 : 1;
@@ -53,25 +62,20 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(AttendArgs g)
     const uint32_t G = g.group;
 
     // which rows, which tokens
-    uint32_t seq, local, before, nch, chunk = 1, rt;
+    uint32_t seq, rt, part, nch, chunk = 1, piece_slot;
     Seq sv;
     if constexpr (LIST) {
         const uint32_t tiles = div_up(G, ROWS);
-        nch = g.target;
-        if (!find_item(g.b, item, [&](const Seq &v) { return (uint32_t)v.nq * tiles * nch; }, [](const Seq &) { return 0u; }, seq, sv,
-                       local, before))
-            return;
+        uint32_t local, unused;
+        nch = g.pieces;
+        if (!find_item(g.b, item, [&](const Seq &v) { return (uint32_t)v.nq * tiles * nch; }, [](const Seq &) { return 0u; }, seq, sv, local, unused)) return;
+        rt = local / nch;
+        part = local % nch;
+        piece_slot = item;
     } else {
-        chunk = chunk_steps<ROWS>(g);
-        if (!find_item(
-                g.b, item,
-                [&](const Seq &v) { return takes(g, v) ? div_up((uint32_t)v.nq * G, ROWS) * div_up(seq_steps(g, v), chunk) : 0u; },
-                [](const Seq &) { return 0u; }, seq, sv, local, before))
-            return;
-        nch = div_up(seq_steps(g, sv), chunk);
+        chunk = chunk_steps<ROWS, (int)kStep>(g);
+        if (!find_piece<ROWS, (int)kStep>(g, item, chunk, seq, sv, rt, part, nch, piece_slot)) return;
     }
-    rt = local / nch;
-    const uint32_t part = local % nch;
     uint32_t row0, nrows, tok0;                      // rows row0 .. of the token list starting at tok0
     if constexpr (LIST) {
         const uint32_t tiles = div_up(G, ROWS);
@@ -145,73 +149,73 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(AttendArgs g)
         if (u1 > (uint32_t)((hi_max + 15) >> 4)) u1 = (uint32_t)((hi_max + 15) >> 4);
     }
 
-    auto place = [&](uint32_t u) {
-        Place p;
-        p.there = u < u1;
-        uint32_t t = 0;
-        if (p.there) {
-            if constexpr (LIST) {
-                const uint32_t e = (uint32_t)list[u >> (lb - 4)];
-                t = e << lb;
-                p.there = e <= (uint32_t)sv.kv >> lb;       // entries past the sequence see nothing
-                t += (u & ((1u << (lb - 4)) - 1u)) << 4;
-                p.there = p.there && t < (uint32_t)sv.kv;
-            } else {
-                t = u << 4;
-            }
+    // Where the wave's pieces lie: lane 2 i + a has piece a of the wave's step i, 32 steps at a
+    // time, as addresses (page 0, and no bit in `held`, where there is no page).  A step's
+    // addresses are then lane reads, not trips to memory and 64-bit products.
+    const uint32_t pmask = (1u << g.c.log_page) - 1u;
+    uint64_t kat, vat, held;
+    int32_t first_token;
+    auto settle = [&](uint32_t u) {
+        u += 8 * (lane >> 1) + (lane & 1u);
+        bool there = u < u1;
+        uint32_t t = u << 4;
+        if constexpr (LIST) {
+            const uint32_t e = there ? (uint32_t)list[u >> (lb - 4)] : 0u;
+            there = there && e <= (uint32_t)sv.kv >> lb;        // entries past the sequence see nothing
+            t = (e << lb) + ((u & ((1u << (lb - 4)) - 1u)) << 4);
+            there = there && t < (uint32_t)sv.kv;
         }
         uint32_t page = 0;
-        if (p.there) {
+        if (there) {
             page = (uint32_t)table[t >> g.c.log_page];
             if (page >= g.c.n_pages) {
                 report(g.b.err, ZX_E_CORRUPT);
                 page = 0;
-                p.there = false;
+                there = false;
             }
         }
-        p.token = (int32_t)t;
-        p.page = page;
-        return p;
+        const uint64_t at = t & pmask;
+        kat = (uint64_t)g.c.k + (uint64_t)((int64_t)page * g.c.k_page + (int64_t)h * g.c.k_head) + at * g.c.k_token;
+        vat = (uint64_t)g.c.v + (uint64_t)((int64_t)page * g.c.v_page + (int64_t)h * g.c.v_head) + at * g.c.v_token;
+        first_token = (int32_t)t;
+        held = __ballot(there);
     };
-    const uint32_t pmask = (1u << g.c.log_page) - 1u;
+    auto lane64 = [](uint64_t x, uint32_t l) {
+        return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)x, (int)l) |
+               (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)(x >> 32), (int)l) << 32;
+    };
     const uint32_t koff = lr * g.c.k_token + lq * 16u;
     const uint32_t voff = lq * 4u * g.c.v_token + lr * (VW * ES);
-    auto kbase = [&](const Place &p) {
-        return g.c.k + (int64_t)p.page * g.c.k_page + (int64_t)h * g.c.k_head + (uint64_t)((uint32_t)p.token & pmask) * g.c.k_token;
-    };
-    auto vbase = [&](const Place &p) {
-        return g.c.v + (int64_t)p.page * g.c.v_page + (int64_t)h * g.c.v_head + (uint64_t)((uint32_t)p.token & pmask) * g.c.v_token;
-    };
 
     u4 kreg[2][KL];
     uint32_t vreg[8][NP][VD];
-    auto load_k = [&](const Place (&p)[2]) {
+    auto load_k = [&](uint32_t i) {              // step i of the 32
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
-            const uint8_t *b = kbase(p[a]);
+            const global_u1 *b = (const global_u1 *)lane64(kat, 2 * i + a) + koff;
 #pragma unroll
-            for (int i = 0; i < KL; ++i) kreg[a][i] = *reinterpret_cast<const u4 *>(b + koff + 64u * i);
+            for (int e = 0; e < KL; ++e) kreg[a][e] = *(const global_u4 *)(b + 64 * e);
         }
     };
-    auto load_v = [&](const Place (&p)[2]) {
+    auto load_v = [&](uint32_t i) {
 #pragma unroll
         for (int a = 0; a < 2; ++a) {
-            const uint8_t *b = vbase(p[a]);
+            const global_u1 *b = (const global_u1 *)lane64(vat, 2 * i + a);
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
+            for (int e = 0; e < 4; ++e)
 #pragma unroll
                 for (int n = 0; n < NP; ++n) {
-                    const uint8_t *s = b + voff + (uint32_t)i * g.c.v_token + n * (16 * VW * ES);
+                    const global_u1 *s = b + (voff + (uint32_t)e * g.c.v_token) + n * (16 * VW * ES);
                     if constexpr (VD == 4) {
-                        const u4 x = *reinterpret_cast<const u4 *>(s);
+                        const u4 x = *(const global_u4 *)s;
 #pragma unroll
-                        for (int w = 0; w < 4; ++w) vreg[4 * a + i][n][w] = x[w];
+                        for (int w = 0; w < 4; ++w) vreg[4 * a + e][n][w] = x[w];
                     } else if constexpr (VD == 2) {
-                        const u2 x = *reinterpret_cast<const u2 *>(s);
-                        vreg[4 * a + i][n][0] = x[0];
-                        vreg[4 * a + i][n][1] = x[1];
+                        const u2 x = *(const global_u2 *)s;
+                        vreg[4 * a + e][n][0] = x[0];
+                        vreg[4 * a + e][n][1] = x[1];
                     } else {
-                        vreg[4 * a + i][n][0] = *reinterpret_cast<const uint32_t *>(s);
+                        vreg[4 * a + e][n][0] = *(const global_u32 *)s;
                     }
                 }
         }
@@ -230,17 +234,16 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(AttendArgs g)
     }
     const float c = g.scale * (g.c.k_scale ? g.c.k_scale[h] : 1.0f);
 
-    uint32_t u = u0 + 2 * wave;
-    Place here[2], next[2];
+    uint32_t u = u0 + 2 * wave, step = 0;
+    bool any_odd = false;                        // values with infinities or NaN were left out
     if (u < u1) {
-        here[0] = place(u);
-        here[1] = place(u + 1);
-        load_k(here);
-        load_v(here);
-        next[0] = place(u + 8);
-        next[1] = place(u + 9);
+        settle(u);
+        load_k(0);
+        load_v(0);
     }
     for (; u < u1; u += 8) {
+        const int32_t token[2] = {__builtin_amdgcn_readlane(first_token, (int)(2 * step)), __builtin_amdgcn_readlane(first_token, (int)(2 * step + 1))};
+        const bool there[2] = {(held >> (2 * step) & 1u) != 0, (held >> (2 * step + 1) & 1u) != 0};
         // scores: 16 tokens x 16 rows a tile; a lane has row lr, tokens 4 lq .. 4 lq + 3 of each piece
         f4 s[MT][2];
 #pragma unroll
@@ -262,13 +265,17 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(AttendArgs g)
             }
         }
         const bool more = u + 8 < u1;
-        if (more) load_k(next);
+        if (more) {
+            step = (step + 1) & 31u;
+            if (step == 0) settle(u + 8);
+            load_k(step);
+        }
 
         // does any row not see any of these tokens?
         bool part_seen = false;
 #pragma unroll
         for (int a = 0; a < 2; ++a)
-            part_seen = part_seen || !here[a].there || here[a].token < lo_max || here[a].token + 16 > hi_min;
+            part_seen = part_seen || !there[a] || token[a] < lo_max || token[a] + 16 > hi_min;
 #pragma unroll
         for (int t = 0; t < MT; ++t) {
             float mx = -kInf;
@@ -278,8 +285,8 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(AttendArgs g)
                 for (int i = 0; i < 4; ++i) {
                     float x = s[t][a][i] * c;
                     if (part_seen) {
-                        const int32_t tk = here[a].token + 4 * (int32_t)lq + i;
-                        x = here[a].there && tk >= lo[t] && tk < hi[t] ? x : -kInf;
+                        const int32_t tk = token[a] + 4 * (int32_t)lq + i;
+                        x = there[a] && tk >= lo[t] && tk < hi[t] ? x : -kInf;
                     }
                     s[t][a][i] = x;
                     mx = fmaxf(mx, x);
@@ -311,21 +318,29 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(AttendArgs g)
             p[t] = u4{pack2(s[t][0][0], s[t][0][1]), pack2(s[t][0][2], s[t][0][3]), pack2(s[t][1][0], s[t][1][1]), pack2(s[t][1][2], s[t][1][3])};
 
         // values that no row sees are not there (pages hold anything behind a sequence's end)
-        bool odd = false;
         if (part_seen) {
 #pragma unroll
             for (int a = 0; a < 2; ++a)
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const int32_t tk = here[a].token + 4 * (int32_t)lq + i;
-                    const bool seen = here[a].there && tk >= lo_min && tk < hi_max;
+                    const int32_t tk = token[a] + 4 * (int32_t)lq + i;
+                    const bool seen = there[a] && tk >= lo_min && tk < hi_max;
 #pragma unroll
                     for (int n = 0; n < NP; ++n)
 #pragma unroll
                         for (int w = 0; w < VD; ++w) vreg[4 * a + i][n][w] = seen ? vreg[4 * a + i][n][w] : 0u;
                 }
+            if (lo_min != lo_max || hi_min != hi_max) {
+                // An infinity or NaN that only some rows see: zero times it would reach the
+                // others.  It is left out here and added at the end to the rows that see it.
+#pragma unroll
+                for (int i = 0; i < 8; ++i)
+#pragma unroll
+                    for (int n = 0; n < NP; ++n)
+#pragma unroll
+                        for (int w = 0; w < VD; ++w) any_odd = tame<DT>(vreg[i][n][w]) || any_odd;
+            }
         }
-        const bool differ = part_seen && (lo_min != lo_max || hi_min != hi_max);
 #pragma unroll
         for (int n = 0; n < NP; ++n) {
 #pragma unroll
@@ -344,49 +359,6 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(AttendArgs g)
                     v0[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x05040100u);
                     v1[i] = __builtin_amdgcn_perm(x[2 * i + 1], x[2 * i], 0x07060302u);
                 }
-                if (differ) {
-                    // rows see different tokens here: an infinity or NaN may belong to some rows only
-                    bool any = false;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) any = any || odd_pair(v0[i]) || odd_pair(v1[i]);
-                    odd = __any(any);
-                    if (odd) {
-#pragma unroll
-                        for (int t = 0; t < MT; ++t) {
-                            u4 see;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const int a = k / 2, i = 2 * (k % 2);
-                                const int32_t tk = here[a].token + 4 * (int32_t)lq + i;
-                                see[k] = (here[a].there && tk >= lo[t] && tk < hi[t] ? 0x3F80u : 0u) |
-                                         (here[a].there && tk + 1 >= lo[t] && tk + 1 < hi[t] ? 0x3F800000u : 0u);
-                            }
-#pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const u4 v = e ? v1 : v0;
-                                u4 wp, wn;
-#pragma unroll
-                                for (int k = 0; k < 4; ++k) {
-                                    wp[k] = wild_pair<0>(v[k]);
-                                    wn[k] = wild_pair<1>(v[k]);
-                                }
-                                const f4 z = {0, 0, 0, 0};
-                                const f4 np = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, wp), __builtin_bit_cast(bf8, see), z, 0, 0, 0);
-                                const f4 nn = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, wn), __builtin_bit_cast(bf8, see), z, 0, 0, 0);
-#pragma unroll
-                                for (int i = 0; i < 4; ++i) {
-                                    if (np[i] > 0.0f) o[t][n][2 * w + e][i] += kInf;
-                                    if (nn[i] > 0.0f) o[t][n][2 * w + e][i] -= kInf;
-                                }
-                            }
-                        }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            v0[k] = tame_pair(v0[k]);
-                            v1[k] = tame_pair(v1[k]);
-                        }
-                    }
-                }
 #pragma unroll
                 for (int t = 0; t < MT; ++t) {
                     o[t][n][2 * w] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, v0), __builtin_bit_cast(bf8, p[t]), o[t][n][2 * w], 0, 0, 0);
@@ -394,18 +366,40 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(AttendArgs g)
                 }
             }
         }
-        if (more) {
-            load_v(next);
-            here[0] = next[0];
-            here[1] = next[1];
-            next[0] = place(u + 16);
-            next[1] = place(u + 17);
+        if (more) load_v(step);
+    }
+    if (__any(any_odd)) {
+        // the infinities and NaN that were left out, for the rows that see them
+#pragma unroll 1
+        for (u = u0 + 2 * wave, step = 0; u < u1; u += 8, step = (step + 1) & 31u) {
+            if (step == 0) settle(u);
+#pragma unroll 1
+            for (uint32_t e = 0; e < 32; ++e) {
+                const uint32_t at = 2 * step + (e >> 4);
+                const int32_t tk = __builtin_amdgcn_readlane(first_token, (int)at) + (int32_t)(e & 15u);
+                if (!(held >> at & 1u) || tk < lo_min || tk >= hi_max) continue;
+                const uint8_t *b = (const uint8_t *)lane64(vat, at) + (uint64_t)(e & 15u) * g.c.v_token;
+#pragma unroll
+                for (int n = 0; n < NP; ++n)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+#pragma unroll
+                        for (int j = 0; j < VW; ++j) {
+                            const uint32_t ch = n * 16 * VW + (4 * lq + i) * VW + j;
+                            float x;
+                            if constexpr (DT == ZX_BF16) x = (float)reinterpret_cast<const __bf16 *>(b)[ch];
+                            else x = __builtin_bit_cast(float, fp8_pair<false>(b[ch]) << 16);
+                            if (__builtin_fabsf(x) < kInf) x = 0.0f;
+#pragma unroll
+                            for (int t = 0; t < MT; ++t) o[t][n][j][i] += tk >= lo[t] && tk < hi[t] ? x : 0.0f;
+                        }
+            }
         }
     }
 
     // join the four waves, 16 rows at a time
     const float vs = g.c.v_scale ? g.c.v_scale[h] : 1.0f;
-    const uint64_t slot = ((uint64_t)item * g.c.heads + h) * ROWS;
+    const uint64_t slot = ((uint64_t)piece_slot * g.c.heads + h) * ROWS;
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
         if (t) __syncthreads();
@@ -467,117 +461,105 @@ __global__ __launch_bounds__(kRowsThreads) void k_rows(AttendArgs g)
 
 struct Plan {
     bool rows, chunk;                // which kernels run
-    uint32_t mt, rows_items, rows_target, rows_slots, rows_max;
-    uint32_t waves, chunk_items, chunk_split;
-    bool rows_join, chunk_join;
+    AttendArgs r, c;                 // their arguments: how sequences are split
+    uint32_t mt, rows_items, rows_join, rows_max;   // rows_join: row tiles that may be split (0: none)
+    ChunkPlan cp;
     uint64_t rows_part, rows_stat, chunk_part, chunk_stat, bytes;   // offsets into the workspace
 };
 
-constexpr uint32_t kFewRows = 32;    // rows of a sequence that k_rows takes
-constexpr uint32_t kRowsGroups = 768;
+constexpr uint32_t kFewRows = 64;    // rows of a sequence that k_rows takes
+// Workgroups of k_rows that the card holds at a time.
+constexpr uint32_t rows_groups(uint32_t d, uint32_t mt) { return 256u * (uint32_t)rows_waves((int)d, (int)mt); }
 
-inline uint32_t bound_tiles(uint64_t n, uint64_t seqs, uint64_t group, uint64_t rows)
-{
-    // sum over the sequences of ceil(nq * group / rows)
-    const uint64_t a = n * ceil_div(group, rows), b = n * group / rows + seqs;
-    return (uint32_t)(a < b ? a : b);
-}
-
-Plan make_plan(const zx_paged_cache *c, const zx_paged_batch *b, uint32_t n, uint32_t q_heads, uint32_t n_blocks)
+Plan make_plan(const zx_paged_cache *c, const zx_paged_batch *b, uint32_t n, uint32_t q_heads, uint32_t n_blocks, const AttendArgs &g)
 {
     Plan p{};
+    p.r = p.c = g;
     const uint32_t G = q_heads / c->kv_heads, H = c->kv_heads, D = c->head_dim;
     const uint64_t room = (uint64_t)b->table_width * c->page_tokens, cap = b->max_kv < room ? b->max_kv : room;
     const uint32_t max_q = b->max_q < n ? b->max_q : n;
     const uint32_t seqs = b->n_seqs < n ? b->n_seqs : n;      // sequences with new tokens
+    const uint64_t most = (uint64_t)max_q * G < 1 ? 1 : (uint64_t)max_q * G;
     auto area = [&](uint64_t bytes) {
         const uint64_t at = p.bytes;
         p.bytes += (bytes + 255) & ~255ull;
         return at;
     };
+    uint64_t rows_slots = 0;
     if (n_blocks) {
         p.rows = true;
         p.mt = 1;
-        p.rows_items = n * ceil_div(G, 16);
-        const uint32_t steps = ceil_div((uint64_t)n_blocks * c->block_tokens, kStep);
-        uint32_t s = ceil_div(kRowsGroups, (uint64_t)p.rows_items * H);
-        if (s > steps) s = steps;
-        p.rows_target = s ? s : 1;
-        p.rows_slots = p.rows_items * p.rows_target;
-        p.rows_join = p.rows_target > 1;
+        const uint32_t tiles = n * ceil_div(G, 16), steps = ceil_div((uint64_t)n_blocks * c->block_tokens, kStep);
+        uint32_t s = ceil_div(rows_groups(D, 1), (uint64_t)tiles * H);
+        p.r.pieces = s > steps ? steps : s;
+        p.rows_items = tiles * p.r.pieces;
         p.rows_max = G < 16 ? G : 16;
+        if (p.r.pieces > 1) {
+            p.rows_join = tiles;
+            rows_slots = p.rows_items;
+        }
     } else {
-        p.chunk = (uint64_t)max_q * G > kFewRows;
+        p.chunk = most > kFewRows;
         p.rows = !p.chunk || seqs > 1;       // a batch may mix single tokens with long chunks
         if (p.rows) {
-            p.mt = D <= 128 && (uint64_t)max_q * G > 16 ? 2 : 1;
-            const uint32_t R = 16 * p.mt, tiles = p.chunk ? seqs * (kFewRows / R) : bound_tiles(n, seqs, G, R);
-            p.rows_target = ceil_div(kRowsGroups, H);
-            p.rows_slots = p.rows_target + tiles;
-            p.rows_items = tiles;
-            p.rows_join = cap > kStep;
-            const uint64_t most = (uint64_t)max_q * G;
-            p.rows_max = most < 1 ? 1 : (uint32_t)(most < R ? most : R);
+            p.mt = D == 64 && most > 32 ? 3 : D <= 128 && most > 16 ? 2 : 1;
+            const uint32_t R = 16 * p.mt, tiles = p.chunk ? seqs * ceil_div(kFewRows, R) : bound_tiles(n, seqs, G, R);
+            plan_split(tiles, ceil_div(rows_groups(D, p.mt), H), 2, 1, 1, cap, kStep, p.r);
+            rows_slots = p.r.slots;
+            p.rows_items = split_items(tiles, p.r);
+            p.rows_join = split_tiles(tiles, p.r);
+            p.rows_max = (uint32_t)(most < R ? most : R);
         }
         if (p.chunk) {
-            p.waves = chunk_waves((uint64_t)max_q * G, D);
-            const uint32_t R = 32 * p.waves;
-            p.chunk_items = bound_tiles(n, seqs, G, R);
-            // split the tokens of a row tile where the row tiles alone leave most of the card idle
-            uint32_t s = 512 / (p.chunk_items * H ? p.chunk_items * H : 1);
-            const uint32_t most = (uint32_t)(cap / 512);
-            if (s > most) s = most;
-            p.chunk_split = s < 1 ? 1 : s > 64 ? 64 : s;
-            p.chunk_join = p.chunk_split > 1;
+            p.cp = plan_chunk(most, D, H, n, seqs, G, cap, p.c);
+            if (p.c.slots) {
+                const uint64_t r = (uint64_t)p.c.slots * H * 32 * p.cp.waves;
+                p.chunk_part = area(r * D * 4);
+                p.chunk_stat = area(r * 8);
+            }
         }
     }
-    if (p.rows_join) {
-        const uint64_t r = (uint64_t)p.rows_slots * H * 16 * p.mt;
+    if (rows_slots) {
+        const uint64_t r = rows_slots * H * 16 * p.mt;
         p.rows_part = area(r * D * 4);
         p.rows_stat = area(r * 8);
     }
-    if (p.chunk_join) {
-        const uint64_t r = (uint64_t)p.chunk_items * p.chunk_split * H * 32 * p.waves;
-        p.chunk_part = area(r * D * 4);
-        p.chunk_stat = area(r * 8);
-    }
+    p.r.lo_rows = 0;
+    p.r.hi_rows = p.chunk ? kFewRows : 0xFFFFFFFFu;
+    p.c.lo_rows = p.rows ? kFewRows : 0;
+    p.c.hi_rows = 0xFFFFFFFFu;
     return p;
 }
 
 template <int DT, int D>
-void run_plan(const Plan &p, AttendArgs g, uint32_t n_blocks, uint8_t *ws, hipStream_t stream)
+void run_plan(Plan &p, uint32_t n_blocks, uint8_t *ws, hipStream_t stream)
 {
-    const uint32_t H = g.c.heads;
     if (p.rows) {
-        AttendArgs a = g;
+        AttendArgs &a = p.r;
         a.part = reinterpret_cast<float *>(ws + p.rows_part);
         a.stat = reinterpret_cast<float *>(ws + p.rows_stat);
-        a.target = p.rows_target;
-        a.slots = p.rows_slots;
-        a.lo_rows = 0;
-        a.hi_rows = p.chunk ? kFewRows : 0xFFFFFFFFu;
-        const dim3 grid(p.rows_slots * H), block(kRowsThreads);
-        const dim3 jgrid(p.rows_items * H, 1, p.rows_max);
+        const dim3 grid(p.rows_items * a.c.heads), block(kRowsThreads), jgrid(p.rows_join * a.c.heads, 1, join_depth(p.rows_join * a.c.heads, p.rows_max));
         if (n_blocks) {
             hipLaunchKernelGGL((k_rows<DT, D, 1, true>), grid, block, 0, stream, a);
-            if (p.rows_join) hipLaunchKernelGGL((k_join<D, 16, JOIN_LIST>), jgrid, dim3(256), 0, stream, a);
+            if (p.rows_join) hipLaunchKernelGGL((k_join<D, 16, 0>), jgrid, dim3(256), 0, stream, a);
         } else if (p.mt == 1) {
             hipLaunchKernelGGL((k_rows<DT, D, 1, false>), grid, block, 0, stream, a);
-            if (p.rows_join) hipLaunchKernelGGL((k_join<D, 16, JOIN_ROWS>), jgrid, dim3(256), 0, stream, a);
-        } else if constexpr (D <= 128) {
-            hipLaunchKernelGGL((k_rows<DT, D, 2, false>), grid, block, 0, stream, a);
-            if (p.rows_join) hipLaunchKernelGGL((k_join<D, 32, JOIN_ROWS>), jgrid, dim3(256), 0, stream, a);
+            if (p.rows_join) hipLaunchKernelGGL((k_join<D, 16, (int)kStep>), jgrid, dim3(256), 0, stream, a);
+        } else if (p.mt == 2) {
+            if constexpr (D <= 128) {
+                hipLaunchKernelGGL((k_rows<DT, D, 2, false>), grid, block, 0, stream, a);
+                if (p.rows_join) hipLaunchKernelGGL((k_join<D, 32, (int)kStep>), jgrid, dim3(256), 0, stream, a);
+            }
+        } else if constexpr (D == 64) {
+            hipLaunchKernelGGL((k_rows<DT, D, 3, false>), grid, block, 0, stream, a);
+            if (p.rows_join) hipLaunchKernelGGL((k_join<D, 48, (int)kStep>), jgrid, dim3(256), 0, stream, a);
         }
     }
     if (p.chunk) {
-        AttendArgs a = g;
+        AttendArgs &a = p.c;
         a.part = reinterpret_cast<float *>(ws + p.chunk_part);
         a.stat = reinterpret_cast<float *>(ws + p.chunk_stat);
-        a.target = p.chunk_split;
-        a.slots = p.chunk_items * p.chunk_split;
-        a.lo_rows = p.rows ? kFewRows : 0;
-        a.hi_rows = 0xFFFFFFFFu;
-        run_chunk(DT, D, p.waves, p.chunk_items, p.chunk_split, a, stream);
+        run_chunk(DT, D, p.cp, a, stream);
     }
 }
 
@@ -605,7 +587,7 @@ extern "C" size_t zx_paged_attend_workspace_bytes(const zx_paged_cache *cache, c
 {
     zxp::AttendArgs g{};
     if (zxp::checks(cache, batch, n_tokens, q_heads, n_blocks, nullptr, g) != ZX_OK || n_tokens == 0 || batch->n_seqs == 0) return 0;
-    return (size_t)zxp::make_plan(cache, batch, n_tokens, q_heads, n_blocks).bytes;
+    return (size_t)zxp::make_plan(cache, batch, n_tokens, q_heads, n_blocks, g).bytes;
 }
 
 extern "C" zx_status zx_paged_attend(const zx_paged_cache *cache, const zx_paged_batch *batch, uint32_t n_tokens, const zx_rows *q,
@@ -621,8 +603,6 @@ extern "C" zx_status zx_paged_attend(const zx_paged_cache *cache, const zx_paged
     if (!(scale > 0.0f) || scale > 1e30f || window > 0x3FFFFFFFu || (blocks && (!causal || window))) return ZX_E_INVAL;
     if (n_tokens == 0 || batch->n_seqs == 0) return ZX_OK;
     if ((st = make_rows(q, g.q)) != ZX_OK || (st = make_rows(out, g.out)) != ZX_OK) return st;
-    const Plan p = make_plan(cache, batch, n_tokens, q_heads, n_blocks);
-    if (p.bytes && (!workspace || ws_bytes < p.bytes || !al16(workspace))) return ZX_E_INVAL;
     g.lse = lse;
     g.blocks = blocks;
     g.n_blocks = n_blocks;
@@ -631,16 +611,18 @@ extern "C" zx_status zx_paged_attend(const zx_paged_cache *cache, const zx_paged
     g.window = (int32_t)window;
     g.group = q_heads / cache->kv_heads;
     g.q_heads = q_heads;
+    Plan p = make_plan(cache, batch, n_tokens, q_heads, n_blocks, g);
+    if (p.bytes && (!workspace || ws_bytes < p.bytes || !al16(workspace))) return ZX_E_INVAL;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const uint32_t D = cache->head_dim;
     if (cache->dtype == ZX_BF16) {
-        if (D == 64) run_plan<ZX_BF16, 64>(p, g, n_blocks, ws, stream);
-        else if (D == 128) run_plan<ZX_BF16, 128>(p, g, n_blocks, ws, stream);
-        else run_plan<ZX_BF16, 256>(p, g, n_blocks, ws, stream);
+        if (D == 64) run_plan<ZX_BF16, 64>(p, n_blocks, ws, stream);
+        else if (D == 128) run_plan<ZX_BF16, 128>(p, n_blocks, ws, stream);
+        else run_plan<ZX_BF16, 256>(p, n_blocks, ws, stream);
     } else {
-        if (D == 64) run_plan<ZX_FP8_E4M3FN, 64>(p, g, n_blocks, ws, stream);
-        else if (D == 128) run_plan<ZX_FP8_E4M3FN, 128>(p, g, n_blocks, ws, stream);
-        else run_plan<ZX_FP8_E4M3FN, 256>(p, g, n_blocks, ws, stream);
+        if (D == 64) run_plan<ZX_FP8_E4M3FN, 64>(p, n_blocks, ws, stream);
+        else if (D == 128) run_plan<ZX_FP8_E4M3FN, 128>(p, n_blocks, ws, stream);
+        else run_plan<ZX_FP8_E4M3FN, 256>(p, n_blocks, ws, stream);
     }
     return hipGetLastError() == hipSuccess ? ZX_OK : ZX_E_HIP;
 }

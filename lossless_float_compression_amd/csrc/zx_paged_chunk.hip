@@ -24,10 +24,6 @@ namespace {
 
 constexpr int kTile = 64;
 
-// global memory by name: an address put together from integers would else be read as one of any kind
-typedef __attribute__((address_space(1))) u4 global_u4;
-typedef __attribute__((address_space(1))) uint8_t global_u1;
-
 template <int DT, int D, int NW>
 __global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void k_chunk(AttendArgs g)
 {
@@ -46,16 +42,11 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void k_chunk(AttendArgs g
     const uint32_t lr = lane & 31u, lh = lane >> 5;
     const uint32_t G = g.group;
     const uint32_t h = blockIdx.x % g.c.heads, rest = blockIdx.x / g.c.heads;
-    const uint32_t part = rest % g.target, item = rest / g.target;
-    uint32_t seq, local, unused;
+    uint32_t seq, rt, part, nch, slot;
     Seq sv;
-    if (!find_item(g.b, item, [&](const Seq &v) { return takes(g, v) ? div_up((uint32_t)v.nq * G, ROWS) : 0u; }, [](const Seq &) { return 0u; }, seq, sv,
-                   local, unused))
-        return;
-    // the last row tiles see the most tokens: they go first
-    const uint32_t all = (uint32_t)sv.nq * G, rt = div_up(all, ROWS) - 1 - local;
-    const uint64_t slot = (uint64_t)(item - local + rt) * g.target + part;
-    if (g.target > 1 && slot >= g.slots) return;       // overlapping sequences: more row tiles than there is room for
+    if (!find_piece<ROWS, kTile>(g, rest, chunk_steps<ROWS, kTile>(g), seq, sv, rt, part, nch, slot)) return;
+    const uint32_t all = (uint32_t)sv.nq * G;
+    if (nch == 1) rt = div_up(all, ROWS) - 1 - rt;         // the last row tiles see the most tokens: they go first
     const uint32_t row0 = rt * ROWS, row9 = row0 + ROWS < all ? row0 + ROWS : all;
     const int32_t pos0 = sv.kv - sv.nq;
     const int32_t pa = pos0 + (int32_t)(row0 / G), pb = pos0 + (int32_t)((row9 - 1) / G);
@@ -80,7 +71,7 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void k_chunk(AttendArgs g
 
     uint32_t t0 = (uint32_t)lo_min / kTile, t1 = div_up((uint32_t)hi_max, kTile);
     if (t1 < t0) t1 = t0;
-    const uint32_t per = div_up(t1 - t0, g.target);
+    const uint32_t per = div_up(t1 - t0, nch);
     t0 += part * per;
     if (t0 > t1) t0 = t1;
     if (t1 > t0 + per) t1 = t0 + per;
@@ -404,7 +395,7 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void k_chunk(AttendArgs g
 
     if (!live || wr + lr >= w9) return;
     l = sum_halves(l);
-    if (g.target == 1) {
+    if (nch == 1) {
         const float inv = l == 0.0f ? 0.0f : (g.c.v_scale ? g.c.v_scale[h] : 1.0f) / l;
         __bf16 *op = g.out.p + at * g.out.token + (int64_t)qh * g.out.head + 4 * lh;
 #pragma unroll
@@ -415,7 +406,7 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void k_chunk(AttendArgs g
                     u2{pack2(o[d][4 * i] * inv, o[d][4 * i + 1] * inv), pack2(o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv)};
         if (g.lse && lh == 0) g.lse[at * g.q_heads + qh] = l == 0.0f ? -kInf : (m + log2f(l)) * kLn2;
     } else {
-        const uint64_t r = (slot * g.c.heads + h) * ROWS + (row - row0);
+        const uint64_t r = ((uint64_t)slot * g.c.heads + h) * ROWS + (row - row0);
         float *dst = g.part + r * D + 4 * lh;
 #pragma unroll
         for (int d = 0; d < ND; ++d)
@@ -430,30 +421,40 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void k_chunk(AttendArgs g
 }
 
 template <int DT, int D, int NW>
-void launch(uint32_t items, uint32_t split, const AttendArgs &g, hipStream_t stream)
+void launch(const ChunkPlan &p, const AttendArgs &g, hipStream_t stream)
 {
-    hipLaunchKernelGGL((k_chunk<DT, D, NW>), dim3(items * split * g.c.heads), dim3(64 * NW), 0, stream, g);
-    if (split > 1) hipLaunchKernelGGL((k_join<D, 32 * NW, JOIN_CHUNK>), dim3(items * g.c.heads, 1, 16), dim3(256), 0, stream, g);
+    hipLaunchKernelGGL((k_chunk<DT, D, NW>), dim3(split_items(p.tiles, g) * g.c.heads), dim3(64 * NW), 0, stream, g);
+    if (const uint32_t t = split_tiles(p.tiles, g)) hipLaunchKernelGGL((k_join<D, 32 * NW, kTile>), dim3(t * g.c.heads, 1, join_depth(t * g.c.heads, 32 * NW)), dim3(256), 0, stream, g);
 }
 
 template <int DT>
-void by_size(uint32_t D, uint32_t waves, uint32_t items, uint32_t split, const AttendArgs &g, hipStream_t stream)
+void by_size(uint32_t D, const ChunkPlan &p, const AttendArgs &g, hipStream_t stream)
 {
-    if (D == 256) launch<DT, 256, 4>(items, split, g, stream);
-    else if (D == 128 && waves == 8) launch<DT, 128, 8>(items, split, g, stream);
-    else if (D == 128) launch<DT, 128, 4>(items, split, g, stream);
-    else if (waves == 8) launch<DT, 64, 8>(items, split, g, stream);
-    else launch<DT, 64, 4>(items, split, g, stream);
+    if (D == 256) launch<DT, 256, 4>(p, g, stream);
+    else if (D == 128 && p.waves == 8) launch<DT, 128, 8>(p, g, stream);
+    else if (D == 128) launch<DT, 128, 4>(p, g, stream);
+    else if (p.waves == 8) launch<DT, 64, 8>(p, g, stream);
+    else launch<DT, 64, 4>(p, g, stream);
 }
 
 }  // namespace
 
-uint32_t chunk_waves(uint64_t rows, uint32_t head_dim) { return head_dim == 256 || rows <= 128 ? 4 : 8; }
+constexpr uint32_t kChunkRounds = 3;
 
-void run_chunk(int dtype, uint32_t head_dim, uint32_t waves, uint32_t items, uint32_t split, const AttendArgs &g, hipStream_t stream)
+ChunkPlan plan_chunk(uint64_t rows, uint32_t head_dim, uint32_t heads, uint64_t tokens, uint64_t seqs, uint64_t group, uint64_t cap, AttendArgs &g)
 {
-    if (dtype == ZX_BF16) by_size<ZX_BF16>(head_dim, waves, items, split, g, stream);
-    else by_size<ZX_FP8_E4M3FN>(head_dim, waves, items, split, g, stream);
+    ChunkPlan p{};
+    p.waves = head_dim == 256 || rows <= 128 ? 4 : 8;
+    const uint32_t R = 32 * p.waves;
+    p.tiles = bound_tiles(tokens, seqs, group, R);
+    plan_split(p.tiles, ceil_div(256, heads), kChunkRounds, 8, 64, cap, kTile, g);
+    return p;
+}
+
+void run_chunk(int dtype, uint32_t head_dim, const ChunkPlan &p, const AttendArgs &g, hipStream_t stream)
+{
+    if (dtype == ZX_BF16) by_size<ZX_BF16>(head_dim, p, g, stream);
+    else by_size<ZX_FP8_E4M3FN>(head_dim, p, g, stream);
 }
 
 }  // namespace zxp

@@ -17,6 +17,7 @@ namespace zxp {
 namespace {
 
 constexpr uint32_t kThreads = 256;
+constexpr int kDigit = 10;              // bits of a radix digit of k_top
 constexpr uint32_t kHeld = 4096;        // keys of a row that k_top holds in LDS (32 KB)
 
 struct SelectArgs {
@@ -39,12 +40,37 @@ __device__ __forceinline__ uint64_t order_key(double x)
     return b < 0 ? ~(uint64_t)b : (uint64_t)b | 0x8000000000000000ull;
 }
 
-// Tokens of a sequence come in groups of TT that share what is read of the bounds.
+// x of the lane that DPP pattern CTRL names
+template <int CTRL>
+__device__ __forceinline__ double moved(double x)
+{
+    const uint64_t b = (uint64_t)__double_as_longlong(x);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)b, CTRL, 0xF, 0xF, true);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)(b >> 32), CTRL, 0xF, 0xF, true);
+    return __longlong_as_double((int64_t)((uint64_t)hi << 32 | lo));
+}
+
+// Sum over the LB neighbouring lanes of a block, in all of them: pairs, pairs of pairs
+// (quad_perm), halves of a row of 16 (half_mirror, row_mirror), rows.
+template <int LB>
+__device__ __forceinline__ double sum_lanes(double x)
+{
+    x += moved<0xB1>(x);                                 // quad_perm 1 0 3 2
+    x += moved<0x4E>(x);                                 // quad_perm 2 3 0 1
+    x += moved<0x141>(x);                                // row_half_mirror
+    if constexpr (LB >= 16) x += moved<0x140>(x);        // row_mirror
+    if constexpr (LB >= 32) x += __shfl_xor(x, 16, 64);
+    return x;
+}
+
+// Tokens of a sequence come in groups of TT that share what is read of the bounds.  A lane
+// has eight channels of a block's two bounds; kUnroll blocks are in flight for it at a time.
 template <int D, int TT>
 __global__ __launch_bounds__(kThreads) void k_score(SelectArgs g)
 {
     constexpr uint32_t LB = D / 8;                       // lanes of a block
     constexpr uint32_t PB = kThreads / LB;               // blocks at a time
+    constexpr int kUnroll = 4;
     const uint32_t h = blockIdx.x % g.c.heads, grp = blockIdx.x / g.c.heads;
     uint32_t seq, local, unused;
     Seq sv;
@@ -58,53 +84,84 @@ __global__ __launch_bounds__(kThreads) void k_score(SelectArgs g)
     if (j0 >= j1) return;
 
     const uint32_t ln = threadIdx.x % LB, slot = threadIdx.x / LB;
-    double up[TT][8], dn[TT][8];
-#pragma unroll
-    for (int t = 0; t < TT; ++t) {
-        const uint32_t tt = tok + ((uint32_t)t < nt ? (uint32_t)t : nt - 1);
-        const __bf16 *qp = g.q.p + (int64_t)(sv.q0 + (int32_t)tt) * g.q.token + (int64_t)(h * g.group) * g.q.head + 8 * ln;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) up[t][i] = dn[t][i] = 0.0;
-        for (uint32_t e = 0; e < g.group; ++e) {
-            const bf8 x = *reinterpret_cast<const bf8 *>(qp + (int64_t)e * g.q.head);
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float y = (float)x[i];
-                // a NaN stays one in both sums
-                up[t][i] += (double)(y < 0.0f ? 0.0f : y);
-                dn[t][i] += (double)(y > 0.0f ? 0.0f : y);
-            }
-        }
-    }
     const int32_t *table = g.b.table + (uint64_t)seq * g.b.width;
     const uint32_t lp = g.c.log_page - lb, nbp = 1u << lp;
-    for (uint32_t j = j0 + slot; j < j1; j += PB) {
-        uint32_t page = (uint32_t)table[j >> lp];
-        const bool there = page < g.c.n_pages;
-        if (!there) {
-            report(g.b.err, ZX_E_CORRUPT);
-            page = 0;
+    bf8 lo[kUnroll], hi[kUnroll];
+    uint32_t none = 0;                                               // blocks of these that have no page
+    auto fetch = [&](uint32_t j) {
+        uint32_t page[kUnroll];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const uint32_t ju = j + u * PB < j1 ? j + u * PB : j1 - 1;
+            page[u] = (uint32_t)table[ju >> lp];
         }
-        const __bf16 *bp = g.c.bounds + (((uint64_t)page * g.c.heads + h) * nbp + (j & (nbp - 1u))) * (2 * D) + 8 * ln;
-        const bf8 lo = *reinterpret_cast<const bf8 *>(bp), hi = *reinterpret_cast<const bf8 *>(bp + D);
-        double s[TT];
+        none = 0;
 #pragma unroll
-        for (int t = 0; t < TT; ++t) s[t] = 0.0;
+        for (int u = 0; u < kUnroll; ++u) {
+            const uint32_t ju = j + u * PB < j1 ? j + u * PB : j1 - 1;
+            if (page[u] >= g.c.n_pages) {
+                report(g.b.err, ZX_E_CORRUPT);
+                page[u] = 0;
+                none |= 1u << u;
+            }
+            const __bf16 *bp = g.c.bounds + (((uint64_t)page[u] * g.c.heads + h) * nbp + (ju & (nbp - 1u))) * (2 * D) + 8 * ln;
+            lo[u] = *reinterpret_cast<const bf8 *>(bp);
+            hi[u] = *reinterpret_cast<const bf8 *>(bp + D);
+        }
+    };
+    fetch(j0 + slot);                                                // under way while the queries are added up
+    double up[TT][8], dn[TT][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const double a = (double)(float)lo[i], b = (double)(float)hi[i];
+    for (int t = 0; t < TT; ++t)
 #pragma unroll
-            for (int t = 0; t < TT; ++t) s[t] = __builtin_fma(up[t][i], b, __builtin_fma(dn[t][i], a, s[t]));
+        for (int i = 0; i < 8; ++i) up[t][i] = dn[t][i] = 0.0;
+    constexpr int kQ = TT == 1 ? 4 : 2;                              // heads read at a time, for each token
+    for (uint32_t e = 0; e < g.group; e += kQ) {
+        bf8 x[TT][kQ];
+#pragma unroll
+        for (int t = 0; t < TT; ++t) {
+            const uint32_t tt = tok + ((uint32_t)t < nt ? (uint32_t)t : nt - 1);
+            const __bf16 *qp = g.q.p + (int64_t)(sv.q0 + (int32_t)tt) * g.q.token + (int64_t)(h * g.group) * g.q.head + 8 * ln;
+#pragma unroll
+            for (int k = 0; k < kQ; ++k) x[t][k] = *reinterpret_cast<const bf8 *>(qp + (int64_t)(e + k < g.group ? e + k : e) * g.q.head);
         }
 #pragma unroll
-        for (uint32_t w = LB / 2; w >= 1; w >>= 1)
+        for (int t = 0; t < TT; ++t)
 #pragma unroll
-            for (int t = 0; t < TT; ++t) s[t] += __shfl_xor(s[t], (int)w, 64);
-        if (ln < nt) {
-            double x = s[0];
+            for (int k = 0; k < kQ; ++k)
 #pragma unroll
-            for (int t = 1; t < TT; ++t) x = ln == (uint32_t)t ? s[t] : x;
-            g.keys[((uint64_t)(grp * TT + ln) * g.c.heads + h) * g.nb + j] = there ? order_key(x) : 0;
+                for (int i = 0; i < 8; ++i) {
+                    const float y = e + k < g.group ? (float)x[t][k][i] : 0.0f;
+                    // a NaN stays one in both sums
+                    up[t][i] += (double)(y < 0.0f ? 0.0f : y);
+                    dn[t][i] += (double)(y > 0.0f ? 0.0f : y);
+                }
+    }
+    for (uint32_t j = j0 + slot; j < j1; j += kUnroll * PB) {
+        double s[kUnroll][TT];
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+#pragma unroll
+            for (int t = 0; t < TT; ++t) s[u][t] = 0.0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const double a = (double)(float)lo[u][i], b = (double)(float)hi[u][i];
+#pragma unroll
+                for (int t = 0; t < TT; ++t) s[u][t] = __builtin_fma(up[t][i], b, __builtin_fma(dn[t][i], a, s[u][t]));
+            }
+        }
+        const uint32_t gone = none;
+        if (j + kUnroll * PB < j1) fetch(j + kUnroll * PB);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+#pragma unroll
+            for (int t = 0; t < TT; ++t) s[u][t] = sum_lanes<(int)LB>(s[u][t]);
+            if (ln < nt && j + u * PB < j1) {
+                double x = s[u][0];
+#pragma unroll
+                for (int t = 1; t < TT; ++t) x = ln == (uint32_t)t ? s[u][t] : x;
+                g.keys[((uint64_t)(grp * TT + ln) * g.c.heads + h) * g.nb + j + u * PB] = gone >> u & 1u ? 0 : order_key(x);
+            }
         }
     }
 }
@@ -113,7 +170,7 @@ template <int TT>
 __global__ __launch_bounds__(kThreads) void k_top(SelectArgs g)
 {
     __shared__ uint64_t held[kHeld];
-    __shared__ uint32_t hist[256];
+    __shared__ uint32_t hist[1 << kDigit];
     __shared__ uint64_t wide[2][4];
     __shared__ uint32_t pick[3];
     __shared__ uint32_t sums[2][4];
@@ -173,32 +230,34 @@ __global__ __launch_bounds__(kThreads) void k_top(SelectArgs g)
         top = 0;
     }
     while (top > 0 && same != want) {
-        const int bits = top < 8 ? top : 8, sh = top - bits;
-        hist[tid] = 0;
+        const int bits = top < kDigit ? top : kDigit, sh = top - bits;
+        for (uint32_t i = tid; i < 1u << kDigit; i += kThreads) hist[i] = 0;
         __syncthreads();
         for (uint32_t i = tid; i < n; i += kThreads) {
             const uint64_t x = key(i);
             if ((x & mask) == cut) atomicAdd(&hist[(uint32_t)(x >> sh) & ((1u << bits) - 1u)], 1u);
         }
         __syncthreads();
-        if (wave == 0) {
-            // lane l has digits 255 - 4 l downwards: the digit at which the count from above reaches `want`
-            uint32_t c[4], mine = 0, total;
+        // thread t has kEach digits, the highest first: the digit at which the count from above reaches `want`
+        constexpr uint32_t kEach = (1u << kDigit) / kThreads;
+        uint32_t c[kEach], mine = 0, total;
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                c[i] = hist[255u - 4u * lane - i];
-                mine += c[i];
-            }
-            uint32_t above = wave_excl_scan(mine, total);
+        for (uint32_t i = 0; i < kEach; ++i) {
+            c[i] = hist[(1u << kDigit) - 1u - kEach * tid - i];
+            mine += c[i];
+        }
+        uint32_t above = wave_excl_scan(mine, total);
+        if (lane == 0) sums[0][wave] = total;
+        __syncthreads();
+        for (uint32_t w = 0; w < wave; ++w) above += sums[0][w];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                if (above < want && above + c[i] >= want) {
-                    pick[0] = 255u - 4u * lane - i;
-                    pick[1] = above;
-                    pick[2] = c[i];
-                }
-                above += c[i];
+        for (uint32_t i = 0; i < kEach; ++i) {
+            if (above < want && above + c[i] >= want) {
+                pick[0] = (1u << kDigit) - 1u - kEach * tid - i;
+                pick[1] = above;
+                pick[2] = c[i];
             }
+            above += c[i];
         }
         __syncthreads();
         cut |= (uint64_t)pick[0] << sh;
@@ -312,8 +371,8 @@ extern "C" zx_status zx_paged_select(const zx_paged_cache *cache, const zx_paged
     g.nb = s.nb;
     g.slab = s.slab;
     // blocks of a workgroup: few enough to fill the card, many enough to be worth its start
-    const uint32_t at_once = kThreads / (cache->head_dim / 8);
-    const uint64_t want = ceil_div(2048, (uint64_t)s.slab * cache->kv_heads);
+    const uint32_t at_once = 4 * kThreads / (cache->head_dim / 8);
+    const uint64_t want = ceil_div(s.tt == 1 ? 1280 : 512, (uint64_t)s.slab * cache->kv_heads);
     uint32_t per = ceil_div(s.nb ? s.nb : 1, want);
     per = ceil_div(per, at_once) * at_once;
     if (ceil_div(s.nb ? s.nb : 1, per) > 65535) per = ceil_div(ceil_div(s.nb, 65535), at_once) * at_once;
