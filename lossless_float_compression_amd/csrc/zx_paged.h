@@ -63,32 +63,38 @@ template <class Count, class Weight>
 __device__ __forceinline__ bool find_item(const Batch &b, uint32_t idx, Count count, Weight weight, uint32_t &seq, Seq &sv,
                                           uint32_t &local, uint32_t &before)
 {
+    constexpr int kAtOnce = 4;                   // steps whose lengths are read together
     const uint32_t lane = threadIdx.x & 63u;
     uint32_t acc = 0, wacc = 0;
-    for (uint32_t s0 = 0; s0 < b.n_seqs; s0 += 64) {
-        Seq v{0, 0, 0};
-        uint32_t c = 0, w = 0;
-        if (s0 + lane < b.n_seqs) {
-            v = load_seq(b, s0 + lane);
-            c = count(v);
-            w = weight(v);
+    for (uint32_t s0 = 0; s0 < b.n_seqs; s0 += 64 * kAtOnce) {
+        Seq v[kAtOnce];
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            v[i] = Seq{0, 0, 0};
+            if (s0 + 64 * i + lane < b.n_seqs) v[i] = load_seq(b, s0 + 64 * i + lane);
         }
-        uint32_t total, wtotal;
-        const uint32_t ex = wave_excl_scan(c, total);
-        const uint32_t wex = wave_excl_scan(w, wtotal);
-        if (idx < acc + total) {
-            const uint64_t m = __ballot(idx >= acc + ex && idx < acc + ex + c);
-            const int l = __builtin_ctzll(m);
-            seq = s0 + (uint32_t)l;
-            sv.q0 = __builtin_amdgcn_readlane(v.q0, l);
-            sv.nq = __builtin_amdgcn_readlane(v.nq, l);
-            sv.kv = __builtin_amdgcn_readlane(v.kv, l);
-            local = idx - acc - (uint32_t)__builtin_amdgcn_readlane((int)ex, l);
-            before = wacc + (uint32_t)__builtin_amdgcn_readlane((int)wex, l);
-            return true;
+#pragma unroll
+        for (int i = 0; i < kAtOnce; ++i) {
+            if (s0 + 64 * i >= b.n_seqs) break;
+            const bool in = s0 + 64 * i + lane < b.n_seqs;
+            const uint32_t c = in ? count(v[i]) : 0, w = in ? weight(v[i]) : 0;
+            uint32_t total, wtotal;
+            const uint32_t ex = wave_excl_scan(c, total);
+            const uint32_t wex = wave_excl_scan(w, wtotal);
+            if (idx < acc + total) {
+                const uint64_t m = __ballot(idx >= acc + ex && idx < acc + ex + c);
+                const int l = __builtin_ctzll(m);
+                seq = s0 + 64 * i + (uint32_t)l;
+                sv.q0 = __builtin_amdgcn_readlane(v[i].q0, l);
+                sv.nq = __builtin_amdgcn_readlane(v[i].nq, l);
+                sv.kv = __builtin_amdgcn_readlane(v[i].kv, l);
+                local = idx - acc - (uint32_t)__builtin_amdgcn_readlane((int)ex, l);
+                before = wacc + (uint32_t)__builtin_amdgcn_readlane((int)wex, l);
+                return true;
+            }
+            acc += total;
+            wacc += wtotal;
         }
-        acc += total;
-        wacc += wtotal;
     }
     return false;
 }

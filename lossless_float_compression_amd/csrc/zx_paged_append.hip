@@ -3,7 +3,7 @@
 //
 // A workgroup takes one segment of a sequence's new tokens (the tokens of one bounded
 // block, or of 32 places where the cache has no bounds) and a group of heads: of the
-// keys and values, or of the queries.  It computes the cosines and sines of the
+// keys, of the values or of the queries.  It computes the cosines and sines of the
 // segment's positions once, in LDS, and turns the rows of all its heads with them.  A
 // thread holds 16 channels, eight rotated pairs.  One workgroup owns a block's bounds
 // for its heads, so they are reduced in registers and LDS with no atomics and do not
@@ -85,6 +85,8 @@ constexpr uint32_t kSeg = 32;          // places of a segment where there are no
 constexpr uint32_t kTab = 32;          // tokens whose cosines and sines are held at a time
 constexpr uint32_t kGroup = 8;         // heads of a workgroup
 
+typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
+
 struct Turn {
     const double *inv_freq;
     const int32_t *positions;
@@ -102,18 +104,6 @@ struct AppendArgs {
     uint32_t q_heads, log_seg;
 };
 
-// Two 8-channel pieces of a row: channels a .. a + 7 and b .. b + 7.
-struct Piece {
-    float a[8], b[8];
-};
-
-__device__ __forceinline__ void load8(const __bf16 *p, float (&o)[8])
-{
-    const bf8 x = *reinterpret_cast<const bf8 *>(p);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) o[i] = (float)x[i];
-}
-
 __device__ __forceinline__ bf8 to_bf8(const float (&x)[8])
 {
     bf8 o;
@@ -121,6 +111,15 @@ __device__ __forceinline__ bf8 to_bf8(const float (&x)[8])
     for (int i = 0; i < 8; ++i) o[i] = (__bf16)x[i];
     return o;
 }
+
+// BF16 pairs as pairs of 16-bit integers that order like them (-0 below +0), and back.
+__device__ __forceinline__ i16x2 ordered(uint32_t w)
+{
+    const i16x2 b = __builtin_bit_cast(i16x2, w);
+    return b ^ ((b >> 15) & (int16_t)0x7FFF);
+}
+__device__ __forceinline__ uint16_t unordered(int16_t x) { return (uint16_t)(x ^ ((x >> 15) & 0x7FFF)); }
+constexpr int16_t kTopBf16 = 0x7F80, kLowBf16 = (int16_t)~0x7F80;   // +inf and -inf in that order
 
 // x / scale as E4M3, to the nearest, saturating at 448; NaN stays NaN.
 __device__ __forceinline__ float fp8_in(float x, float scale)
@@ -140,45 +139,239 @@ __device__ __forceinline__ u2 to_fp8(const float (&x)[8])
     return o;
 }
 
-__device__ __forceinline__ void from_fp8(u2 v, float (&o)[8])
+__device__ __forceinline__ uint32_t bf16_pair_of_fp8(uint32_t w, bool high)
 {
-#pragma unroll
-    for (int w = 0; w < 2; ++w) {
-        const f2 lo = __builtin_amdgcn_cvt_pk_f32_fp8((int)v[w], false), hi = __builtin_amdgcn_cvt_pk_f32_fp8((int)v[w], true);
-        o[4 * w] = lo[0];
-        o[4 * w + 1] = lo[1];
-        o[4 * w + 2] = hi[0];
-        o[4 * w + 3] = hi[1];
-    }
+    const f2 x = high ? __builtin_amdgcn_cvt_pk_f32_fp8((int)w, true) : __builtin_amdgcn_cvt_pk_f32_fp8((int)w, false);
+    const bf2 r = {(__bf16)x[0], (__bf16)x[1]};
+    return __builtin_bit_cast(uint32_t, r);
 }
 
-// Store a piece of eight channels as the cache holds it; x becomes the stored values.
+// Store eight channels as the cache holds them; the stored values as BF16 pairs (exact).
 template <int DT>
-__device__ __forceinline__ void store8(uint8_t *row, uint32_t ch, float (&x)[8], float scale)
+__device__ __forceinline__ u4 store8(uint8_t *row, uint32_t ch, float (&x)[8], float scale, bool yes)
 {
+    u4 r;
     if constexpr (DT == ZX_BF16) {
         const bf8 y = to_bf8(x);
-        *reinterpret_cast<bf8 *>(row + 2 * ch) = y;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = (float)y[i];
+        if (yes) *reinterpret_cast<bf8 *>(row + 2 * ch) = y;
+        r = __builtin_bit_cast(u4, y);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) x[i] = fp8_in(x[i], scale);
         const u2 y = to_fp8(x);
-        *reinterpret_cast<u2 *>(row + ch) = y;
-        from_fp8(y, x);
+        if (yes) *reinterpret_cast<u2 *>(row + ch) = y;
+        r = u4{bf16_pair_of_fp8(y[0], false), bf16_pair_of_fp8(y[0], true), bf16_pair_of_fp8(y[1], false), bf16_pair_of_fp8(y[1], true)};
+    }
+    return r;
+}
+
+enum { KEYS, VALUES, QUERIES };
+
+// The new tokens of one segment: places p0 .. p1 - 1 of a sequence, whose packed row of
+// place p is row0 + p.
+struct Segment {
+    int32_t p0, p1, row0, start;     // start: first place of the segment's block
+    const int32_t *table;
+    bool older;                      // the block has tokens ahead of p0
+};
+
+template <int DT, int D, int ROLE>
+__device__ __forceinline__ void append_rows(const AppendArgs &g, const Segment &sg, uint32_t group, float *lds)
+{
+    constexpr uint32_t TPR = D / 16;                    // threads of a row
+    constexpr uint32_t ROWS = kThreads / TPR;           // rows at a time
+    constexpr int kBatch = ROLE == KEYS ? 2 : 4;        // rows of a thread that are read together
+    const uint32_t tid = threadIdx.x;
+    const uint32_t lanes = ROLE == QUERIES ? kGroup : g.kv_lanes, heads = ROLE == QUERIES ? g.q_heads : g.c.heads;   // lanes: heads side by side
+    const uint32_t h0 = group * lanes;
+    const uint32_t slot = tid / TPR, c = tid % TPR;
+    const uint32_t tslot = slot / lanes, tstep = ROWS / lanes;
+    const bool live = h0 + slot % lanes < heads;
+    const uint32_t head = live ? h0 + slot % lanes : heads - 1;
+    const uint32_t half = ROLE == VALUES ? 0 : g.turn.half;
+    const bool turned = 8 * c < half;
+    // a thread's two pieces: the two sides of eight pairs, or 16 channels that are not turned or hold whole pairs
+    const bool split = turned && !g.turn.interleaved;
+    const uint32_t ca = split ? 8 * c : 16 * c, cb = split ? half + 8 * c : 16 * c + 8;
+    const Rows &in = ROLE == QUERIES ? g.q : ROLE == KEYS ? g.k : g.v;
+    const __bf16 *src = in.p + (int64_t)sg.row0 * in.token + (int64_t)head * in.head;
+    float scale = 1.0f;
+    if (DT != ZX_BF16 && ROLE != QUERIES) {
+        const float *sc = ROLE == KEYS ? g.c.k_scale : g.c.v_scale;
+        if (sc) scale = sc[head];
+    }
+    const bool bounds = ROLE == KEYS && g.c.bounds;
+    i16x2 lo[8], hi[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        lo[i] = i16x2{kTopBf16, kTopBf16};
+        hi[i] = i16x2{kLowBf16, kLowBf16};
+    }
+
+    for (int32_t t0 = sg.p0; t0 < sg.p1; t0 += (int32_t)kTab) {
+        const uint32_t nt = (uint32_t)(sg.p1 - t0) < kTab ? (uint32_t)(sg.p1 - t0) : kTab;
+        bf8 ra[kBatch], rb[kBatch];
+        uint32_t page[kBatch];
+        auto fetch = [&](uint32_t t) {                  // rows past the last one repeat it
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const uint32_t tu = t + u * tstep < nt ? t + u * tstep : nt - 1;
+                const int32_t p = t0 + (int32_t)tu;
+                const __bf16 *r = src + (int64_t)p * in.token;
+                ra[u] = *reinterpret_cast<const bf8 *>(r + ca);
+                rb[u] = *reinterpret_cast<const bf8 *>(r + cb);
+                if (ROLE != QUERIES) page[u] = (uint32_t)sg.table[p >> g.c.log_page];
+            }
+        };
+        fetch(tslot);                                   // under way while the cosines and sines are worked out
+        if (half) {
+            if (t0 > sg.p0) __syncthreads();
+            for (uint32_t i = tid; i < nt * half; i += kThreads) {
+                const uint32_t t = i / half, j = i - t * half;
+                const int32_t p = g.turn.positions ? g.turn.positions[sg.row0 + t0 + (int32_t)t] : t0 + (int32_t)t;
+                // whole turns are dropped in 64 bits: what is left keeps its 24 bits at any position
+                const double rev = (double)p * g.turn.inv_freq[j] * 0.15915494309189533577;
+                const float r = (float)(rev - __builtin_rint(rev));
+                float sn, cs;
+                sincospif(2.0f * r, &sn, &cs);
+                reinterpret_cast<f2 *>(lds)[t * half + j] = f2{cs * g.turn.magnitude, sn * g.turn.magnitude};
+            }
+            __syncthreads();
+        }
+        for (uint32_t tb = tslot; tb < nt; tb += kBatch * tstep) {
+            if (tb != tslot) fetch(tb);
+#pragma unroll
+            for (int u = 0; u < kBatch; ++u) {
+                const uint32_t tu = tb + u * tstep;
+                const bool yes = live && tu < nt;
+                const uint32_t t = tu < nt ? tu : nt - 1;
+                const int32_t p = t0 + (int32_t)t;
+                float x[8], y[8];
+#pragma unroll
+                for (int i = 0; i < 8; ++i) {
+                    x[i] = (float)ra[u][i];
+                    y[i] = (float)rb[u][i];
+                }
+                if (turned) {
+                    const f4 *tab = reinterpret_cast<const f4 *>(reinterpret_cast<const f2 *>(lds) + t * half + 8 * c);
+                    auto turn = [](float &a, float &b, float cs, float sn) {
+                        const float u = a * cs - b * sn;
+                        b = b * cs + a * sn;
+                        a = u;
+                    };
+                    if (split) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const f4 w = tab[i];        // of two pairs
+                            turn(x[2 * i], y[2 * i], w[0], w[1]);
+                            turn(x[2 * i + 1], y[2 * i + 1], w[2], w[3]);
+                        }
+                    } else {
+#pragma unroll
+                        for (int i = 0; i < 2; ++i) {
+                            const f4 w = tab[i], v = tab[2 + i];
+                            turn(x[4 * i], x[4 * i + 1], w[0], w[1]);
+                            turn(x[4 * i + 2], x[4 * i + 3], w[2], w[3]);
+                            turn(y[4 * i], y[4 * i + 1], v[0], v[1]);
+                            turn(y[4 * i + 2], y[4 * i + 3], v[2], v[3]);
+                        }
+                    }
+                }
+                if constexpr (ROLE == QUERIES) {
+                    __bf16 *dst = g.qo.p + (int64_t)(sg.row0 + p) * g.qo.token + (int64_t)head * g.qo.head;
+                    if (yes) {
+                        *reinterpret_cast<bf8 *>(dst + ca) = to_bf8(x);
+                        *reinterpret_cast<bf8 *>(dst + cb) = to_bf8(y);
+                    }
+                } else {
+                    const bool there = page[u] < g.c.n_pages;
+                    if (!there) report(g.b.err, ZX_E_CORRUPT);
+                    const uint32_t at = (uint32_t)p & ((1u << g.c.log_page) - 1u), pg = there ? page[u] : 0;
+                    uint8_t *dst = ROLE == KEYS ? g.c.k + (int64_t)head * g.c.k_head + (int64_t)pg * g.c.k_page + (uint64_t)at * g.c.k_token
+                                                : g.c.v + (int64_t)head * g.c.v_head + (int64_t)pg * g.c.v_page + (uint64_t)at * g.c.v_token;
+                    if constexpr (DT == ZX_BF16 && ROLE == VALUES) {
+                        if (yes && there) {             // bits as they are
+                            *reinterpret_cast<bf8 *>(dst + 2 * ca) = ra[u];
+                            *reinterpret_cast<bf8 *>(dst + 2 * cb) = rb[u];
+                        }
+                    } else {
+                        const u4 wa = store8<DT>(dst, ca, x, scale, yes && there), wb = store8<DT>(dst, cb, y, scale, yes && there);
+                        if (bounds) {
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const i16x2 a = ordered(wa[i]), b = ordered(wb[i]);
+                                lo[i] = __builtin_elementwise_min(lo[i], a);
+                                hi[i] = __builtin_elementwise_max(hi[i], a);
+                                lo[4 + i] = __builtin_elementwise_min(lo[4 + i], b);
+                                hi[4 + i] = __builtin_elementwise_max(hi[4 + i], b);
+                            }
+                        }
+                    }
+                }
+                __builtin_amdgcn_sched_barrier(0);      // one row's values at a time
+            }
+        }
+    }
+
+    if constexpr (ROLE == KEYS) {
+        if (!bounds) return;
+        const uint32_t page = (uint32_t)sg.table[sg.start >> g.c.log_page];
+        if (page >= g.c.n_pages) return;                // reported above; the whole workgroup leaves
+        // [rows][smallest, largest][D] as ordered 16-bit integers
+        int16_t *const sh = reinterpret_cast<int16_t *>(lds);
+        __syncthreads();
+        i16x2 *mine = reinterpret_cast<i16x2 *>(sh + slot * (2 * D));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            mine[ca / 2 + i] = lo[i];
+            mine[cb / 2 + i] = lo[4 + i];
+            mine[(D + ca) / 2 + i] = hi[i];
+            mine[(D + cb) / 2 + i] = hi[4 + i];
+        }
+        __syncthreads();
+        const uint32_t nb = 1u << (g.c.log_page - g.c.log_block);
+        const uint32_t blk = (uint32_t)(sg.start >> g.c.log_block) & (nb - 1u);
+        const uint32_t nh = heads - h0 < lanes ? heads - h0 : lanes;
+        const uint32_t used = (uint32_t)(sg.p1 - sg.p0) < tstep ? (uint32_t)(sg.p1 - sg.p0) : tstep;    // rows of a head that took part
+        for (uint32_t i = tid; i < nh * 2 * D; i += kThreads) {
+            const uint32_t h = i / (2 * D), w = i % (2 * D);
+            const bool low = w < (uint32_t)D;
+            int16_t x = sh[h * (2 * D) + w];
+            for (uint32_t r = 1; r < used; ++r) {
+                const int16_t y = sh[(r * lanes + h) * (2 * D) + w];
+                x = low ? (y < x ? y : x) : (y > x ? y : x);
+            }
+            if (low ? x < kLowBf16 : x > kTopBf16) {
+                // a NaN got in: the values once more, without it
+                x = low ? kTopBf16 : kLowBf16;
+                for (int32_t p = sg.p0; p < sg.p1; ++p) {
+                    const uint64_t at = (uint32_t)p & ((1u << g.c.log_page) - 1u);
+                    const uint8_t *row = g.c.k + (int64_t)page * g.c.k_page + (int64_t)(h0 + h) * g.c.k_head + at * g.c.k_token;
+                    const uint32_t ch = w % D;
+                    const uint32_t bits = DT == ZX_BF16 ? reinterpret_cast<const uint16_t *>(row)[ch] : bf16_pair_of_fp8(row[ch], false) & 0xFFFFu;
+                    if ((bits & 0x7FFFu) > 0x7F80u) continue;
+                    const int16_t y = ordered(bits)[0];
+                    x = low ? (y < x ? y : x) : (y > x ? y : x);
+                }
+            }
+            uint16_t *o = reinterpret_cast<uint16_t *>(g.c.bounds) + (((uint64_t)page * g.c.heads + h0 + h) * nb + blk) * (2 * D) + w;
+            if (sg.older) {
+                const uint32_t old = *o;
+                if ((old & 0x7FFFu) <= 0x7F80u) {
+                    const int16_t y = ordered(old)[0];
+                    x = low ? (y < x ? y : x) : (y > x ? y : x);
+                }
+            }
+            *o = unordered(x);
+        }
     }
 }
 
 template <int DT, int D>
-__global__ __launch_bounds__(kThreads) void k_paged_append(AppendArgs g)
+__global__ __launch_bounds__(kThreads, 4) void k_paged_append(AppendArgs g)
 {
-    constexpr uint32_t TPR = D / 16;            // threads of a row
-    constexpr uint32_t ROWS = kThreads / TPR;   // rows at a time
-    // the cosines and sines of kTab tokens; then, for the bounds, every thread's 16 smallest and 16 largest
-    __shared__ __align__(16) float lds[kTab * D > kThreads * 32 ? kTab * D : kThreads * 32];
-
-    const uint32_t tid = threadIdx.x;
+    // the cosines and sines of kTab tokens; then the bounds of every thread's 16 channels
+    __shared__ __align__(16) float lds[kTab * D > kThreads * 16 ? kTab * D : kThreads * 16];
     uint32_t seq, seg, unused;
     Seq sv;
     const uint32_t ls = g.log_seg;
@@ -192,158 +385,17 @@ __global__ __launch_bounds__(kThreads) void k_paged_append(AppendArgs g)
         [](const Seq &) { return 0u; }, seq, sv, seg, unused);
     if (!found) return;
     const int32_t first = sv.kv > sv.nq ? sv.kv - sv.nq : 0;       // first new token that has a place
-    const int32_t s0 = ((first >> ls) + (int32_t)seg) << ls;
-    const int32_t p0 = s0 > first ? s0 : first;
-    const int32_t p1 = s0 + (1 << ls) < sv.kv ? s0 + (1 << ls) : sv.kv;
-    const int32_t row0 = sv.q0 + sv.nq - sv.kv;                     // packed row of position p: row0 + p
-
-    const bool is_q = blockIdx.y >= g.kv_groups;
-    const uint32_t lanes = is_q ? kGroup : g.kv_lanes;              // heads side by side
-    const uint32_t h0 = is_q ? (blockIdx.y - g.kv_groups) * kGroup : blockIdx.y * g.kv_lanes;
-    const uint32_t slot = tid / TPR, c = tid % TPR;
-    const uint32_t head = h0 + slot % lanes, tslot = slot / lanes, tstep = ROWS / lanes;
-    const bool live = head < (is_q ? g.q_heads : g.c.heads);
-    const uint32_t half = g.turn.half;
-    const bool turned = 8 * c < half;
-    // a thread's two pieces: the two sides of eight pairs, or 16 channels that are not turned or hold whole pairs
-    const bool split = turned && !g.turn.interleaved;
-    const uint32_t ca = split ? 8 * c : 16 * c, cb = split ? half + 8 * c : 16 * c + 8;
-    const int32_t *table = g.b.table + (uint64_t)seq * g.b.width;
-    float ks = 1.0f, vs = 1.0f;
-    if (DT != ZX_BF16 && !is_q && live) {
-        ks = g.c.k_scale ? g.c.k_scale[head] : 1.0f;
-        vs = g.c.v_scale ? g.c.v_scale[head] : 1.0f;
-    }
-    const bool bounds = !is_q && g.c.bounds;
-    Piece lo, hi;
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        lo.a[i] = lo.b[i] = __builtin_huge_valf();
-        hi.a[i] = hi.b[i] = -__builtin_huge_valf();
-    }
-
-    for (int32_t t0 = p0; t0 < p1; t0 += (int32_t)kTab) {
-        const uint32_t nt = (uint32_t)(p1 - t0) < kTab ? (uint32_t)(p1 - t0) : kTab;
-        if (half) {
-            __syncthreads();
-            for (uint32_t i = tid; i < nt * half; i += kThreads) {
-                const uint32_t t = i / half, j = i - t * half;
-                const int32_t p = g.turn.positions ? g.turn.positions[row0 + t0 + (int32_t)t] : t0 + (int32_t)t;
-                // whole turns are dropped in 64 bits: what is left keeps its 24 bits at any position
-                const double rev = (double)p * g.turn.inv_freq[j] * 0.15915494309189533577;
-                const float r = (float)(rev - __builtin_rint(rev));
-                float sn, cs;
-                sincospif(2.0f * r, &sn, &cs);
-                reinterpret_cast<f2 *>(lds)[t * half + j] = f2{cs * g.turn.magnitude, sn * g.turn.magnitude};
-            }
-            __syncthreads();
-        }
-        if (!live) continue;
-        for (uint32_t t = tslot; t < nt; t += tstep) {
-            const int32_t p = t0 + (int32_t)t;
-            const int64_t row = row0 + p;
-            Piece x;
-            const __bf16 *src = is_q ? g.q.p + row * g.q.token + (int64_t)head * g.q.head : g.k.p + row * g.k.token + (int64_t)head * g.k.head;
-            load8(src + ca, x.a);
-            load8(src + cb, x.b);
-            if (turned) {
-                const f4 *tab = reinterpret_cast<const f4 *>(reinterpret_cast<const f2 *>(lds) + t * half + 8 * c);
-                float cs[8], sn[8];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const f4 w = tab[i];
-                    cs[2 * i] = w[0];
-                    sn[2 * i] = w[1];
-                    cs[2 * i + 1] = w[2];
-                    sn[2 * i + 1] = w[3];
-                }
-                if (split) {
-#pragma unroll
-                    for (int i = 0; i < 8; ++i) {
-                        const float a = x.a[i], b = x.b[i];
-                        x.a[i] = a * cs[i] - b * sn[i];
-                        x.b[i] = b * cs[i] + a * sn[i];
-                    }
-                } else {
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const float a = x.a[2 * i], b = x.a[2 * i + 1], d = x.b[2 * i], e = x.b[2 * i + 1];
-                        x.a[2 * i] = a * cs[i] - b * sn[i];
-                        x.a[2 * i + 1] = b * cs[i] + a * sn[i];
-                        x.b[2 * i] = d * cs[4 + i] - e * sn[4 + i];
-                        x.b[2 * i + 1] = e * cs[4 + i] + d * sn[4 + i];
-                    }
-                }
-            }
-            if (is_q) {
-                __bf16 *dst = g.qo.p + row * g.qo.token + (int64_t)head * g.qo.head;
-                *reinterpret_cast<bf8 *>(dst + ca) = to_bf8(x.a);
-                *reinterpret_cast<bf8 *>(dst + cb) = to_bf8(x.b);
-                continue;
-            }
-            const uint32_t page = (uint32_t)table[p >> g.c.log_page];
-            if (page >= g.c.n_pages) {
-                report(g.b.err, ZX_E_CORRUPT);
-                continue;
-            }
-            const uint32_t at = (uint32_t)p & ((1u << g.c.log_page) - 1u);
-            uint8_t *kr = g.c.k + (int64_t)page * g.c.k_page + (int64_t)head * g.c.k_head + (uint64_t)at * g.c.k_token;
-            store8<DT>(kr, ca, x.a, ks);
-            store8<DT>(kr, cb, x.b, ks);
-            if (bounds) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    lo.a[i] = fminf(lo.a[i], x.a[i]);
-                    hi.a[i] = fmaxf(hi.a[i], x.a[i]);
-                    lo.b[i] = fminf(lo.b[i], x.b[i]);
-                    hi.b[i] = fmaxf(hi.b[i], x.b[i]);
-                }
-            }
-            const __bf16 *vr = g.v.p + row * g.v.token + (int64_t)head * g.v.head + 16 * c;
-            uint8_t *vd = g.c.v + (int64_t)page * g.c.v_page + (int64_t)head * g.c.v_head + (uint64_t)at * g.c.v_token;
-            if constexpr (DT == ZX_BF16) {
-                const u4 w0 = reinterpret_cast<const u4 *>(vr)[0], w1 = reinterpret_cast<const u4 *>(vr)[1];
-                reinterpret_cast<u4 *>(vd + 32 * c)[0] = w0;
-                reinterpret_cast<u4 *>(vd + 32 * c)[1] = w1;
-            } else {
-                load8(vr, x.a);
-                load8(vr + 8, x.b);
-                store8<DT>(vd, 16 * c, x.a, vs);
-                store8<DT>(vd, 16 * c + 8, x.b, vs);
-            }
-        }
-    }
-
-    if (!bounds) return;
-    const uint32_t page = (uint32_t)table[s0 >> g.c.log_page];
-    if (page >= g.c.n_pages) return;            // reported above; the whole workgroup leaves
-    __syncthreads();
-    float *mine = lds + slot * (2 * D);         // [rows][smallest, largest][D]
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        mine[ca + i] = lo.a[i];
-        mine[cb + i] = lo.b[i];
-        mine[D + ca + i] = hi.a[i];
-        mine[D + cb + i] = hi.b[i];
-    }
-    __syncthreads();
-    const uint32_t nb = 1u << (g.c.log_page - g.c.log_block);
-    const uint32_t blk = (uint32_t)(s0 >> g.c.log_block) & (nb - 1u);
-    const uint32_t nh = g.c.heads - h0 < lanes ? g.c.heads - h0 : lanes;
-    for (uint32_t i = tid; i < nh * 2 * D; i += kThreads) {
-        const uint32_t h = i / (2 * D), w = i % (2 * D);
-        float x = lds[h * (2 * D) + w];
-        for (uint32_t r = 1; r < tstep; ++r) {
-            const float y = lds[(r * lanes + h) * (2 * D) + w];
-            x = w < (uint32_t)D ? fminf(x, y) : fmaxf(x, y);
-        }
-        __bf16 *o = g.c.bounds + (((uint64_t)page * g.c.heads + h0 + h) * nb + blk) * (2 * D) + w;
-        if (first > s0) {                       // the block has older tokens
-            const float y = (float)*o;
-            x = w < (uint32_t)D ? fminf(x, y) : fmaxf(x, y);
-        }
-        *o = (__bf16)x;                         // a stored value: exact
-    }
+    Segment sg;
+    sg.start = ((first >> ls) + (int32_t)seg) << ls;
+    sg.p0 = sg.start > first ? sg.start : first;
+    sg.p1 = sg.start + (1 << ls) < sv.kv ? sg.start + (1 << ls) : sv.kv;
+    sg.row0 = sv.q0 + sv.nq - sv.kv;
+    sg.table = g.b.table + (uint64_t)seq * g.b.width;
+    sg.older = first > sg.start;
+    // groups of heads: of the keys, of the values, of the queries
+    if (blockIdx.y < g.kv_groups) append_rows<DT, D, KEYS>(g, sg, blockIdx.y, lds);
+    else if (blockIdx.y < 2 * g.kv_groups) append_rows<DT, D, VALUES>(g, sg, blockIdx.y - g.kv_groups, lds);
+    else append_rows<DT, D, QUERIES>(g, sg, blockIdx.y - 2 * g.kv_groups, lds);
 }
 
 template <int DT>
@@ -385,7 +437,7 @@ extern "C" zx_status zx_paged_append(const zx_paged_cache *cache, const zx_paged
     g.kv_groups = ceil_div(g.c.heads, g.kv_lanes);
     const uint64_t by_len = ((uint64_t)n_tokens >> g.log_seg) + 2ull * batch->n_seqs;
     const uint32_t segs = (uint32_t)(by_len < n_tokens ? by_len : n_tokens);
-    const dim3 grid(segs, g.kv_groups + ceil_div(g.q_heads, kGroup));
+    const dim3 grid(segs, 2 * g.kv_groups + ceil_div(g.q_heads, kGroup));
     if (cache->dtype == ZX_BF16) launch<ZX_BF16>(g, cache->head_dim, grid, stream);
     else launch<ZX_FP8_E4M3FN>(g, cache->head_dim, grid, stream);
     return hipGetLastError() == hipSuccess ? ZX_OK : ZX_E_HIP;
