@@ -221,15 +221,26 @@ static __global__ __launch_bounds__(256) void k_join(AttendArgs g)
     if (nch <= 8) {
         // few pieces: GR rows at a time, a lane adds up its four channels
         for (uint32_t row = blockIdx.z * GR + gr; row < nrows; row += gridDim.z * GR) {
-            float mm = -kInf, ll = 0.0f;
-            for (uint32_t i = 0; i < nch; ++i) mm = fmaxf(mm, g.stat[where(i, row) * 2]);
+            // (reads past the last piece repeat it: all are under way at once)
+            f4 y[8];
+            float pm[8], pl[8], mm = -kInf, ll = 0.0f;
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i) {
+                const uint64_t at = where(i < nch ? i : nch - 1, row);
+                pm[i] = g.stat[at * 2];
+                pl[i] = g.stat[at * 2 + 1];
+                y[i] = *reinterpret_cast<const f4 *>(g.part + at * D + 4 * ln);
+            }
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i) mm = fmaxf(mm, pm[i]);
             const float base = mm == -kInf ? 0.0f : mm;
             f4 x = {0, 0, 0, 0};
-            for (uint32_t i = 0; i < nch; ++i) {
-                const uint64_t at = where(i, row);
-                const float f = __builtin_amdgcn_exp2f(g.stat[at * 2] - base);
-                ll += g.stat[at * 2 + 1] * f;
-                x += *reinterpret_cast<const f4 *>(g.part + at * D + 4 * ln) * f;
+#pragma unroll
+            for (uint32_t i = 0; i < 8; ++i) {
+                if (i >= nch) break;
+                const float f = __builtin_amdgcn_exp2f(pm[i] - base);
+                ll += pl[i] * f;
+                x += y[i] * f;
             }
             const float inv = ll == 0.0f ? 0.0f : vs / ll;
             *reinterpret_cast<u2 *>(g.out.p + place(row) * g.out.token + (int64_t)head(row) * g.out.head + 4 * ln) =

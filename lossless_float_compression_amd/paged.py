@@ -186,6 +186,7 @@ class PagedBatch:
         self.q_start, self.kv_len, self.page_table = q_start, kv_len, page_table
         self.n_seqs = n
         self.device = q_start.device
+        self._index = q_start.get_device()
         self._c = zx_paged_batch(n, page_table.shape[1], _ANY if max_q is None else min(int(max_q), _ANY),
                                  _ANY if max_kv is None else min(int(max_kv), _ANY), q_start.data_ptr(),
                                  kv_len.data_ptr(), page_table.data_ptr())
@@ -254,6 +255,7 @@ class PagedKVCache:
                 raise ValueError(f"bounds must be a contiguous bfloat16 device tensor {list(bshape)}")
         self.bounds = bounds
         ptr = lambda t: None if t is None else t.data_ptr()   # noqa: E731
+        self._index = self.device.index
         self._c = zx_paged_cache(self.dtype, self.n_pages, self.kv_heads, self.head_dim, self.page_tokens,
                                  self.block_tokens or 0, k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2),
                                  v.stride(0), v.stride(1), v.stride(2), ptr(self.k_scale), ptr(self.v_scale),
@@ -281,11 +283,11 @@ class PagedKVCache:
     # ---- argument checks
     def _rows(self, t: torch.Tensor, name: str, heads: Optional[int], n: Optional[int], written: bool = False) -> zx_rows:
         sh = t.shape
-        if t.dtype != torch.bfloat16 or len(sh) != 3 or sh[2] != self.head_dim or (n is not None and sh[0] != n) or (
+        if t.dtype is not torch.bfloat16 or len(sh) != 3 or sh[2] != self.head_dim or (n is not None and sh[0] != n) or (
                 heads is not None and sh[1] != heads):
             raise ValueError(f"{name} must be a bfloat16 tensor [{'tokens' if n is None else n}, "
                              f"{'heads' if heads is None else heads}, {self.head_dim}], got {t.dtype} {list(sh)}")
-        if t.device != self.device:
+        if t.get_device() != self._index:
             raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
         s0, s1, s2 = t.stride()
         p = t.data_ptr()
@@ -296,35 +298,35 @@ class PagedKVCache:
         return zx_rows(p, s0, s1)
 
     def _common(self, batch: PagedBatch, err: Optional[torch.Tensor]):
-        if batch.device != self.device:
+        if batch._index != self._index:
             raise ValueError(f"the batch is on {batch.device}, the cache on {self.device}")
         if err is not None:
-            _int32(err, "err", self.device)
-            return err.data_ptr()
+            return _int32(err, "err", self.device).data_ptr()
         return None
 
     def _group(self, q: torch.Tensor) -> None:
         if q.dim() != 3 or q.shape[1] == 0 or q.shape[1] % self.kv_heads:
             raise ValueError(f"q must be [tokens, heads, {self.head_dim}] with a multiple of {self.kv_heads} heads")
 
-    def _elsewhere(self, stream, tensors, call):
-        """Run `call` on a side stream (after what the current one holds), with the cache's
-        device current; None if neither is needed.  The tensors' memory is not handed out
-        again before the side stream is done with them."""
-        if torch.cuda.current_device() != self.device.index:
+    def _away(self, stream) -> bool:
+        """Whether a call has to change the current device or stream first."""
+        return torch.cuda.current_device() != self._index or (stream is not None and _zx._side_stream(stream) is not None)
+
+    def _elsewhere(self, stream, batch, tensors, call):
+        """`call(stream)` with the cache's device current, or on a side stream after what the
+        current one holds.  The tensors' memory is not handed out again before the side
+        stream is done with them."""
+        if torch.cuda.current_device() != self._index:
             with torch.cuda.device(self.device):
-                return (call(stream),)
-        side = _zx._side_stream(stream)
-        if side is None:
-            return None
-        if side.device != self.device:
-            raise ValueError(f"the stream is on {side.device}, the cache on {self.device}")
-        side.wait_stream(torch.cuda.current_stream())
-        for t in tensors:
+                return call(stream)
+        if stream.device != self.device:
+            raise ValueError(f"the stream is on {stream.device}, the cache on {self.device}")
+        stream.wait_stream(torch.cuda.current_stream())
+        for t in (*tensors, batch.q_start, batch.kv_len, batch.page_table, *self._tensors):
             if t is not None:
-                t.record_stream(side)
-        with torch.cuda.stream(side):
-            return (call(None),)
+                t.record_stream(stream)
+        with torch.cuda.stream(stream):
+            return call(None)
 
     def _raw(self, stream) -> int:
         if isinstance(stream, C.c_void_p):
@@ -350,11 +352,9 @@ class PagedKVCache:
 
         err: device int32 word, 4 where lengths or page ids were out of range.  `stream`: a
         torch stream to run on after the work already enqueued on the current one."""
-        moved = self._elsewhere(stream, (k, v, q, q_out, positions, err, batch.q_start, batch.kv_len, batch.page_table,
-                                         None if rotary is None else rotary.inv_freq, *self._tensors),
-                                lambda s: self.append(k, v, batch, q, rotary, positions, q_out, err, s))
-        if moved is not None:
-            return moved[0]
+        if self._away(stream):
+            return self._elsewhere(stream, batch, (k, v, q, q_out, positions, err, None if rotary is None else rotary.inv_freq),
+                                   lambda s: self.append(k, v, batch, q, rotary, positions, q_out, err, s))
         e = self._common(batch, err)
         n = k.shape[0]
         ck, cv = self._rows(k, "k", self.kv_heads, None), self._rows(v, "v", self.kv_heads, n)
@@ -401,11 +401,9 @@ class PagedKVCache:
 
         Rows behind the last sequence, and of sequences that are out of range, keep what they
         hold.  The same inputs give the same bits.  err, stream: as `append`."""
-        moved = self._elsewhere(stream, (q, out, lse, err, blocks, batch.q_start, batch.kv_len, batch.page_table,
-                                         *self._tensors),
-                                lambda s: self.attend(q, batch, scale, causal, window, blocks, out, lse, err, s))
-        if moved is not None:
-            return moved[0]
+        if self._away(stream):
+            return self._elsewhere(stream, batch, (q, out, lse, err, blocks),
+                                   lambda s: self.attend(q, batch, scale, causal, window, blocks, out, lse, err, s))
         e = self._common(batch, err)
         self._group(q)
         n, heads = q.shape[0], q.shape[1]
@@ -452,10 +450,9 @@ class PagedKVCache:
         the group's summed scores, from the bounds that `append` keeps (ties: the earlier block).
         q holds rotated queries, as for `attend`.  Rows behind the last sequence are left as they
         are (-1 when allocated here).  err, stream: as `append`."""
-        moved = self._elsewhere(stream, (q, blocks, err, batch.q_start, batch.kv_len, batch.page_table, *self._tensors),
-                                lambda s: self.select(q, batch, top_k, keep_first, keep_last, blocks, err, s))
-        if moved is not None:
-            return moved[0]
+        if self._away(stream):
+            return self._elsewhere(stream, batch, (q, blocks, err),
+                                   lambda s: self.select(q, batch, top_k, keep_first, keep_last, blocks, err, s))
         e = self._common(batch, err)
         self._group(q)
         n, heads = q.shape[0], q.shape[1]
