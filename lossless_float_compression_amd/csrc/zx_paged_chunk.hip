@@ -25,7 +25,7 @@ namespace {
 constexpr int kTile = 64;
 
 template <int DT, int D, int NW>
-__global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void k_chunk(AttendArgs g)
+__global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_chunk(AttendArgs g)
 {
     constexpr int ROWS = 32 * NW, NT = 64 * NW;
     constexpr int ES = DT == ZX_BF16 ? 2 : 1;
@@ -46,7 +46,12 @@ __global__ __launch_bounds__(NW * 64, NW == 8 ? 2 : 1) void k_chunk(AttendArgs g
     Seq sv;
     if (!find_piece<ROWS, kTile>(g, rest, chunk_steps<ROWS, kTile>(g), seq, sv, rt, part, nch, slot)) return;
     const uint32_t all = (uint32_t)sv.nq * G;
-    if (nch == 1) rt = div_up(all, ROWS) - 1 - rt;         // the last row tiles see the most tokens: they go first
+    if (nch == 1) {
+        // The last row tiles see the most tokens: they go first.  Of two workgroups on a CU
+        // the second has the tiles from the other end, shortest first, while there are no more.
+        const uint32_t tiles = div_up(all, ROWS), room = div_up(256, g.c.heads);
+        rt = NW == 4 && rt >= room && tiles <= 2 * room ? rt - room : tiles - 1 - rt;
+    }
     const uint32_t row0 = rt * ROWS, row9 = row0 + ROWS < all ? row0 + ROWS : all;
     const int32_t pos0 = sv.kv - sv.nq;
     const int32_t pa = pos0 + (int32_t)(row0 / G), pb = pos0 + (int32_t)((row9 - 1) / G);
@@ -444,10 +449,10 @@ constexpr uint32_t kChunkRounds = 3;
 ChunkPlan plan_chunk(uint64_t rows, uint32_t head_dim, uint32_t heads, uint64_t tokens, uint64_t seqs, uint64_t group, uint64_t cap, AttendArgs &g)
 {
     ChunkPlan p{};
-    p.waves = head_dim == 256 || rows <= 128 ? 4 : 8;
-    const uint32_t R = 32 * p.waves;
-    p.tiles = bound_tiles(tokens, seqs, group, R);
-    plan_split(p.tiles, ceil_div(256, heads), kChunkRounds, 8, 64, cap, kTile, g);
+    const uint32_t wide = bound_tiles(tokens, seqs, group, 256);
+    p.waves = head_dim == 256 || rows <= 128 || (uint64_t)wide * heads <= 0 ? 4 : 8;
+    p.tiles = p.waves == 8 ? wide : bound_tiles(tokens, seqs, group, 128);
+    plan_split(p.tiles, ceil_div(p.waves == 8 || head_dim == 256 ? 256 : 512, heads), kChunkRounds, 8, 64, cap, kTile, g);
     return p;
 }
 
