@@ -19,8 +19,7 @@ constexpr float kInf = __builtin_huge_valf();
 // as exactly as weights below one.
 constexpr float kSlack = 8.0f;
 
-constexpr uint32_t kRowsThreads = 256;        // four waves
-constexpr uint32_t kStep = 128;               // tokens of a workgroup's step: 32 for each wave
+constexpr uint32_t kStep = 128;               // tokens of a four-wave workgroup's step in k_rows: 32 for each wave
 
 struct AttendArgs {
     Cache c;

@@ -39,12 +39,14 @@ __device__ __forceinline__ bool tame(uint32_t &w)
     }
 }
 
+// Waves of one SIMD that k_rows leaves registers for.
 constexpr int rows_waves(int d, int mt) { return d == 256 ? 1 : mt == 3 ? 2 : mt == 2 ? (d == 64 ? 3 : 2) : d == 64 ? 4 : 3; }
 
-template <int DT, int D, int MT, bool LIST>
-__global__ __launch_bounds__(kRowsThreads, rows_waves(D, MT)) void k_rows(AttendArgs g)
+template <int DT, int D, int MT, bool LIST, int NW>
+__global__ __launch_bounds__(64 * NW, rows_waves(D, MT) * 4 >= NW ? rows_waves(D, MT) : NW / 4) void k_rows(AttendArgs g)
 {
     constexpr int ROWS = 16 * MT;
+    constexpr uint32_t kPieces = 2 * NW;             // 16-token pieces of a step
     constexpr int ES = DT == ZX_BF16 ? 2 : 1;
     constexpr int NK = D / 32;                       // matrix steps over the channels
     constexpr int VW = D < 128 ? D / 16 : 8;         // value channels a lane reads of one token
@@ -52,8 +54,8 @@ __global__ __launch_bounds__(kRowsThreads, rows_waves(D, MT)) void k_rows(Attend
     constexpr int VD = VW * ES / 4;                  // dwords of one
     constexpr int KL = D * 16 * ES / 64 / 16;        // 16-byte loads a lane makes of 16 keys
     constexpr int OS = D + 4;                        // LDS row of the join, in floats
-    __shared__ __align__(16) float ods[4 * 16 * OS];
-    __shared__ float mls[2][4][16];
+    __shared__ __align__(16) float ods[NW * 16 * OS];
+    __shared__ float mls[2][NW][16];
 
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -73,8 +75,8 @@ __global__ __launch_bounds__(kRowsThreads, rows_waves(D, MT)) void k_rows(Attend
         part = local % nch;
         piece_slot = item;
     } else {
-        chunk = chunk_steps<ROWS, (int)kStep>(g);
-        if (!find_piece<ROWS, (int)kStep>(g, item, chunk, seq, sv, rt, part, nch, piece_slot)) return;
+        chunk = chunk_steps<ROWS, 32 * NW>(g);
+        if (!find_piece<ROWS, 32 * NW>(g, item, chunk, seq, sv, rt, part, nch, piece_slot)) return;
     }
     uint32_t row0, nrows, tok0;                      // rows row0 .. of the token list starting at tok0
     if constexpr (LIST) {
@@ -137,14 +139,18 @@ __global__ __launch_bounds__(kRowsThreads, rows_waves(D, MT)) void k_rows(Attend
             }
             n += 64;
         }
-        const uint32_t steps = div_up(n << (lb - 4), kStep / 16), per = div_up(steps, nch);
-        u0 = part * per * (kStep / 16);
-        u1 = u0 + per * (kStep / 16);
+        const uint32_t steps = div_up(n << (lb - 4), kPieces), per = div_up(steps, nch);
+        u0 = part * per * kPieces;
+        u1 = u0 + per * kPieces;
         if (u1 > n << (lb - 4)) u1 = n << (lb - 4);
     } else {
         const uint32_t base = (uint32_t)(first_seen(g, pos0) >> 4);
-        u0 = base + part * chunk * (kStep / 16);
-        u1 = u0 + chunk * (kStep / 16);
+        u0 = base;
+        u1 = 0x7FFFFFFFu;
+        if (nch > 1) {
+            u0 += part * chunk * kPieces;
+            u1 = u0 + chunk * kPieces;
+        }
         if (u0 < (uint32_t)(lo_min >> 4)) u0 = (uint32_t)(lo_min >> 4);
         if (u1 > (uint32_t)((hi_max + 15) >> 4)) u1 = (uint32_t)((hi_max + 15) >> 4);
     }
@@ -156,7 +162,7 @@ __global__ __launch_bounds__(kRowsThreads, rows_waves(D, MT)) void k_rows(Attend
     uint64_t kat, vat, held;
     int32_t first_token;
     auto settle = [&](uint32_t u) {
-        u += 8 * (lane >> 1) + (lane & 1u);
+        u += kPieces * (lane >> 1) + (lane & 1u);
         bool there = u < u1;
         uint32_t t = u << 4;
         if constexpr (LIST) {
@@ -241,7 +247,7 @@ __global__ __launch_bounds__(kRowsThreads, rows_waves(D, MT)) void k_rows(Attend
         load_k(0);
         load_v(0);
     }
-    for (; u < u1; u += 8) {
+    for (; u < u1; u += kPieces) {
         const int32_t token[2] = {__builtin_amdgcn_readlane(first_token, (int)(2 * step)), __builtin_amdgcn_readlane(first_token, (int)(2 * step + 1))};
         const bool there[2] = {(held >> (2 * step) & 1u) != 0, (held >> (2 * step + 1) & 1u) != 0};
         // scores: 16 tokens x 16 rows a tile; a lane has row lr, tokens 4 lq .. 4 lq + 3 of each piece
@@ -264,10 +270,10 @@ __global__ __launch_bounds__(kRowsThreads, rows_waves(D, MT)) void k_rows(Attend
                     s[t][a] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf8, kk), __builtin_bit_cast(bf8, q[t][i]), s[t][a], 0, 0, 0);
             }
         }
-        const bool more = u + 8 < u1;
+        const bool more = u + kPieces < u1;
         if (more) {
             step = (step + 1) & 31u;
-            if (step == 0) settle(u + 8);
+            if (step == 0) settle(u + kPieces);
             load_k(step);
         }
 
@@ -371,7 +377,7 @@ __global__ __launch_bounds__(kRowsThreads, rows_waves(D, MT)) void k_rows(Attend
     if (__any(any_odd)) {
         // the infinities and NaN that were left out, for the rows that see them
 #pragma unroll 1
-        for (u = u0 + 2 * wave, step = 0; u < u1; u += 8, step = (step + 1) & 31u) {
+        for (u = u0 + 2 * wave, step = 0; u < u1; u += kPieces, step = (step + 1) & 31u) {
             if (step == 0) settle(u);
 #pragma unroll 1
             for (uint32_t e = 0; e < 32; ++e) {
@@ -397,7 +403,7 @@ __global__ __launch_bounds__(kRowsThreads, rows_waves(D, MT)) void k_rows(Attend
         }
     }
 
-    // join the four waves, 16 rows at a time
+    // join the waves, 16 rows at a time
     const float vs = g.c.v_scale ? g.c.v_scale[h] : 1.0f;
     const uint64_t slot = ((uint64_t)piece_slot * g.c.heads + h) * ROWS;
 #pragma unroll
@@ -418,17 +424,17 @@ __global__ __launch_bounds__(kRowsThreads, rows_waves(D, MT)) void k_rows(Attend
                 for (int j = 0; j < VW; j += 4)
                     *reinterpret_cast<f4 *>(dst + n * 16 * VW + (4 * lq + i) * VW + j) = f4{o[t][n][j][i], o[t][n][j + 1][i], o[t][n][j + 2][i], o[t][n][j + 3][i]};
         __syncthreads();
-        for (uint32_t e = threadIdx.x; e < 16 * (D / 8); e += kRowsThreads) {
+        for (uint32_t e = threadIdx.x; e < 16 * (D / 8); e += 64 * NW) {
             const uint32_t r = e / (D / 8), ch = (e % (D / 8)) * 8;
             const uint32_t row = t * 16 + r;
             if (row >= nrows) continue;
             float mm = -kInf;
 #pragma unroll
-            for (int w = 0; w < 4; ++w) mm = fmaxf(mm, mls[0][w][r]);
+            for (int w = 0; w < NW; ++w) mm = fmaxf(mm, mls[0][w][r]);
             const float base = mm == -kInf ? 0.0f : mm;
             float ll = 0.0f, x[8] = {};
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
+            for (int w = 0; w < NW; ++w) {
                 const float f = __builtin_amdgcn_exp2f(mls[0][w][r] - base);
                 ll += mls[1][w][r] * f;
                 const float *src = ods + (w * 16 + r) * OS + ch;
@@ -463,11 +469,16 @@ struct Plan {
     bool rows, chunk;                // which kernels run
     AttendArgs r, c;                 // their arguments: how sequences are split
     uint32_t mt, rows_items, rows_join, rows_max;   // rows_join: row tiles that may be split (0: none)
+    bool wide;                       // k_rows with eight waves, and nothing split
     ChunkPlan cp;
     uint64_t rows_part, rows_stat, chunk_part, chunk_stat, bytes;   // offsets into the workspace
 };
 
 constexpr uint32_t kFewRows = 64;    // rows of a sequence that k_rows takes
+// Up to so many tokens eight waves of one workgroup read them all: half as many steps as four waves
+// have, and no second kernel to join pieces (1000 tokens, one sequence of 8 K/V heads: 9 us of the GPU
+// instead of 12, and one launch instead of two).
+constexpr uint32_t kWideTokens = 1536;
 // Workgroups of k_rows that the card holds at a time.
 constexpr uint32_t rows_groups(uint32_t d, uint32_t mt) { return 256u * (uint32_t)rows_waves((int)d, (int)mt); }
 
@@ -490,8 +501,9 @@ Plan make_plan(const zx_paged_cache *c, const zx_paged_batch *b, uint32_t n, uin
         p.rows = true;
         p.mt = 1;
         const uint32_t tiles = n * ceil_div(G, 16), steps = ceil_div((uint64_t)n_blocks * c->block_tokens, kStep);
-        uint32_t s = ceil_div(rows_groups(D, 1), (uint64_t)tiles * H);
-        p.r.pieces = s > steps ? steps : s;
+        const uint32_t s = ceil_div(rows_groups(D, 1), (uint64_t)tiles * H);
+        p.wide = D <= 128 && s > 1 && (uint64_t)n_blocks * c->block_tokens <= kWideTokens;
+        p.r.pieces = p.wide ? 1 : s > steps ? steps : s;
         p.rows_items = tiles * p.r.pieces;
         p.rows_max = G < 16 ? G : 16;
         if (p.r.pieces > 1) {
@@ -505,6 +517,8 @@ Plan make_plan(const zx_paged_cache *c, const zx_paged_batch *b, uint32_t n, uin
             p.mt = D == 64 && most > 32 ? 3 : D <= 128 && most > 16 ? 2 : 1;
             const uint32_t R = 16 * p.mt, tiles = p.chunk ? seqs * ceil_div(kFewRows, R) : bound_tiles(n, seqs, G, R);
             plan_split(tiles, ceil_div(rows_groups(D, p.mt), H), 2, 1, 1, cap, kStep, p.r);
+            p.wide = D <= 128 && p.mt <= 2 && p.r.one_round && p.r.slots && cap <= kWideTokens;
+            if (p.wide) p.r.slots = 0;
             rows_slots = p.r.slots;
             p.rows_items = split_items(tiles, p.r);
             p.rows_join = split_tiles(tiles, p.r);
@@ -531,6 +545,19 @@ Plan make_plan(const zx_paged_cache *c, const zx_paged_batch *b, uint32_t n, uin
     return p;
 }
 
+template <int DT, int D, int MT, bool LIST, int UNIT>
+void launch_rows(const Plan &p, const AttendArgs &a, dim3 grid, dim3 jgrid, hipStream_t stream)
+{
+    if constexpr (D <= 128 && MT <= 2) {
+        if (p.wide) {
+            hipLaunchKernelGGL((k_rows<DT, D, MT, LIST, 8>), grid, dim3(512), 0, stream, a);
+            return;
+        }
+    }
+    hipLaunchKernelGGL((k_rows<DT, D, MT, LIST, 4>), grid, dim3(256), 0, stream, a);
+    if (p.rows_join) hipLaunchKernelGGL((k_join<D, 16 * MT, UNIT>), jgrid, dim3(256), 0, stream, a);
+}
+
 template <int DT, int D>
 void run_plan(Plan &p, uint32_t n_blocks, uint8_t *ws, hipStream_t stream)
 {
@@ -538,21 +565,15 @@ void run_plan(Plan &p, uint32_t n_blocks, uint8_t *ws, hipStream_t stream)
         AttendArgs &a = p.r;
         a.part = reinterpret_cast<float *>(ws + p.rows_part);
         a.stat = reinterpret_cast<float *>(ws + p.rows_stat);
-        const dim3 grid(p.rows_items * a.c.heads), block(kRowsThreads), jgrid(p.rows_join * a.c.heads, 1, join_depth(p.rows_join * a.c.heads, p.rows_max));
+        const dim3 grid(p.rows_items * a.c.heads), jgrid(p.rows_join * a.c.heads, 1, join_depth(p.rows_join * a.c.heads, p.rows_max));
         if (n_blocks) {
-            hipLaunchKernelGGL((k_rows<DT, D, 1, true>), grid, block, 0, stream, a);
-            if (p.rows_join) hipLaunchKernelGGL((k_join<D, 16, 0>), jgrid, dim3(256), 0, stream, a);
+            launch_rows<DT, D, 1, true, 0>(p, a, grid, jgrid, stream);
         } else if (p.mt == 1) {
-            hipLaunchKernelGGL((k_rows<DT, D, 1, false>), grid, block, 0, stream, a);
-            if (p.rows_join) hipLaunchKernelGGL((k_join<D, 16, (int)kStep>), jgrid, dim3(256), 0, stream, a);
+            launch_rows<DT, D, 1, false, (int)kStep>(p, a, grid, jgrid, stream);
         } else if (p.mt == 2) {
-            if constexpr (D <= 128) {
-                hipLaunchKernelGGL((k_rows<DT, D, 2, false>), grid, block, 0, stream, a);
-                if (p.rows_join) hipLaunchKernelGGL((k_join<D, 32, (int)kStep>), jgrid, dim3(256), 0, stream, a);
-            }
+            if constexpr (D <= 128) launch_rows<DT, D, 2, false, (int)kStep>(p, a, grid, jgrid, stream);
         } else if constexpr (D == 64) {
-            hipLaunchKernelGGL((k_rows<DT, D, 3, false>), grid, block, 0, stream, a);
-            if (p.rows_join) hipLaunchKernelGGL((k_join<D, 48, (int)kStep>), jgrid, dim3(256), 0, stream, a);
+            launch_rows<DT, D, 3, false, (int)kStep>(p, a, grid, jgrid, stream);
         }
     }
     if (p.chunk) {

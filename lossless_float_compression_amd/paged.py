@@ -87,11 +87,11 @@ def _device_of(device) -> torch.device:
     return d
 
 
-def _int32(t, name: str, dev=None) -> torch.Tensor:
-    if not torch.is_tensor(t) or t.dtype != torch.int32 or not t.is_cuda or not t.is_contiguous():
+def _int32(t, name: str, index: Optional[int] = None) -> torch.Tensor:
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous device int32 tensor")
-    if dev is not None and t.device != dev:
-        raise ValueError(f"{name} is on {t.device}, the cache on {dev}")
+    if index is not None and t.get_device() != index:
+        raise ValueError(f"{name} is on {t.device}, the cache on cuda:{index}")
     return t
 
 
@@ -187,6 +187,7 @@ class PagedBatch:
         self.n_seqs = n
         self.device = q_start.device
         self._index = q_start.get_device()
+        self._needs = {}                 # workspace sizes, by the sizes that decide them
         self._c = zx_paged_batch(n, page_table.shape[1], _ANY if max_q is None else min(int(max_q), _ANY),
                                  _ANY if max_kv is None else min(int(max_kv), _ANY), q_start.data_ptr(),
                                  kv_len.data_ptr(), page_table.data_ptr())
@@ -256,6 +257,7 @@ class PagedKVCache:
         self.bounds = bounds
         ptr = lambda t: None if t is None else t.data_ptr()   # noqa: E731
         self._index = self.device.index
+        self._key = (self.kv_heads, self.head_dim, self.page_tokens, self.block_tokens)
         self._c = zx_paged_cache(self.dtype, self.n_pages, self.kv_heads, self.head_dim, self.page_tokens,
                                  self.block_tokens or 0, k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2),
                                  v.stride(0), v.stride(1), v.stride(2), ptr(self.k_scale), ptr(self.v_scale),
@@ -301,7 +303,7 @@ class PagedKVCache:
         if batch._index != self._index:
             raise ValueError(f"the batch is on {batch.device}, the cache on {self.device}")
         if err is not None:
-            return _int32(err, "err", self.device).data_ptr()
+            return _int32(err, "err", self._index).data_ptr()
         return None
 
     def _group(self, q: torch.Tensor) -> None:
@@ -377,7 +379,7 @@ class PagedKVCache:
             cr = rotary._ref
         cp = None
         if positions is not None:
-            if rotary is None or _int32(positions, "positions", self.device).shape != (n,):
+            if rotary is None or _int32(positions, "positions", self._index).shape != (n,):
                 raise ValueError("positions must be [tokens], and need a rotary")
             cp = positions.data_ptr()
         st = _lib().zx_paged_append(self._ref, batch._ref, n, C.byref(ck), C.byref(cv), cr, cp, cq, heads, co, e,
@@ -419,14 +421,14 @@ class PagedKVCache:
             raise ValueError("window must be 0 (none) or a number of tokens")
         pl = pb = None
         if lse is not None:
-            if lse.dtype != torch.float32 or lse.shape != (n, heads) or lse.device != self.device or not lse.is_contiguous():
+            if lse.dtype is not torch.float32 or lse.shape != (n, heads) or lse.get_device() != self._index or not lse.is_contiguous():
                 raise ValueError("lse must be a contiguous float32 device tensor [tokens, heads]")
             pl = lse.data_ptr()
         nb = 0
         if blocks is not None:
             if self.block_tokens is None or not causal or window:
                 raise ValueError("blocks need a cache with block_tokens, causal attention and no window")
-            _int32(blocks, "blocks", self.device)
+            _int32(blocks, "blocks", self._index)
             if blocks.dim() != 3 or blocks.shape[0] != n or blocks.shape[1] != self.kv_heads or not 0 < blocks.shape[2] <= 65536:
                 raise ValueError(f"blocks must be [tokens, {self.kv_heads}, n]")
             nb = blocks.shape[2]
@@ -434,7 +436,9 @@ class PagedKVCache:
         if n == 0:
             return out
         L = _lib()
-        need = L.zx_paged_attend_workspace_bytes(self._ref, batch._ref, n, heads, nb)
+        need = batch._needs.get((self._key, n, heads, nb))
+        if need is None:
+            need = batch._needs[(self._key, n, heads, nb)] = L.zx_paged_attend_workspace_bytes(self._ref, batch._ref, n, heads, nb)
         pw = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
         st = L.zx_paged_attend(self._ref, batch._ref, n, C.byref(cq), heads, C.byref(co), pl, scale, causal, window, pb, nb,
                                None if pw is None else pw.data_ptr(), need, e, self._raw(stream))
@@ -463,13 +467,15 @@ class PagedKVCache:
             raise ValueError("top_k must be 1..1024 and at least keep_first + keep_last")
         if blocks is None:
             blocks = torch.full((n, self.kv_heads, top_k), -1, dtype=torch.int32, device=self.device)
-        _int32(blocks, "blocks", self.device)
+        _int32(blocks, "blocks", self._index)
         if blocks.shape != (n, self.kv_heads, top_k):
             raise ValueError(f"blocks must be [{n}, {self.kv_heads}, {top_k}]")
         if n == 0:
             return blocks
         L = _lib()
-        need = L.zx_paged_select_workspace_bytes(self._ref, batch._ref, n)
+        need = batch._needs.get((self._key, n))
+        if need is None:
+            need = batch._needs[(self._key, n)] = L.zx_paged_select_workspace_bytes(self._ref, batch._ref, n)
         pw = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
         st = L.zx_paged_select(self._ref, batch._ref, n, C.byref(cq), heads, top_k, keep_first, keep_last, blocks.data_ptr(),
                                None if pw is None else pw.data_ptr(), need, e, self._raw(stream))
@@ -490,7 +496,7 @@ class PagedKVCache:
             raise TypeError("the pool has another dtype than the cache")
         if not torch.is_tensor(pages) or pages.dtype not in (torch.int32, torch.int64) or pages.dim() != 1 or pages.device != self.device:
             raise ValueError("pages must be a device integer tensor [n]")
-        _int32(slots, "slots", self.device)
+        _int32(slots, "slots", self._index)
         bpp = self.blocks_per_page()
         if slots.shape != (2, pages.numel(), bpp):
             raise ValueError(f"slots must be [2, {pages.numel()}, {bpp}]: keys, then values")

@@ -107,6 +107,8 @@ def test_attend_refusals(lib):
     assert attend(c=cb, blocks=P(0x9000), nb=4, window=5) == INVAL
     assert attend(c=cb, blocks=P(0x9000), nb=65537) == INVAL
     assert attend(n=1 << 23) == INVAL
+    assert lib.zx_paged_attend_workspace_bytes(C.byref(c), C.byref(b), 7, 8, 0) == 0      # at most 320 tokens: nothing is split
+    b = batch(table_width=500)
     need = lib.zx_paged_attend_workspace_bytes(C.byref(c), C.byref(b), 7, 8, 0)
     assert need > 0
     assert attend() == INVAL                                          # no workspace
