@@ -475,10 +475,13 @@ struct Plan {
 };
 
 constexpr uint32_t kFewRows = 64;    // rows of a sequence that k_rows takes
-// Up to so many tokens eight waves of one workgroup read them all: half as many steps as four waves
-// have, and no second kernel to join pieces (1000 tokens, one sequence of 8 K/V heads: 9 us of the GPU
-// instead of 12, and one launch instead of two).
-constexpr uint32_t kWideTokens = 1536;
+// Up to so many bytes of keys and values one workgroup of eight waves reads them all, and there
+// is no second launch to join pieces.  A CU draws about 57 bytes a nanosecond, so with few
+// row tiles pieces on several CUs are read sooner, but the second launch takes that back:
+// one token over 1000, 8 K/V heads, BF16: 14.1 us a call like this, 13.9 in pieces; over 16
+// selected blocks of 64: 24.5 with the selection, 27 in pieces; 123 tokens, 2 K/V heads, over 40
+// blocks of 32, E4M3: 43 and 52.
+constexpr uint64_t kWideBytes = 512 << 10;
 // Workgroups of k_rows that the card holds at a time.
 constexpr uint32_t rows_groups(uint32_t d, uint32_t mt) { return 256u * (uint32_t)rows_waves((int)d, (int)mt); }
 
@@ -486,7 +489,7 @@ Plan make_plan(const zx_paged_cache *c, const zx_paged_batch *b, uint32_t n, uin
 {
     Plan p{};
     p.r = p.c = g;
-    const uint32_t G = q_heads / c->kv_heads, H = c->kv_heads, D = c->head_dim;
+    const uint32_t G = q_heads / c->kv_heads, H = c->kv_heads, D = c->head_dim, es = c->dtype == ZX_BF16 ? 2 : 1;
     const uint64_t room = (uint64_t)b->table_width * c->page_tokens, cap = b->max_kv < room ? b->max_kv : room;
     const uint32_t max_q = b->max_q < n ? b->max_q : n;
     const uint32_t seqs = b->n_seqs < n ? b->n_seqs : n;      // sequences with new tokens
@@ -502,7 +505,7 @@ Plan make_plan(const zx_paged_cache *c, const zx_paged_batch *b, uint32_t n, uin
         p.mt = 1;
         const uint32_t tiles = n * ceil_div(G, 16), steps = ceil_div((uint64_t)n_blocks * c->block_tokens, kStep);
         const uint32_t s = ceil_div(rows_groups(D, 1), (uint64_t)tiles * H);
-        p.wide = D <= 128 && s > 1 && (uint64_t)n_blocks * c->block_tokens <= kWideTokens;
+        p.wide = D <= 128 && s > 1 && 2 * (uint64_t)n_blocks * c->block_tokens * D * es <= kWideBytes;
         p.r.pieces = p.wide ? 1 : s > steps ? steps : s;
         p.rows_items = tiles * p.r.pieces;
         p.rows_max = G < 16 ? G : 16;
@@ -517,7 +520,7 @@ Plan make_plan(const zx_paged_cache *c, const zx_paged_batch *b, uint32_t n, uin
             p.mt = D == 64 && most > 32 ? 3 : D <= 128 && most > 16 ? 2 : 1;
             const uint32_t R = 16 * p.mt, tiles = p.chunk ? seqs * ceil_div(kFewRows, R) : bound_tiles(n, seqs, G, R);
             plan_split(tiles, ceil_div(rows_groups(D, p.mt), H), 2, 1, 1, cap, kStep, p.r);
-            p.wide = D <= 128 && p.mt <= 2 && p.r.one_round && p.r.slots && cap <= kWideTokens;
+            p.wide = D <= 128 && p.mt <= 2 && p.r.one_round && p.r.slots && 2 * cap * D * es <= kWideBytes;
             if (p.wide) p.r.slots = 0;
             rows_slots = p.r.slots;
             p.rows_items = split_items(tiles, p.r);
