@@ -454,7 +454,7 @@ zx_status zx_paged_append(const zx_paged_cache *cache, const zx_paged_batch *bat
  * Scores, the softmax's sums and the output are accumulated in 32 bits; weights are
  * rounded to BF16 before they meet the values.  Equal inputs give equal bits. */
 size_t zx_paged_attend_workspace_bytes(const zx_paged_cache *cache, const zx_paged_batch *batch,
-                                       uint32_t n_tokens, uint32_t q_heads, uint32_t n_blocks);
+                                       uint32_t n_tokens, uint32_t q_heads, uint32_t window, uint32_t n_blocks);
 zx_status zx_paged_attend(const zx_paged_cache *cache, const zx_paged_batch *batch, uint32_t n_tokens,
                           const zx_rows *q, uint32_t q_heads, const zx_rows *out, float *lse, float scale,
                           int causal, uint32_t window, const int32_t *blocks, uint32_t n_blocks, void *workspace,

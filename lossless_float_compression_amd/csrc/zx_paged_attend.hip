@@ -490,8 +490,10 @@ Plan make_plan(const zx_paged_cache *c, const zx_paged_batch *b, uint32_t n, uin
     Plan p{};
     p.r = p.c = g;
     const uint32_t G = q_heads / c->kv_heads, H = c->kv_heads, D = c->head_dim, es = c->dtype == ZX_BF16 ? 2 : 1;
-    const uint64_t room = (uint64_t)b->table_width * c->page_tokens, cap = b->max_kv < room ? b->max_kv : room;
+    const uint64_t room = (uint64_t)b->table_width * c->page_tokens, all = b->max_kv < room ? b->max_kv : room;
     const uint32_t max_q = b->max_q < n ? b->max_q : n;
+    // tokens that the rows of one sequence can see
+    const uint64_t near = (uint64_t)g.window + max_q + 15, cap = g.window && near < all ? near : all;
     const uint32_t seqs = b->n_seqs < n ? b->n_seqs : n;      // sequences with new tokens
     const uint64_t most = (uint64_t)max_q * G < 1 ? 1 : (uint64_t)max_q * G;
     auto area = [&](uint64_t bytes) {
@@ -515,7 +517,11 @@ Plan make_plan(const zx_paged_cache *c, const zx_paged_batch *b, uint32_t n, uin
         }
     } else {
         p.chunk = most > kFewRows;
-        p.rows = !p.chunk || seqs > 1;       // a batch may mix single tokens with long chunks
+        // A batch may mix single tokens with long chunks.  k_chunk can serve both; k_rows and its join read the
+        // single tokens' caches faster but cost two launches.  Us without / with them, 8 heads of 128 channels: 4 sequences
+        // of up to 100 new tokens over 1000 29 / 32, over 4000 39 / 46; 512 new beside 16 single tokens over 2000 60 / 91,
+        // but beside 64 of them 193 / 174, and beside 16 over 16000 449 / 352.
+        p.rows = !p.chunk || (seqs > 1 && (cap > 4096 || (uint64_t)seqs * H > 256));
         if (p.rows) {
             p.mt = D == 64 && most > 32 ? 3 : D <= 128 && most > 16 ? 2 : 1;
             const uint32_t R = 16 * p.mt, tiles = p.chunk ? seqs * ceil_div(kFewRows, R) : bound_tiles(n, seqs, G, R);
@@ -587,14 +593,15 @@ void run_plan(Plan &p, uint32_t n_blocks, uint8_t *ws, hipStream_t stream)
     }
 }
 
-zx_status checks(const zx_paged_cache *cache, const zx_paged_batch *batch, uint32_t n_tokens, uint32_t q_heads, uint32_t n_blocks, uint32_t *err,
-                 AttendArgs &g)
+zx_status checks(const zx_paged_cache *cache, const zx_paged_batch *batch, uint32_t n_tokens, uint32_t q_heads, uint32_t n_blocks, uint32_t window,
+                 uint32_t *err, AttendArgs &g)
 {
     zx_status st = make_cache(cache, g.c);
     if (st == ZX_OK) st = make_batch(batch, cache, n_tokens, err, g.b);
     if (st != ZX_OK) return st;
     if (q_heads == 0 || q_heads % cache->kv_heads || q_heads > 65536 || n_blocks > 65536) return ZX_E_INVAL;
     if (n_blocks && !cache->block_tokens) return ZX_E_INVAL;
+    g.window = (int32_t)window;
     const uint64_t work = (uint64_t)n_tokens * q_heads;
     if (work > 0x3FFFFFFFull) return ZX_E_LIMIT;
     // the kernels count steps and pieces in 32 bits
@@ -607,10 +614,10 @@ zx_status checks(const zx_paged_cache *cache, const zx_paged_batch *batch, uint3
 }  // namespace zxp
 
 extern "C" size_t zx_paged_attend_workspace_bytes(const zx_paged_cache *cache, const zx_paged_batch *batch, uint32_t n_tokens,
-                                                  uint32_t q_heads, uint32_t n_blocks)
+                                                  uint32_t q_heads, uint32_t window, uint32_t n_blocks)
 {
     zxp::AttendArgs g{};
-    if (zxp::checks(cache, batch, n_tokens, q_heads, n_blocks, nullptr, g) != ZX_OK || n_tokens == 0 || batch->n_seqs == 0) return 0;
+    if (window > 0x3FFFFFFFu || zxp::checks(cache, batch, n_tokens, q_heads, n_blocks, window, nullptr, g) != ZX_OK || n_tokens == 0 || batch->n_seqs == 0) return 0;
     return (size_t)zxp::make_plan(cache, batch, n_tokens, q_heads, n_blocks, g).bytes;
 }
 
@@ -622,9 +629,10 @@ extern "C" zx_status zx_paged_attend(const zx_paged_cache *cache, const zx_paged
     using namespace zxp;
     AttendArgs g{};
     if ((blocks == nullptr) != (n_blocks == 0)) return ZX_E_INVAL;
-    zx_status st = checks(cache, batch, n_tokens, q_heads, n_blocks, err, g);
+    if (window > 0x3FFFFFFFu) return ZX_E_INVAL;
+    zx_status st = checks(cache, batch, n_tokens, q_heads, n_blocks, window, err, g);
     if (st != ZX_OK) return st;
-    if (!(scale > 0.0f) || scale > 1e30f || window > 0x3FFFFFFFu || (blocks && (!causal || window))) return ZX_E_INVAL;
+    if (!(scale > 0.0f) || scale > 1e30f || (blocks && (!causal || window))) return ZX_E_INVAL;
     if (n_tokens == 0 || batch->n_seqs == 0) return ZX_OK;
     if ((st = make_rows(q, g.q)) != ZX_OK || (st = make_rows(out, g.out)) != ZX_OK) return st;
     g.lse = lse;
@@ -632,7 +640,6 @@ extern "C" zx_status zx_paged_attend(const zx_paged_cache *cache, const zx_paged
     g.n_blocks = n_blocks;
     g.scale = scale * kLog2e;
     g.causal = causal;
-    g.window = (int32_t)window;
     g.group = q_heads / cache->kv_heads;
     g.q_heads = q_heads;
     Plan p = make_plan(cache, batch, n_tokens, q_heads, n_blocks, g);

@@ -450,7 +450,10 @@ ChunkPlan plan_chunk(uint64_t rows, uint32_t head_dim, uint32_t heads, uint64_t 
 {
     ChunkPlan p{};
     const uint32_t wide = bound_tiles(tokens, seqs, group, 256);
-    p.waves = head_dim == 256 || rows <= 128 || (uint64_t)wide * heads <= 0 ? 4 : 8;
+    // Eight waves of 32 rows read a tile of keys half as often as four, four leave fewer CUs idle.  With 8 K/V heads of 128
+    // channels and 4 heads on each, us at four / eight waves: 512 new tokens 23 / 26, 1024 37 / 40, 2048 68 / 71, 3 x 200 over
+    // 3000 72 / 83, but 4096 181 / 169, 2 x 300 over 8000 127 / 117.  (Eight waves of 256 channels do not fit the registers.)
+    p.waves = head_dim == 256 || rows <= 128 || ((uint64_t)wide * heads <= 256 && cap <= 4096) ? 4 : 8;
     p.tiles = p.waves == 8 ? wide : bound_tiles(tokens, seqs, group, 128);
     plan_split(p.tiles, ceil_div(p.waves == 8 || head_dim == 256 ? 256 : 512, heads), kChunkRounds, 8, 64, cap, kTile, g);
     return p;

@@ -9,8 +9,11 @@
 // adding up in 32 bits would now and then say differently for blocks next to the border,
 // so the sums are taken in 64 bits (the vector units' 64-bit multiply-add has the rate of the 32-bit one).
 //
-//   k_score  one key (the sum, as an integer that orders like it) per token, head and block
-//   k_top    the top_k-th largest key by radix selection, then the taken blocks in ascending order
+//   k_pick   one workgroup for a token and K/V head: a key (the sum, as an integer that orders like it)
+//            for each block, in LDS, then the top_k-th largest by radix selection and the
+//            taken blocks in ascending order
+//   k_score, k_top  the same in two steps, with the keys in memory: for more blocks than LDS holds, or
+//            few tokens and so many blocks that one CU alone would read too long
 #include "zx_paged.h"
 
 namespace zxp {
@@ -63,65 +66,49 @@ __device__ __forceinline__ double sum_lanes(double x)
     return x;
 }
 
-// Tokens of a sequence come in groups of TT that share what is read of the bounds.  A lane
-// has eight channels of a block's two bounds; kUnroll blocks are in flight for it at a time.
-template <int D, int TT>
-__global__ __launch_bounds__(kThreads) void k_score(SelectArgs g)
-{
-    constexpr uint32_t LB = D / 8;                       // lanes of a block
-    constexpr uint32_t PB = kThreads / LB;               // blocks at a time
-    constexpr int kUnroll = 4;
-    const uint32_t h = blockIdx.x % g.c.heads, grp = blockIdx.x / g.c.heads;
-    uint32_t seq, local, unused;
-    Seq sv;
-    if (!find_item(g.b, g.slab0 + grp, [](const Seq &v) { return div_up((uint32_t)v.nq, TT); }, [](const Seq &) { return 0u; }, seq, sv, local, unused)) return;
-    const uint32_t tok = local * TT, nt = (uint32_t)sv.nq - tok < (uint32_t)TT ? (uint32_t)sv.nq - tok : (uint32_t)TT;
-    const int32_t p9 = sv.kv - sv.nq + (int32_t)(tok + nt - 1);      // position of the last token
-    if (p9 < 0) return;
-    const uint32_t lb = g.c.log_block, seen = ((uint32_t)p9 >> lb) + 1;
-    if (seen <= g.top_k) return;                                     // every block is taken
-    const uint32_t j0 = blockIdx.y * g.per, j1 = j0 + g.per < seen ? j0 + g.per : seen;
-    if (j0 >= j1) return;
-
-    const uint32_t ln = threadIdx.x % LB, slot = threadIdx.x / LB;
-    const int32_t *table = g.b.table + (uint64_t)seq * g.b.width;
-    const uint32_t lp = g.c.log_page - lb, nbp = 1u << lp;
+// The bounds of kUnroll blocks j, j + STEP, ..: eight channels of each for a lane (blocks past j1 - 1 repeat it).
+constexpr int kUnroll = 4;
+struct Fetched {
     bf8 lo[kUnroll], hi[kUnroll];
-    uint32_t none = 0;                                               // blocks of these that have no page
-    auto fetch = [&](uint32_t j) {
-        uint32_t page[kUnroll];
+    uint32_t none;                                       // blocks of these that have no page
+};
+template <int D, uint32_t STEP>
+__device__ __forceinline__ void fetch(const SelectArgs &g, const int32_t *table, uint32_t h, uint32_t j, uint32_t j1, uint32_t ln, Fetched &f)
+{
+    const uint32_t lp = g.c.log_page - g.c.log_block, nbp = 1u << lp;
+    uint32_t page[kUnroll];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const uint32_t ju = j + u * PB < j1 ? j + u * PB : j1 - 1;
-            page[u] = (uint32_t)table[ju >> lp];
-        }
-        none = 0;
+    for (int u = 0; u < kUnroll; ++u) page[u] = (uint32_t)table[(j + u * STEP < j1 ? j + u * STEP : j1 - 1) >> lp];
+    f.none = 0;
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-            const uint32_t ju = j + u * PB < j1 ? j + u * PB : j1 - 1;
-            if (page[u] >= g.c.n_pages) {
-                report(g.b.err, ZX_E_CORRUPT);
-                page[u] = 0;
-                none |= 1u << u;
-            }
-            const __bf16 *bp = g.c.bounds + (((uint64_t)page[u] * g.c.heads + h) * nbp + (ju & (nbp - 1u))) * (2 * D) + 8 * ln;
-            lo[u] = *reinterpret_cast<const bf8 *>(bp);
-            hi[u] = *reinterpret_cast<const bf8 *>(bp + D);
+    for (int u = 0; u < kUnroll; ++u) {
+        const uint32_t ju = j + u * STEP < j1 ? j + u * STEP : j1 - 1;
+        if (page[u] >= g.c.n_pages) {
+            report(g.b.err, ZX_E_CORRUPT);
+            page[u] = 0;
+            f.none |= 1u << u;
         }
-    };
-    fetch(j0 + slot);                                                // under way while the queries are added up
-    double up[TT][8], dn[TT][8];
+        const __bf16 *bp = g.c.bounds + (((uint64_t)page[u] * g.c.heads + h) * nbp + (ju & (nbp - 1u))) * (2 * D) + 8 * ln;
+        f.lo[u] = *reinterpret_cast<const bf8 *>(bp);
+        f.hi[u] = *reinterpret_cast<const bf8 *>(bp + D);
+    }
+}
+
+// Sums over the group's heads of the positive and of the negative parts of eight channels, for TT tokens
+// from packed row `row` on (those past nt repeat the last).  A NaN stays one in both sums.
+template <int TT>
+__device__ __forceinline__ void group_sums(const SelectArgs &g, int64_t row, uint32_t nt, uint32_t h, uint32_t ln, double (&up)[TT][8], double (&dn)[TT][8])
+{
+    constexpr int kQ = TT == 1 ? 4 : 2;                  // heads read at a time, for each token
 #pragma unroll
     for (int t = 0; t < TT; ++t)
 #pragma unroll
         for (int i = 0; i < 8; ++i) up[t][i] = dn[t][i] = 0.0;
-    constexpr int kQ = TT == 1 ? 4 : 2;                              // heads read at a time, for each token
     for (uint32_t e = 0; e < g.group; e += kQ) {
         bf8 x[TT][kQ];
 #pragma unroll
         for (int t = 0; t < TT; ++t) {
-            const uint32_t tt = tok + ((uint32_t)t < nt ? (uint32_t)t : nt - 1);
-            const __bf16 *qp = g.q.p + (int64_t)(sv.q0 + (int32_t)tt) * g.q.token + (int64_t)(h * g.group) * g.q.head + 8 * ln;
+            const __bf16 *qp = g.q.p + (row + ((uint32_t)t < nt ? (uint32_t)t : nt - 1)) * g.q.token + (int64_t)(h * g.group) * g.q.head + 8 * ln;
 #pragma unroll
             for (int k = 0; k < kQ; ++k) x[t][k] = *reinterpret_cast<const bf8 *>(qp + (int64_t)(e + k < g.group ? e + k : e) * g.q.head);
         }
@@ -132,91 +119,93 @@ __global__ __launch_bounds__(kThreads) void k_score(SelectArgs g)
 #pragma unroll
                 for (int i = 0; i < 8; ++i) {
                     const float y = e + k < g.group ? (float)x[t][k][i] : 0.0f;
-                    // a NaN stays one in both sums
                     up[t][i] += (double)(y < 0.0f ? 0.0f : y);
                     dn[t][i] += (double)(y > 0.0f ? 0.0f : y);
                 }
     }
+}
+
+// Block u of those fetched, for one token: the sum over all lanes of the block, in all of them.
+template <int LB>
+__device__ __forceinline__ double block_sum(const Fetched &f, int u, const double (&up)[8], const double (&dn)[8])
+{
+    double s = 0.0;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) s = __builtin_fma(up[i], (double)(float)f.hi[u][i], __builtin_fma(dn[i], (double)(float)f.lo[u][i], s));
+    return sum_lanes<LB>(s);
+}
+
+// Tokens of a sequence come in groups of TT that share what is read of the bounds.
+template <int D, int TT>
+__global__ __launch_bounds__(kThreads) void k_score(SelectArgs g)
+{
+    constexpr uint32_t LB = D / 8;                       // lanes of a block
+    constexpr uint32_t PB = kThreads / LB;               // blocks at a time
+    const uint32_t h = blockIdx.x % g.c.heads, grp = blockIdx.x / g.c.heads;
+    uint32_t seq, local, unused;
+    Seq sv;
+    if (!find_item(g.b, g.slab0 + grp, [](const Seq &v) { return div_up((uint32_t)v.nq, TT); }, [](const Seq &) { return 0u; }, seq, sv, local, unused)) return;
+    const uint32_t tok = local * TT, nt = (uint32_t)sv.nq - tok < (uint32_t)TT ? (uint32_t)sv.nq - tok : (uint32_t)TT;
+    const int32_t p9 = sv.kv - sv.nq + (int32_t)(tok + nt - 1);      // position of the last token
+    if (p9 < 0) return;
+    const uint32_t seen = ((uint32_t)p9 >> g.c.log_block) + 1;
+    if (seen <= g.top_k) return;                                     // every block is taken
+    const uint32_t j0 = blockIdx.y * g.per, j1 = j0 + g.per < seen ? j0 + g.per : seen;
+    if (j0 >= j1) return;
+
+    const uint32_t ln = threadIdx.x % LB, slot = threadIdx.x / LB;
+    const int32_t *table = g.b.table + (uint64_t)seq * g.b.width;
+    Fetched f;
+    fetch<D, PB>(g, table, h, j0 + slot, j1, ln, f);                 // under way while the queries are added up
+    double up[TT][8], dn[TT][8];
+    group_sums<TT>(g, sv.q0 + (int64_t)tok, nt, h, ln, up, dn);
     for (uint32_t j = j0 + slot; j < j1; j += kUnroll * PB) {
         double s[kUnroll][TT];
 #pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
+        for (int u = 0; u < kUnroll; ++u)
 #pragma unroll
-            for (int t = 0; t < TT; ++t) s[u][t] = 0.0;
+            for (int t = 0; t < TT; ++t) s[u][t] = block_sum<(int)LB>(f, u, up[t], dn[t]);
+        const uint32_t gone = f.none;
+        if (j + kUnroll * PB < j1) fetch<D, PB>(g, table, h, j + kUnroll * PB, j1, ln, f);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const double a = (double)(float)lo[u][i], b = (double)(float)hi[u][i];
-#pragma unroll
-                for (int t = 0; t < TT; ++t) s[u][t] = __builtin_fma(up[t][i], b, __builtin_fma(dn[t][i], a, s[u][t]));
-            }
-        }
-        const uint32_t gone = none;
-        if (j + kUnroll * PB < j1) fetch(j + kUnroll * PB);
-#pragma unroll
-        for (int u = 0; u < kUnroll; ++u) {
-#pragma unroll
-            for (int t = 0; t < TT; ++t) s[u][t] = sum_lanes<(int)LB>(s[u][t]);
+        for (int u = 0; u < kUnroll; ++u)
             if (ln < nt && j + u * PB < j1) {
                 double x = s[u][0];
 #pragma unroll
                 for (int t = 1; t < TT; ++t) x = ln == (uint32_t)t ? s[u][t] : x;
                 g.keys[((uint64_t)(grp * TT + ln) * g.c.heads + h) * g.nb + j + u * PB] = gone >> u & 1u ? 0 : order_key(x);
             }
-        }
     }
 }
 
-template <int TT>
-__global__ __launch_bounds__(kThreads) void k_top(SelectArgs g)
+struct Picking {
+    uint32_t hist[1 << kDigit];
+    uint64_t wide[2][8];
+    uint32_t sums[2][8];
+    uint32_t pick[3];
+};
+
+// Blocks f0 .. f0 + n - 1 compete with their keys for `want` < n places of `out`; the rest of
+// a row's top_k are the blocks in front of them and behind them.  By all NT threads.
+template <uint32_t NT, class Key>
+__device__ __forceinline__ void pick_row(const SelectArgs &g, Key key, uint32_t f0, uint32_t n, uint32_t want, uint64_t least, uint64_t most, int32_t *out, Picking &sh)
 {
-    __shared__ uint64_t held[kHeld];
-    __shared__ uint32_t hist[1 << kDigit];
-    __shared__ uint64_t wide[2][4];
-    __shared__ uint32_t pick[3];
-    __shared__ uint32_t sums[2][4];
-    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
-    const uint32_t h = blockIdx.x % g.c.heads, row = blockIdx.x / g.c.heads;
-    uint32_t seq, local, unused;
-    Seq sv;
-    if (!find_item(g.b, g.slab0 * TT + row, [](const Seq &v) { return div_up((uint32_t)v.nq, TT) * TT; }, [](const Seq &) { return 0u; }, seq, sv, local, unused))
-        return;
-    if (local >= (uint32_t)sv.nq) return;
-    const int32_t p = sv.kv - sv.nq + (int32_t)local;
-    const uint32_t seen = p < 0 ? 0u : ((uint32_t)p >> g.c.log_block) + 1;
-    const uint32_t K = g.top_k;
-    int32_t *out = g.blocks + ((uint64_t)(sv.q0 + (int32_t)local) * g.c.heads + h) * K;
-    if (seen <= K) {
-        for (uint32_t i = tid; i < K; i += kThreads) out[i] = i < seen ? (int32_t)i : -1;
-        return;
-    }
-    // blocks f0 .. f1 - 1 compete; those before and behind are taken anyway
-    const uint32_t f0 = g.keep_first, f1 = seen - g.keep_last, n = f1 - f0;
-    uint32_t want = K - g.keep_first - g.keep_last;      // of the n > want that compete
-    const uint64_t *src = g.keys + ((uint64_t)row * g.c.heads + h) * g.nb + f0;
-    const bool in_lds = n <= kHeld;
-    uint64_t least = ~0ull, most = 0;
-    for (uint32_t i = tid; i < n; i += kThreads) {
-        const uint64_t x = src[i];
-        if (in_lds) held[i] = x;
-        least = x < least ? x : least;
-        most = x > most ? x : most;
-    }
+    constexpr uint32_t NWV = NT / 64;
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6, K = g.top_k;
     for (int w = 32; w >= 1; w >>= 1) {
         const uint64_t a = __shfl_xor(least, w, 64), b = __shfl_xor(most, w, 64);
         least = a < least ? a : least;
         most = b > most ? b : most;
     }
     if (lane == 0) {
-        wide[0][wave] = least;
-        wide[1][wave] = most;
+        sh.wide[0][wave] = least;
+        sh.wide[1][wave] = most;
     }
     __syncthreads();
-    for (int w = 0; w < 4; ++w) {
-        least = wide[0][w] < least ? wide[0][w] : least;
-        most = wide[1][w] > most ? wide[1][w] : most;
+    for (uint32_t w = 0; w < NWV; ++w) {
+        least = sh.wide[0][w] < least ? sh.wide[0][w] : least;
+        most = sh.wide[1][w] > most ? sh.wide[1][w] : most;
     }
-    auto key = [&](uint32_t i) { return in_lds ? held[i] : src[i]; };
-
     // keys at or above `cut` in the bits of `mask` are taken, but of those equal to it in
     // these bits only the first `want`
     const uint64_t diff = least ^ most;
@@ -230,46 +219,46 @@ __global__ __launch_bounds__(kThreads) void k_top(SelectArgs g)
         top = 0;
     }
     while (top > 0 && same != want) {
-        const int bits = top < kDigit ? top : kDigit, sh = top - bits;
-        for (uint32_t i = tid; i < 1u << kDigit; i += kThreads) hist[i] = 0;
+        const int bits = top < kDigit ? top : kDigit, sft = top - bits;
+        for (uint32_t i = tid; i < 1u << kDigit; i += NT) sh.hist[i] = 0;
         __syncthreads();
-        for (uint32_t i = tid; i < n; i += kThreads) {
+        for (uint32_t i = tid; i < n; i += NT) {
             const uint64_t x = key(i);
-            if ((x & mask) == cut) atomicAdd(&hist[(uint32_t)(x >> sh) & ((1u << bits) - 1u)], 1u);
+            if ((x & mask) == cut) atomicAdd(&sh.hist[(uint32_t)(x >> sft) & ((1u << bits) - 1u)], 1u);
         }
         __syncthreads();
         // thread t has kEach digits, the highest first: the digit at which the count from above reaches `want`
-        constexpr uint32_t kEach = (1u << kDigit) / kThreads;
+        constexpr uint32_t kEach = (1u << kDigit) / NT;
         uint32_t c[kEach], mine = 0, total;
 #pragma unroll
         for (uint32_t i = 0; i < kEach; ++i) {
-            c[i] = hist[(1u << kDigit) - 1u - kEach * tid - i];
+            c[i] = sh.hist[(1u << kDigit) - 1u - kEach * tid - i];
             mine += c[i];
         }
         uint32_t above = wave_excl_scan(mine, total);
-        if (lane == 0) sums[0][wave] = total;
+        if (lane == 0) sh.sums[0][wave] = total;
         __syncthreads();
-        for (uint32_t w = 0; w < wave; ++w) above += sums[0][w];
+        for (uint32_t w = 0; w < wave; ++w) above += sh.sums[0][w];
 #pragma unroll
         for (uint32_t i = 0; i < kEach; ++i) {
             if (above < want && above + c[i] >= want) {
-                pick[0] = (1u << kDigit) - 1u - kEach * tid - i;
-                pick[1] = above;
-                pick[2] = c[i];
+                sh.pick[0] = (1u << kDigit) - 1u - kEach * tid - i;
+                sh.pick[1] = above;
+                sh.pick[2] = c[i];
             }
             above += c[i];
         }
         __syncthreads();
-        cut |= (uint64_t)pick[0] << sh;
-        mask |= (uint64_t)((1u << bits) - 1u) << sh;
-        want -= pick[1];
-        same = pick[2];
-        top = sh;
+        cut |= (uint64_t)sh.pick[0] << sft;
+        mask |= (uint64_t)((1u << bits) - 1u) << sft;
+        want -= sh.pick[1];
+        same = sh.pick[2];
+        top = sft;
         __syncthreads();
     }
 
     // every thread takes a run of neighbouring blocks, so that ranks come out of one scan
-    const uint32_t run = div_up(n, kThreads), i0 = tid * run < n ? tid * run : n, i1 = i0 + run < n ? i0 + run : n;
+    const uint32_t run = div_up(n, NT), i0 = tid * run < n ? tid * run : n, i1 = i0 + run < n ? i0 + run : n;
     uint32_t over = 0, equal = 0;
     for (uint32_t i = i0; i < i1; ++i) {
         const uint64_t x = key(i) & mask;
@@ -279,13 +268,13 @@ __global__ __launch_bounds__(kThreads) void k_top(SelectArgs g)
     uint32_t ta, tb;
     uint32_t ra = wave_excl_scan(over, ta), rb = wave_excl_scan(equal, tb);
     if (lane == 0) {
-        sums[0][wave] = ta;
-        sums[1][wave] = tb;
+        sh.sums[0][wave] = ta;
+        sh.sums[1][wave] = tb;
     }
     __syncthreads();
     for (uint32_t w = 0; w < wave; ++w) {
-        ra += sums[0][w];
-        rb += sums[1][w];
+        ra += sh.sums[0][w];
+        rb += sh.sums[1][w];
     }
     uint32_t at = g.keep_first + ra + (rb < want ? rb : want);
     for (uint32_t i = i0; i < i1; ++i) {
@@ -294,8 +283,88 @@ __global__ __launch_bounds__(kThreads) void k_top(SelectArgs g)
         if (x == cut) take = rb++ < want;
         if (take) out[at++] = (int32_t)(f0 + i);
     }
-    for (uint32_t i = tid; i < g.keep_first; i += kThreads) out[i] = (int32_t)i;
-    for (uint32_t i = tid; i < g.keep_last; i += kThreads) out[K - g.keep_last + i] = (int32_t)(f1 + i);
+    for (uint32_t i = tid; i < g.keep_first; i += NT) out[i] = (int32_t)i;
+    for (uint32_t i = tid; i < g.keep_last; i += NT) out[K - g.keep_last + i] = (int32_t)(f0 + n + i);
+}
+
+// Blocks that the new token `tok` of a sequence sees; its row of the result.  True where all of them
+// are taken, which is then done.
+__device__ __forceinline__ bool all_taken(const SelectArgs &g, const Seq &sv, uint32_t tok, uint32_t h, uint32_t &seen, int32_t *&out)
+{
+    const int32_t p = sv.kv - sv.nq + (int32_t)tok;
+    seen = p < 0 ? 0u : ((uint32_t)p >> g.c.log_block) + 1;
+    out = g.blocks + ((uint64_t)(sv.q0 + (int32_t)tok) * g.c.heads + h) * g.top_k;
+    if (seen > g.top_k) return false;
+    for (uint32_t i = threadIdx.x; i < g.top_k; i += blockDim.x) out[i] = i < seen ? (int32_t)i : -1;
+    return true;
+}
+
+template <int TT>
+__global__ __launch_bounds__(kThreads) void k_top(SelectArgs g)
+{
+    __shared__ uint64_t held[kHeld];
+    __shared__ Picking sh;
+    const uint32_t h = blockIdx.x % g.c.heads, row = blockIdx.x / g.c.heads;
+    uint32_t seq, local, unused, seen;
+    Seq sv;
+    int32_t *out;
+    if (!find_item(g.b, g.slab0 * TT + row, [](const Seq &v) { return div_up((uint32_t)v.nq, TT) * TT; }, [](const Seq &) { return 0u; }, seq, sv, local, unused))
+        return;
+    if (local >= (uint32_t)sv.nq || all_taken(g, sv, local, h, seen, out)) return;
+    // blocks f0 .. f0 + n - 1 compete; those before and behind are taken anyway
+    const uint32_t f0 = g.keep_first, n = seen - g.keep_last - f0;
+    const uint64_t *src = g.keys + ((uint64_t)row * g.c.heads + h) * g.nb + f0;
+    const bool in_lds = n <= kHeld;
+    uint64_t least = ~0ull, most = 0;
+    for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
+        const uint64_t x = src[i];
+        if (in_lds) held[i] = x;
+        least = x < least ? x : least;
+        most = x > most ? x : most;
+    }
+    const uint32_t want = g.top_k - g.keep_first - g.keep_last;
+    if (in_lds) pick_row<kThreads>(g, [&](uint32_t i) { return held[i]; }, f0, n, want, least, most, out, sh);
+    else pick_row<kThreads>(g, [&](uint32_t i) { return src[i]; }, f0, n, want, least, most, out, sh);
+}
+
+constexpr uint32_t kPickThreads = 512;
+
+template <int D>
+__global__ __launch_bounds__(kPickThreads) void k_pick(SelectArgs g)
+{
+    constexpr uint32_t LB = D / 8, PB = kPickThreads / LB;
+    __shared__ uint64_t held[kHeld];
+    __shared__ Picking sh;
+    const uint32_t h = blockIdx.x % g.c.heads, row = blockIdx.x / g.c.heads;
+    uint32_t seq, local, unused, seen;
+    Seq sv;
+    int32_t *out;
+    if (!find_item(g.b, row, [](const Seq &v) { return (uint32_t)v.nq; }, [](const Seq &) { return 0u; }, seq, sv, local, unused)) return;
+    if (all_taken(g, sv, local, h, seen, out)) return;
+    const uint32_t f0 = g.keep_first, f1 = seen - g.keep_last, n = f1 - f0;
+    const uint32_t ln = threadIdx.x % LB, slot = threadIdx.x / LB;
+    const int32_t *table = g.b.table + (uint64_t)seq * g.b.width;
+    uint64_t least = ~0ull, most = 0;
+    Fetched f;
+    fetch<D, PB>(g, table, h, f0 + slot, f1, ln, f);                 // under way while the queries are added up
+    double up[1][8], dn[1][8];
+    group_sums<1>(g, sv.q0 + (int64_t)local, 1, h, ln, up, dn);
+    for (uint32_t j = f0 + slot; j < f1; j += kUnroll * PB) {
+        const Fetched now = f;
+        if (j + kUnroll * PB < f1) fetch<D, PB>(g, table, h, j + kUnroll * PB, f1, ln, f);
+#pragma unroll
+        for (int u = 0; u < kUnroll; ++u) {
+            const double s = block_sum<(int)LB>(now, u, up[0], dn[0]);
+            if (j + u * PB < f1) {
+                const uint64_t x = now.none >> u & 1u ? 0 : order_key(s);
+                if (ln == 0) held[j + u * PB - f0] = x;
+                least = x < least ? x : least;
+                most = x > most ? x : most;
+            }
+        }
+    }
+    __syncthreads();
+    pick_row<kPickThreads>(g, [&](uint32_t i) { return held[i]; }, f0, n, g.top_k - g.keep_first - g.keep_last, least, most, out, sh);
 }
 
 // Tokens that share a read of the bounds: with one new token a sequence there is nothing to share.
@@ -304,6 +373,7 @@ inline uint32_t sharing(const zx_paged_batch *b, uint32_t n) { return (b->max_q 
 struct Slabs {
     uint32_t tt, groups, slab, nb;
     uint64_t bytes;
+    bool fused;                  // k_pick
 };
 
 // The keys of all tokens at once, or of as many token groups as 256 MB hold.
@@ -316,6 +386,15 @@ Slabs make_slabs(const zx_paged_cache *c, const zx_paged_batch *b, uint32_t n)
     const uint32_t seqs = b->n_seqs < n ? b->n_seqs : n;
     s.groups = s.tt == 1 ? n : n / s.tt + seqs < n ? n / s.tt + seqs : n;
     const uint64_t each = (uint64_t)s.tt * c->kv_heads * s.nb * 8;
+    // k_pick saves a launch, reads the bounds of a token and head with one CU (57 bytes a nanosecond) and
+    // shares no read between tokens.  Us of selection and attention, k_pick / both steps: one token over 8000
+    // tokens (64 KB of bounds a head) 23.6 / 24.7, over 32768 (256 KB) 28.4 / 25.1; 24 and 32 tokens of 8 heads,
+    // each of a sequence over 65536, 52 / 54 and 106 / 108.  Where four tokens share reads: 8 over 30000 29.9 / 32.1,
+    // 3 x 41 of 2 heads over 17000 32 / 43, but 40 over 60000 61 / 53 and 4 x 30 over 8000 51 / 48.
+    const uint64_t read = (uint64_t)s.nb * 4 * c->head_dim, wgs = (uint64_t)n * c->kv_heads;
+    const bool pays = s.tt == 1 ? read <= 128 << 10 || wgs >= 192 : read * (wgs < 256 ? 256 : wgs) <= 256ull * (320 << 10);
+    s.fused = s.nb <= kHeld && pays;
+    if (s.fused) return s;
     const uint64_t most = (256ull << 20) / (each ? each : 1);
     s.slab = most < 1 ? 1 : most < s.groups ? (uint32_t)most : s.groups;
     s.bytes = each * s.slab;
@@ -370,6 +449,14 @@ extern "C" zx_status zx_paged_select(const zx_paged_cache *cache, const zx_paged
     g.keep_last = keep_last;
     g.nb = s.nb;
     g.slab = s.slab;
+    if (s.fused) {
+        if ((uint64_t)n_tokens * cache->kv_heads > 0x7FFFFFFFull) return ZX_E_LIMIT;
+        const dim3 grid(n_tokens * cache->kv_heads);
+        if (cache->head_dim == 64) hipLaunchKernelGGL((k_pick<64>), grid, dim3(kPickThreads), 0, stream, g);
+        else if (cache->head_dim == 128) hipLaunchKernelGGL((k_pick<128>), grid, dim3(kPickThreads), 0, stream, g);
+        else hipLaunchKernelGGL((k_pick<256>), grid, dim3(kPickThreads), 0, stream, g);
+        return hipGetLastError() == hipSuccess ? ZX_OK : ZX_E_HIP;
+    }
     // blocks of a workgroup: few enough to fill the card, many enough to be worth its start
     const uint32_t at_once = 4 * kThreads / (cache->head_dim / 8);
     const uint64_t want = ceil_div(s.tt == 1 ? 1280 : 512, (uint64_t)s.slab * cache->kv_heads);

@@ -58,7 +58,7 @@ def _bind(L) -> None:
     P, U32, I, SZ = C.c_void_p, C.c_uint32, C.c_int, C.c_size_t
     K, B, R = C.POINTER(zx_paged_cache), C.POINTER(zx_paged_batch), C.POINTER(zx_rows)
     L.zx_paged_append.argtypes = [K, B, U32, R, R, C.POINTER(zx_rotary), P, R, U32, R, P, P]
-    L.zx_paged_attend_workspace_bytes.argtypes = [K, B, U32, U32, U32]
+    L.zx_paged_attend_workspace_bytes.argtypes = [K, B, U32, U32, U32, U32]
     L.zx_paged_attend_workspace_bytes.restype = SZ
     L.zx_paged_attend.argtypes = [K, B, U32, R, U32, R, P, C.c_float, I, U32, P, U32, P, SZ, P, P]
     L.zx_paged_select_workspace_bytes.argtypes = [K, B, U32]
@@ -257,7 +257,7 @@ class PagedKVCache:
         self.bounds = bounds
         ptr = lambda t: None if t is None else t.data_ptr()   # noqa: E731
         self._index = self.device.index
-        self._key = (self.kv_heads, self.head_dim, self.page_tokens, self.block_tokens)
+        self._key = (self.dtype, self.kv_heads, self.head_dim, self.page_tokens, self.block_tokens)
         self._c = zx_paged_cache(self.dtype, self.n_pages, self.kv_heads, self.head_dim, self.page_tokens,
                                  self.block_tokens or 0, k.data_ptr(), v.data_ptr(), k.stride(0), k.stride(1), k.stride(2),
                                  v.stride(0), v.stride(1), v.stride(2), ptr(self.k_scale), ptr(self.v_scale),
@@ -436,9 +436,10 @@ class PagedKVCache:
         if n == 0:
             return out
         L = _lib()
-        need = batch._needs.get((self._key, n, heads, nb))
+        key = (self._key, n, heads, window, nb)
+        need = batch._needs.get(key)
         if need is None:
-            need = batch._needs[(self._key, n, heads, nb)] = L.zx_paged_attend_workspace_bytes(self._ref, batch._ref, n, heads, nb)
+            need = batch._needs[key] = L.zx_paged_attend_workspace_bytes(self._ref, batch._ref, n, heads, window, nb)
         pw = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
         st = L.zx_paged_attend(self._ref, batch._ref, n, C.byref(cq), heads, C.byref(co), pl, scale, causal, window, pb, nb,
                                None if pw is None else pw.data_ptr(), need, e, self._raw(stream))

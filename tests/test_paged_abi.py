@@ -107,14 +107,14 @@ def test_attend_refusals(lib):
     assert attend(c=cb, blocks=P(0x9000), nb=4, window=5) == INVAL
     assert attend(c=cb, blocks=P(0x9000), nb=65537) == INVAL
     assert attend(n=1 << 23) == INVAL
-    assert lib.zx_paged_attend_workspace_bytes(C.byref(c), C.byref(b), 7, 8, 0) == 0      # at most 320 tokens: nothing is split
+    assert lib.zx_paged_attend_workspace_bytes(C.byref(c), C.byref(b), 7, 8, 0, 0) == 0      # at most 320 tokens: nothing is split
     b = batch(table_width=500)
-    need = lib.zx_paged_attend_workspace_bytes(C.byref(c), C.byref(b), 7, 8, 0)
+    need = lib.zx_paged_attend_workspace_bytes(C.byref(c), C.byref(b), 7, 8, 0, 0)
     assert need > 0
     assert attend() == INVAL                                          # no workspace
     assert attend(ws=P(0x100000), size=need - 1) == INVAL
     assert attend(ws=P(0x100008), size=need) == INVAL
-    assert lib.zx_paged_attend_workspace_bytes(C.byref(c), C.byref(b), 7, 3, 0) == 0
+    assert lib.zx_paged_attend_workspace_bytes(C.byref(c), C.byref(b), 7, 3, 0, 0) == 0
     # more work than 32-bit counts hold
     huge = batch(n_seqs=65536, table_width=1 << 19)
     assert lib.zx_paged_attend(C.byref(cache(page_tokens=512, k_head_stride=512 * 128, v_head_stride=512 * 128)), C.byref(huge), 65536,
@@ -133,6 +133,8 @@ def test_select_refusals(lib):
     assert select(c=cache()) == INVAL
     for kw in (dict(heads=0), dict(heads=3), dict(top=0), dict(top=1025), dict(first=4), dict(last=0xFFFFFFFF), dict(out=None)):
         assert select(**kw) == INVAL, kw
+    assert lib.zx_paged_select_workspace_bytes(C.byref(cb), C.byref(b), 7) == 0        # ten blocks: no keys in memory
+    b = batch(table_width=5000)
     need = lib.zx_paged_select_workspace_bytes(C.byref(cb), C.byref(b), 7)
     assert need > 0 and select() == INVAL and select(ws=P(0x100000), size=need - 1) == INVAL and select(ws=P(0x100001), size=need) == INVAL
     assert lib.zx_paged_select_workspace_bytes(C.byref(cache()), C.byref(b), 7) == 0
