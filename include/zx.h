@@ -452,7 +452,7 @@ zx_status zx_paged_append(const zx_paged_cache *cache, const zx_paged_batch *bat
  *   workspace  zx_paged_attend_workspace_bytes(...) bytes, 16-byte aligned; its contents
  *           do not matter before the call or after it
  * Scores, the softmax's sums and the output are accumulated in 32 bits; weights are
- * rounded to BF16 before they meet the values.  Equal inputs give equal bits. */
+ * rounded to BF16 before they meet the values.  Equal inputs give equal bits.  out may be q. */
 size_t zx_paged_attend_workspace_bytes(const zx_paged_cache *cache, const zx_paged_batch *batch,
                                        uint32_t n_tokens, uint32_t q_heads, uint32_t window, uint32_t n_blocks);
 zx_status zx_paged_attend(const zx_paged_cache *cache, const zx_paged_batch *batch, uint32_t n_tokens,

@@ -40,16 +40,15 @@ struct AttendArgs {
     uint32_t goal, one_round, least;
 };
 
-// The new tokens of a sequence see tokens from `lo` on, in all; a row at position p
-// sees [max(0, p - window + 1), p + 1) if causal, else up to kv.
+// A row at position p sees tokens [max(0, p - window + 1), p + 1) if causal, else up to kv; at a
+// negative position (fewer tokens than new ones) none.
 __device__ __forceinline__ int32_t first_seen(const AttendArgs &g, int32_t p)
 {
     return g.window > 0 && p - g.window + 1 > 0 ? p - g.window + 1 : 0;
 }
 __device__ __forceinline__ int32_t end_seen(const AttendArgs &g, int32_t p, int32_t kv)
 {
-    const int32_t e = g.causal ? p + 1 : kv;
-    return e < 0 ? 0 : e;
+    return p < 0 ? 0 : g.causal ? p + 1 : kv;
 }
 
 // Steps of UNIT tokens that cover what the sequence's rows see (at least one).
@@ -315,6 +314,8 @@ inline uint32_t join_depth(uint32_t tiles, uint32_t rows)
 struct ChunkPlan {
     uint32_t waves, tiles;           // waves of a workgroup; bound of the row tiles a head
 };
+// A launch counts its threads in 32 bits.
+inline bool launchable(uint64_t workgroups, uint32_t threads) { return workgroups * threads <= 0xFFFFFFFFull; }
 ChunkPlan plan_chunk(uint64_t rows, uint32_t head_dim, uint32_t heads, uint64_t tokens, uint64_t seqs, uint64_t group, uint64_t cap, AttendArgs &g);
 void run_chunk(int dtype, uint32_t head_dim, const ChunkPlan &p, const AttendArgs &g, hipStream_t stream);
 

@@ -643,6 +643,9 @@ extern "C" zx_status zx_paged_attend(const zx_paged_cache *cache, const zx_paged
     g.group = q_heads / cache->kv_heads;
     g.q_heads = q_heads;
     Plan p = make_plan(cache, batch, n_tokens, q_heads, n_blocks, g);
+    const uint64_t H = cache->kv_heads;
+    if ((p.rows && !launchable(p.rows_items * H, 512)) || (p.chunk && !launchable(split_items(p.cp.tiles, p.c) * H, 64 * p.cp.waves)))
+        return ZX_E_LIMIT;
     if (p.bytes && (!workspace || ws_bytes < p.bytes || !al16(workspace))) return ZX_E_INVAL;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     const uint32_t D = cache->head_dim;

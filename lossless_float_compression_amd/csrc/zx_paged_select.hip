@@ -395,7 +395,9 @@ Slabs make_slabs(const zx_paged_cache *c, const zx_paged_batch *b, uint32_t n)
     const bool pays = s.tt == 1 ? read <= 128 << 10 || wgs >= 192 : read * (wgs < 256 ? 256 : wgs) <= 256ull * (320 << 10);
     s.fused = s.nb <= kHeld && pays;
     if (s.fused) return s;
-    const uint64_t most = (256ull << 20) / (each ? each : 1);
+    // (a launch counts its threads in 32 bits)
+    const uint64_t by_bytes = (256ull << 20) / (each ? each : 1), by_threads = 0xFFFFFFFFull / ((uint64_t)kThreads * s.tt * c->kv_heads);
+    const uint64_t most = by_bytes < by_threads ? by_bytes : by_threads;
     s.slab = most < 1 ? 1 : most < s.groups ? (uint32_t)most : s.groups;
     s.bytes = each * s.slab;
     return s;
@@ -440,7 +442,7 @@ extern "C" zx_status zx_paged_select(const zx_paged_cache *cache, const zx_paged
     if ((st = make_rows(q, g.q)) != ZX_OK) return st;
     const Slabs s = make_slabs(cache, batch, n_tokens);
     if (s.bytes && (!workspace || ws_bytes < s.bytes || !al16(workspace))) return ZX_E_INVAL;
-    if ((uint64_t)s.slab * s.tt * cache->kv_heads > 0x7FFFFFFFull || s.nb > (1u << 26)) return ZX_E_LIMIT;
+    if (s.nb > (1u << 26)) return ZX_E_LIMIT;
     g.blocks = blocks;
     g.keys = static_cast<uint64_t *>(workspace);
     g.group = q_heads / cache->kv_heads;
@@ -450,7 +452,7 @@ extern "C" zx_status zx_paged_select(const zx_paged_cache *cache, const zx_paged
     g.nb = s.nb;
     g.slab = s.slab;
     if (s.fused) {
-        if ((uint64_t)n_tokens * cache->kv_heads > 0x7FFFFFFFull) return ZX_E_LIMIT;
+        if ((uint64_t)n_tokens * cache->kv_heads * kPickThreads > 0xFFFFFFFFull) return ZX_E_LIMIT;
         const dim3 grid(n_tokens * cache->kv_heads);
         if (cache->head_dim == 64) hipLaunchKernelGGL((k_pick<64>), grid, dim3(kPickThreads), 0, stream, g);
         else if (cache->head_dim == 128) hipLaunchKernelGGL((k_pick<128>), grid, dim3(kPickThreads), 0, stream, g);

@@ -95,6 +95,16 @@ def _int32(t, name: str, index: Optional[int] = None) -> torch.Tensor:
     return t
 
 
+def _apart(sizes, strides, width: int) -> bool:
+    """Whether rows of `width` elements at these strides are apart from each other: each stride
+    steps over all that the smaller ones reach."""
+    for st, n in sorted((st, n) for n, st in zip(sizes, strides) if n > 1):
+        if st < width:
+            return False
+        width = st * (n - 1) + width
+    return True
+
+
 class Rotary:
     """Rotary positions: in the first `dims` channels of a head (a multiple of 16), pair j
     is turned by position * inv_freq[j] and scaled by `magnitude`.  Pairs are channels
@@ -243,7 +253,7 @@ class PagedKVCache:
                 raise ValueError(f"{name} must be a {self.torch_dtype} device tensor {list(shape)}")
             if t.stride(3) != 1 or any(t.stride(i) % per16 for i in range(3)) or t.data_ptr() % 16:
                 raise ValueError(f"{name}: channels must be contiguous and the other strides multiples of 16 bytes")
-            if any(t.stride(i) < self.head_dim for i in range(3) if t.shape[i] > 1) or t.stride(2) < self.head_dim:
+            if t.stride(2) < self.head_dim or not _apart(t.shape[:3], t.stride()[:3], self.head_dim):
                 raise ValueError(f"{name}: rows must not overlap")
         self.k, self.v = k, v
         self.k_scale, self.v_scale = (self._scale(s, n) for s, n in ((k_scale, "k_scale"), (v_scale, "v_scale")))
@@ -291,11 +301,17 @@ class PagedKVCache:
                              f"{'heads' if heads is None else heads}, {self.head_dim}], got {t.dtype} {list(sh)}")
         if t.get_device() != self._index:
             raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
+        if t.requires_grad and torch.is_grad_enabled():
+            raise ValueError(f"{name} requires a gradient, which these operators do not have: detach it or use torch.no_grad()")
         s0, s1, s2 = t.stride()
+        if sh[0] == 1:
+            s0 = 0
+        if sh[1] == 1:
+            s1 = 0
         p = t.data_ptr()
         if s2 != 1 or s0 % 8 or s1 % 8 or p % 16:
             raise ValueError(f"{name}: channels must be contiguous, the other strides and the start multiples of 16 bytes")
-        if written and ((sh[0] > 1 and s0 < self.head_dim) or (sh[1] > 1 and s1 < self.head_dim)):
+        if written and not (s1 == self.head_dim and s0 == s1 * sh[1]) and not _apart(sh[:2], (s0, s1), self.head_dim):
             raise ValueError(f"{name}: rows that are written must not overlap")
         return zx_rows(p, s0, s1)
 
@@ -394,7 +410,8 @@ class PagedKVCache:
         """softmax(scale q.k) v of the new tokens' queries (bf16 [tokens, heads, head_dim], heads a
         multiple of kv_heads; neighbouring heads share a K/V head) over their sequence's tokens:
         up to their own place (causal) or all, and with `window` only those less than `window`
-        places before it.  scale defaults to head_dim^-1/2.  A row that sees no token is zero.
+        places before it.  scale defaults to head_dim^-1/2.  A row that sees no token is zero.  `out`
+        may be q itself.
 
         blocks: int32 [tokens, kv_heads, n] (from `select`, or any list): only these blocks of
         block_tokens tokens, counted from the sequence's start, are read; a list ends at its first
@@ -492,7 +509,8 @@ class PagedKVCache:
             raise ValueError("a page of keys is not a whole number of 65536-element blocks")
         return n // _zx.BLOCK_ELEMS
 
-    def _page_ids(self, pages: torch.Tensor, pool, slots: torch.Tensor) -> Tuple[torch.Tensor, int]:
+    def _page_ids(self, pages: torch.Tensor, pool, slots: torch.Tensor) -> Tuple[torch.Tensor, torch.Tensor, torch.Tensor]:
+        """(which ids are pages, the ids with any page for the others, the slots with none for the others)"""
         if pool.dtype != self.dtype:
             raise TypeError("the pool has another dtype than the cache")
         if not torch.is_tensor(pages) or pages.dtype not in (torch.int32, torch.int64) or pages.dim() != 1 or pages.device != self.device:
@@ -501,7 +519,9 @@ class PagedKVCache:
         bpp = self.blocks_per_page()
         if slots.shape != (2, pages.numel(), bpp):
             raise ValueError(f"slots must be [2, {pages.numel()}, {bpp}]: keys, then values")
-        return pages.long(), bpp
+        ids = pages.long()
+        ok = (ids >= 0) & (ids < self.n_pages)
+        return ok, ids.clamp(0, self.n_pages - 1), torch.where(ok[:, None], slots, -1)
 
     def _pages_of(self, ids: torch.Tensor) -> torch.Tensor:
         raw = torch.int16 if self.dtype == _zx.BF16 else torch.uint8
@@ -512,23 +532,34 @@ class PagedKVCache:
         """Compress whole pages into `pool` (a KVSlotPool of the cache's dtype): the keys of page
         pages[i] into slots[0, i], its values into slots[1, i] (device int32 [2, n, blocks_per_page()],
         distinct).  Returns (status, bounds): status [2, n, blocks_per_page()] is 0, or 6 for a block
-        that did not fit its slot (keep that page); bounds are the pages' rows of `self.bounds`,
+        that did not fit its slot (keep that page), or 1 where the page or the slot is none; bounds are the pages' rows of `self.bounds`,
         for `restore` (None without bounds).  The pages themselves are left as they are."""
-        ids, _ = self._page_ids(pages, pool, slots)
+        _, ids, slots = self._page_ids(pages, pool, slots)
+        if slots.numel() == 0:
+            return torch.empty_like(slots), None if self.bounds is None else self.bounds[ids]
         status = pool.append(self._pages_of(ids).reshape(-1), slots.reshape(-1), err=err)
         return status.view(slots.shape), None if self.bounds is None else self.bounds[ids]
 
     def restore(self, pages: torch.Tensor, pool, slots: torch.Tensor, bounds: Optional[torch.Tensor] = None,
                 err: Optional[torch.Tensor] = None) -> None:
         """Bring stowed pages back, bit for bit, into pages pages[i] (any free ones, distinct), and
-        their bounds with them.  A block whose slot is empty keeps what the page holds."""
-        ids, bpp = self._page_ids(pages, pool, slots)
+        their bounds with them.  A block whose slot is empty keeps what the page holds; ids that are
+        no page are left out, with 4 in `err`."""
+        ok, ids, slots = self._page_ids(pages, pool, slots)
         if (bounds is None) != (self.bounds is None):
             raise ValueError("give the bounds that stow returned")
-        if bounds is not None and (bounds.shape != (ids.numel(), *self.bounds.shape[1:]) or bounds.dtype != torch.bfloat16):
+        if bounds is not None and (bounds.shape != (ids.numel(), *self.bounds.shape[1:]) or bounds.dtype != torch.bfloat16
+                                   or bounds.device != self.device):
             raise ValueError("bounds are not those of these pages")
+        if slots.numel() == 0:
+            return
         held = self._pages_of(ids)
         pool.decode(slots.reshape(-1), out=held.view(-1, _zx.BLOCK_ELEMS).view(self.torch_dtype), err=err)
+        # an id that is no page stands for one that is; where none is, the page put in its place keeps what it has
+        same = torch.where(ok, torch.arange(ids.numel(), device=self.device), ok.int().argmax())
+        ids, held = ids[same], held[:, same]
+        if bounds is not None:
+            bounds = torch.where(ok.any(), bounds[same], self.bounds[ids])
         raw = held.dtype
         self.k.view(raw).index_copy_(0, ids, held[0])
         self.v.view(raw).index_copy_(0, ids, held[1])

@@ -95,7 +95,7 @@ def see_mask(scene, b, causal=True, window=0):
     n, y = scene.new[b], scene.total[b]
     p = y - n + torch.arange(n, device="cuda")[:, None]
     t = torch.arange(y, device="cuda")[None, :]
-    see = torch.ones((n, y), dtype=torch.bool, device="cuda")
+    see = (p >= 0).expand(n, y).clone()
     if causal:
         see &= t <= p
     if window:

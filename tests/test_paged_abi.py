@@ -115,7 +115,10 @@ def test_attend_refusals(lib):
     assert attend(ws=P(0x100000), size=need - 1) == INVAL
     assert attend(ws=P(0x100008), size=need) == INVAL
     assert lib.zx_paged_attend_workspace_bytes(C.byref(c), C.byref(b), 7, 3, 0, 0) == 0
-    # more work than 32-bit counts hold
+    # more work than 32-bit counts hold, more workgroups than a launch
+    one = batch(max_q=1)
+    assert lib.zx_paged_attend(C.byref(cb), C.byref(one), 1 << 22, C.byref(rows()), 8, C.byref(rows()), None, 1.0, 1, 0, P(0x9000), 4, None, 0,
+                               None, None) == LIMIT
     huge = batch(n_seqs=65536, table_width=1 << 19)
     assert lib.zx_paged_attend(C.byref(cache(page_tokens=512, k_head_stride=512 * 128, v_head_stride=512 * 128)), C.byref(huge), 65536,
                                C.byref(r), 8, C.byref(o), None, 1.0, 1, 0, None, 0, P(0x100000), 1 << 62, None, None) == LIMIT
@@ -139,6 +142,8 @@ def test_select_refusals(lib):
     assert need > 0 and select() == INVAL and select(ws=P(0x100000), size=need - 1) == INVAL and select(ws=P(0x100001), size=need) == INVAL
     assert lib.zx_paged_select_workspace_bytes(C.byref(cache()), C.byref(b), 7) == 0
     assert select(n=0) == OK
+    b = batch(max_q=1)
+    assert select(n=1 << 22) == LIMIT
 
 
 def test_python_refusals():
@@ -157,6 +162,14 @@ def test_python_refusals():
                dict(dims=64, inv_freq=torch.zeros(32, dtype=torch.float64), scaling="linear")):
         with pytest.raises(ValueError):
             zx.Rotary(device="cpu", **kw)
+
+
+def test_rows_apart():
+    apart = zx.paged._apart
+    assert apart((4, 8), (8 * 128, 128), 128) and apart((4, 8), (128, 4 * 128), 128) and apart((1, 8), (0, 128), 128)
+    assert apart((4, 8), (3 * 8 * 128, 136), 128) and apart((0, 8), (5, 128), 128)
+    for strides in ((0, 128), (8 * 128, 120), (7 * 128, 128), (128, 128), (8 * 128 - 8, 128)):
+        assert not apart((4, 8), strides, 128), strides
 
 
 def test_frequencies():

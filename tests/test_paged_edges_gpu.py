@@ -1,0 +1,257 @@
+"""Calls of the paged K/V cache at the edges of what its documentation allows."""
+import sys
+
+import pytest
+import torch
+
+import lossless_float_compression_amd as zx
+from paged_util import RAW, Scene, blocks_reference, check_out, listed_mask, reference, see_mask
+
+pytestmark = pytest.mark.gpu
+BF16, FP8 = zx.BF16, zx.FP8_E4M3FN
+
+
+@pytest.fixture(autouse=True)
+def gpu(request):
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    print(request.node.name, file=sys.stderr, flush=True)
+    yield
+    torch.cuda.synchronize()
+
+
+def dense(s, causal=True, window=0):
+    return reference(s, lambda b: see_mask(s, b, causal, window))
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_select_with_room_for_many_blocks(D):
+    """A wide page table: the keys of the blocks go through memory, for single tokens and for groups of four
+    that share reads; the same blocks as where they stay on chip."""
+    for new, total in (([1, 1, 0, 1], [700, 1, 30, 4000]), ([5, 1, 9, 2], [700, 1, 333, 4000])):
+        for top_k in (2, 9, 300):
+            a = Scene(BF16, 2, 3, D, 32, new, total, C=16, seed=30, pad=1, width=2600)
+            q = max(new)
+            got = a.cache().select(a.q, a.batch(max_q=q), top_k).cpu()
+            assert torch.equal(got[:a.N], blocks_reference(a, top_k, 1, 1)[:a.N])
+            assert torch.equal(a.cache().select(a.q, a.batch(max_q=q, max_kv=max(total)), top_k).cpu(), got)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+@pytest.mark.parametrize("H,G,D,T", [(2, 4, 128, 16), (3, 7, 64, 64), (1, 5, 256, 32)])
+def test_mixed_batch_with_room(dtype, H, G, D, T):
+    """Single tokens beside chunks, where lengths may be long: both kernels run, with their joins."""
+    s = Scene(dtype, H, G, D, T, [1, 120, 1, 0, 7, 90, 1], [999, 200, 1, 50, 40, 1500, 5000], seed=31, pad=1, width=900)
+    for causal, window in ((True, 0), (False, 0), (True, 70)):
+        out, lse = torch.full_like(s.q, 7.0), torch.full(s.q.shape[:2], 5.0, device="cuda")
+        before = out.clone()
+        s.cache().attend(s.q, s.batch(), causal=causal, window=window, out=out, lse=lse)
+        check_out(s, out, lse, dense(s, causal, window), before)
+
+
+def test_many_sequences():
+    """More sequences than a search step holds, most of them with nothing new."""
+    n = 1500
+    new = [1 if i % 5 == 0 else 0 for i in range(n)]
+    new[700], new[1499] = 90, 3
+    total = [(i * 37) % 60 + new[i] for i in range(n)]
+    s = Scene(BF16, 1, 2, 64, 16, new, total, C=16, seed=32, pad=2)
+    check_out(s, s.cache().attend(s.q, s.batch()), None, dense(s))
+    assert torch.equal(s.cache().select(s.q, s.batch(), 3).cpu()[:s.N], blocks_reference(s, 3, 1, 1)[:s.N])
+
+
+@pytest.mark.parametrize("new", [[1, 1], [5, 30], [40, 170]])
+@pytest.mark.parametrize("causal", [True, False])
+def test_fewer_tokens_than_new_ones(new, causal):
+    """New tokens at negative places see nothing, whether the attention is causal or not."""
+    s = Scene(BF16, 2, 4, 128, 16, new, [0, new[1] // 2], seed=33)
+    out, lse = torch.full_like(s.q, 7.0), torch.zeros(s.q.shape[:2], device="cuda")
+    s.cache().attend(s.q, s.batch(), causal=causal, out=out, lse=lse)
+    check_out(s, out, lse, dense(s, causal))
+    assert not out[:new[0]].any()
+
+
+@pytest.mark.parametrize("new", [[1, 1, 1], [3, 9, 1], [60, 1, 200]])
+@pytest.mark.parametrize("width", [1, 800])
+def test_output_over_the_queries(new, width):
+    s = Scene(BF16, 2, 4, 128, 16, new, [600, 90, 2500], C=16, seed=34, width=width)
+    c, b = s.cache(), s.batch()
+    blocks = c.select(s.q, b, 5)
+    for bl in (None, blocks):
+        want = c.attend(s.q, b, blocks=bl)
+        q = s.q.clone()
+        assert c.attend(q, b, blocks=bl, out=q) is q
+        assert torch.equal(q, want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("width", [1, 700])
+def test_nan_in_a_chunk(dtype, D, width):
+    """As every width and type of the tiled kernel, with four waves and with eight: a NaN key or value
+    reaches the rows that see its token, no other."""
+    s = Scene(dtype, 1, 4, D, 16, [200], [330], seed=35, width=width)
+    c, b = s.cache(), s.batch()
+    clean = c.attend(s.q, b)
+    at = 330 - 200 + 77
+    page, off = int(s.table[0, at // 16]), at % 16
+    for pages in (s.vraw, s.kraw):
+        old = pages[page, 0, off].clone()
+        pages[page, 0, off, D - 3] = 0x7FC0 if dtype == BF16 else 0x7F
+        got = c.attend(s.q, b)
+        pages[page, 0, off] = old
+        assert torch.equal(got[:77], clean[:77])
+        hit = got[77:]
+        if pages is s.kraw:
+            assert torch.isnan(hit).all()
+        else:
+            assert torch.isnan(hit[..., D - 3]).all()
+            rest = [i for i in range(D) if i != D - 3]
+            assert torch.equal(hit[..., rest], clean[77:][..., rest])
+
+
+def test_two_calls_at_once():
+    """Two streams use one cache and one batch, each with its own queries, many times over."""
+    s = Scene(BF16, 4, 4, 128, 32, [1, 130, 3], [2000, 1500, 4000], C=32, seed=36, width=200)
+    c, b = s.cache(), s.batch()
+    qs = [s.q, s.q.flip(0).contiguous()]
+    want = [(c.attend(q, b), c.select(q, b, 6)) for q in qs]
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    got = [[], []]
+    for _ in range(10):
+        for i in (0, 1):
+            bl = c.select(qs[i], b, 6, stream=streams[i])
+            with torch.cuda.stream(streams[i]):
+                got[i].append((c.attend(qs[i], b), bl))
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        for out, bl in got[i]:
+            assert torch.equal(out, want[i][0]) and torch.equal(bl, want[i][1])
+
+
+def test_shared_pages():
+    """Two sequences that begin with the same pages, and a page that is in one table twice."""
+    s = Scene(BF16, 2, 4, 128, 16, [1, 70], [300, 400], seed=37)
+    s.table[1, :10] = s.table[0, :10]
+    s.table[1, 12] = s.table[1, 11]
+    check_out(s, s.cache().attend(s.q, s.batch()), None, dense(s))
+
+
+def test_bounds_of_nothing():
+    """max_q or max_kv of zero, tables without columns: sequences that pass them are left out and reported,
+    empty ones are not."""
+    s = Scene(BF16, 2, 2, 128, 16, [1, 2], [30, 20], C=16, seed=38)
+    c = s.cache()
+    rows = torch.randn((s.N, 2, 128), device="cuda").to(torch.bfloat16)
+    held = s.kraw.clone()
+    none = zx.PagedBatch(s.q_start, s.kv_len, s.table[:, :0].contiguous())
+    for b in (s.batch(max_q=0), s.batch(max_kv=0), none):
+        err = torch.zeros(3, dtype=torch.int32, device="cuda")
+        out = c.attend(s.q, b, out=torch.full_like(s.q, 3.0), err=err[:1])
+        bl = c.select(s.q, b, 4, err=err[1:2])
+        c.append(rows, rows, b, err=err[2:])
+        assert err.tolist() == [4, 4, 4] and torch.equal(out, torch.full_like(out, 3.0)) and (bl == -1).all()
+        assert torch.equal(s.kraw, held)
+    zero = torch.zeros_like(s.kv_len)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    b = zx.PagedBatch(s.q_start, zero, s.table[:, :0].contiguous())
+    assert not c.attend(s.q, b, out=torch.full_like(s.q, 3.0), err=err).any()
+    assert (c.select(s.q, b, 4, err=err) == -1).all()
+    c.append(rows, rows, b, err=err)
+    assert int(err.item()) == 0 and torch.equal(s.kraw, held)
+
+
+def test_largest_lists_and_groups():
+    """1024 blocks of 1024 and more; 256 query heads on one K/V head."""
+    s = Scene(FP8, 1, 2, 64, 256, [1, 2], [16 * 1500, 16 * 900], C=16, seed=39)
+    c, b = s.cache(), s.batch()
+    blocks = c.select(s.q, b, 1024)
+    assert torch.equal(blocks.cpu(), blocks_reference(s, 1024, 1, 1))
+    see, _ = listed_mask(s, blocks)
+    check_out(s, c.attend(s.q, b, blocks=blocks), None, reference(s, see))
+    for new in ([1, 1], [3, 1]):
+        s = Scene(BF16, 1, 256, 128, 32, new, [500, 90], C=32, seed=40)
+        check_out(s, s.cache().attend(s.q, s.batch()), None, dense(s))
+        blocks = s.cache().select(s.q, s.batch(), 4)
+        assert torch.equal(blocks.cpu(), blocks_reference(s, 4, 1, 1))
+        see, _ = listed_mask(s, blocks)
+        check_out(s, s.cache().attend(s.q, s.batch(), blocks=blocks), None, reference(s, see))
+
+
+def test_select_and_lists_in_replayed_graphs():
+    """Both forms of the selection, and attention over their lists, replayed with rewritten lengths and eager
+    work between."""
+    for width in (1, 3000):
+        s = Scene(BF16, 2, 4, 128, 16, [1, 6], [1200, 500], C=16, seed=41, width=width)
+        c, b = s.cache(), s.batch()
+        out, blocks = torch.zeros_like(s.q), torch.zeros((s.N, 2, 7), dtype=torch.int32, device="cuda")
+        c.attend(s.q, b, blocks=c.select(s.q, b, 7))
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            c.select(s.q, b, 7, blocks=blocks)
+            c.attend(s.q, b, blocks=blocks, out=out)
+        for total in ([1200, 500], [60, 499], [1, 6], [1199, 300]):
+            s.kv_len.copy_(torch.tensor(total, dtype=torch.int32))
+            bl = c.select(s.q, b, 7)
+            want = c.attend(s.q, b, blocks=bl)
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+            assert torch.equal(blocks, bl) and torch.equal(out, want)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+def test_stow_ids_that_are_no_page(dtype):
+    s = Scene(dtype, 8, 1, 128, 512, [1, 1, 1], [512, 512, 512], C=64, seed=42)
+    c = s.cache()
+    pool = zx.KVSlotPool(2 * 4 * 8, dtype, cap_words=8192)
+    good = s.table[:, 0].tolist()
+    ids = torch.tensor([good[0], -1, good[2], s.n_pages], dtype=torch.int32, device="cuda")
+    slots = torch.arange(64, dtype=torch.int32, device="cuda").view(2, 4, 8)
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    status, bounds = c.stow(ids, pool, slots, err=err)
+    assert int(err.item()) != 0 and not status[:, 0::2].any() and (status[:, 1::2] == 1).all()
+    held = s.kraw.clone(), s.vraw.clone(), s.bounds.clone()
+    for p in (good[0], good[2]):
+        s.kraw[p], s.vraw[p], s.bounds[p] = 1, 1, 0
+    err.zero_()
+    c.restore(ids, pool, slots, bounds, err=err)
+    assert int(err.item()) == 4
+    nothing = torch.full_like(ids, -9)
+    c.restore(nothing, pool, slots, bounds, err=err)
+    c.restore(ids[:0], pool, slots[:, :0], bounds[:0])
+    assert c.stow(ids[:0], pool, slots[:, :0].contiguous())[0].shape == (2, 0, 8)
+    for a, b in zip((s.kraw, s.vraw, s.bounds.view(torch.int16)), (held[0], held[1], held[2].view(torch.int16))):
+        assert torch.equal(a, b)
+
+
+def test_refusals_on_the_device():
+    s = Scene(BF16, 2, 2, 128, 16, [1, 2], [30, 20], C=16, seed=43)
+    c, b = s.cache(), s.batch()
+    k = torch.zeros((3, 2, 128), dtype=torch.bfloat16, device="cuda")
+    wants = s.q.clone().requires_grad_()
+    long = torch.zeros(3 * 4 * 128 + 8, dtype=torch.bfloat16, device="cuda")
+    over = torch.zeros(8192, dtype=torch.bfloat16, device="cuda").as_strided((4, 2, 16, 128), (128, 128, 128, 1))
+    for call in (lambda: c.attend(wants, b), lambda: c.select(wants, b, 2), lambda: c.append(k, k, b, q=wants), lambda: c.attend(s.q.float(), b),
+                 lambda: c.attend(s.q[:, :3], b), lambda: c.attend(s.q[:, :, :64], b), lambda: c.attend(s.q.cpu(), b),
+                 lambda: c.attend(s.q, b, out=s.q[:2]), lambda: c.attend(s.q, b, out=s.q[:1].expand(3, 4, 128)),
+                 lambda: c.attend(s.q, b, out=long.as_strided((3, 4, 128), (256, 128, 1))), lambda: c.attend(long[4:-4].view(3, 4, 128), b),
+                 lambda: c.attend(s.q, b, window=-1), lambda: c.attend(s.q, b, scale=0.0), lambda: c.attend(s.q, b, lse=torch.zeros(3, 4)),
+                 lambda: c.attend(s.q, b, blocks=torch.zeros((3, 2, 4), dtype=torch.int64, device="cuda")),
+                 lambda: c.attend(s.q, b, blocks=torch.zeros((3, 2, 0), dtype=torch.int32, device="cuda")),
+                 lambda: c.attend(s.q, b, causal=False, blocks=torch.zeros((3, 2, 4), dtype=torch.int32, device="cuda")),
+                 lambda: c.select(s.q, b, 0), lambda: c.select(s.q, b, 2, 2, 1), lambda: c.select(s.q, b, 1025), lambda: c.append(k, k[:2], b),
+                 lambda: c.append(k[:, :1], k[:, :1], b), lambda: c.append(k, k, b, q_out=s.q), lambda: c.append(k, k, b, rotary=zx.Rotary(144)),
+                 lambda: c.append(k, k, b, positions=torch.zeros(3, dtype=torch.int32, device="cuda")),
+                 lambda: c.append(k, k, b, rotary=zx.Rotary(64), positions=torch.zeros(2, dtype=torch.int32, device="cuda")),
+                 lambda: zx.PagedKVCache(4, 2, 128, 16, k=over, v=over)):
+        with pytest.raises(ValueError):
+            call()
+    with torch.no_grad():
+        assert torch.equal(c.attend(wants, b), c.attend(s.q, b))
+    # one row: its strides say nothing
+    odd = s.q[:1].as_strided((1, 4, 128), (5, 128, 1))
+    one = zx.PagedBatch(s.q_start[:2].contiguous(), s.kv_len[:1].contiguous(), s.table[:1].contiguous())
+    assert torch.equal(c.attend(odd, one), c.attend(s.q[:1], one))
