@@ -475,13 +475,13 @@ struct Plan {
 };
 
 constexpr uint32_t kFewRows = 64;    // rows of a sequence that k_rows takes
-// Up to so many bytes of keys and values one workgroup of eight waves reads them all, and there
-// is no second launch to join pieces.  A CU draws about 57 bytes a nanosecond, so with few
-// row tiles pieces on several CUs are read sooner, but the second launch takes that back:
-// one token over 1000, 8 K/V heads, BF16: 14.1 us a call like this, 13.9 in pieces; over 16
-// selected blocks of 64: 24.5 with the selection, 27 in pieces; 123 tokens, 2 K/V heads, over 40
-// blocks of 32, E4M3: 43 and 52.
-constexpr uint64_t kWideBytes = 512 << 10;
+// Up to so many bytes of keys and values a row tile, one workgroup of eight waves reads them all, and there is no
+// second launch to join pieces (about 4 us).  A CU draws about 57 bytes a nanosecond, so with few row tiles
+// pieces on several CUs are sooner read from twice 128 KB on; with a workgroup for half the CUs or more, later.
+// Us a call in one launch / in pieces, 8 K/V heads of 128 channels, BF16: one token over 250 8.0 / 11.9, over 500
+// 9.8 / 11.9, over 1000 14.4 / 11.9; 16 tokens, each over its 700, 13.4 / 16.6, over 16 blocks of 64 16.2 / 19.7,
+// but of lengths from 62 to 1000 15.6 / 14.3; 123 tokens, 2 heads, over 40 blocks of 32, E4M3, 13.9 / 21.3.
+constexpr uint64_t wide_bytes(uint64_t tiles) { return tiles < 128 ? 256 << 10 : 512 << 10; }
 // Workgroups of k_rows that the card holds at a time.
 constexpr uint32_t rows_groups(uint32_t d, uint32_t mt) { return 256u * (uint32_t)rows_waves((int)d, (int)mt); }
 
@@ -507,7 +507,7 @@ Plan make_plan(const zx_paged_cache *c, const zx_paged_batch *b, uint32_t n, uin
         p.mt = 1;
         const uint32_t tiles = n * ceil_div(G, 16), steps = ceil_div((uint64_t)n_blocks * c->block_tokens, kStep);
         const uint32_t s = ceil_div(rows_groups(D, 1), (uint64_t)tiles * H);
-        p.wide = D <= 128 && s > 1 && 2 * (uint64_t)n_blocks * c->block_tokens * D * es <= kWideBytes;
+        p.wide = D <= 128 && s > 1 && 2 * (uint64_t)n_blocks * c->block_tokens * D * es <= wide_bytes((uint64_t)tiles * H);
         p.r.pieces = p.wide ? 1 : s > steps ? steps : s;
         p.rows_items = tiles * p.r.pieces;
         p.rows_max = G < 16 ? G : 16;
@@ -526,7 +526,7 @@ Plan make_plan(const zx_paged_cache *c, const zx_paged_batch *b, uint32_t n, uin
             p.mt = D == 64 && most > 32 ? 3 : D <= 128 && most > 16 ? 2 : 1;
             const uint32_t R = 16 * p.mt, tiles = p.chunk ? seqs * ceil_div(kFewRows, R) : bound_tiles(n, seqs, G, R);
             plan_split(tiles, ceil_div(rows_groups(D, p.mt), H), 2, 1, 1, cap, kStep, p.r);
-            p.wide = D <= 128 && p.mt <= 2 && p.r.one_round && p.r.slots && 2 * cap * D * es <= kWideBytes;
+            p.wide = D <= 128 && p.mt <= 2 && p.r.one_round && p.r.slots && 2 * cap * D * es <= wide_bytes((uint64_t)tiles * H);
             if (p.wide) p.r.slots = 0;
             rows_slots = p.r.slots;
             p.rows_items = split_items(tiles, p.r);

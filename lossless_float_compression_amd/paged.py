@@ -273,6 +273,7 @@ class PagedKVCache:
                                  v.stride(0), v.stride(1), v.stride(2), ptr(self.k_scale), ptr(self.v_scale),
                                  ptr(bounds))
         self._ref = C.byref(self._c)
+        self._bytes = torch.empty(0, dtype=torch.uint8, device=self.device)     # what workspaces are allocated like
         self._tensors = tuple(t for t in (self.k, self.v, self.k_scale, self.v_scale, self.bounds) if t is not None)
 
     def _scale(self, s, name: str) -> Optional[torch.Tensor]:
@@ -304,15 +305,18 @@ class PagedKVCache:
         if t.requires_grad and torch.is_grad_enabled():
             raise ValueError(f"{name} requires a gradient, which these operators do not have: detach it or use torch.no_grad()")
         s0, s1, s2 = t.stride()
-        if sh[0] == 1:
-            s0 = 0
-        if sh[1] == 1:
-            s1 = 0
         p = t.data_ptr()
-        if s2 != 1 or s0 % 8 or s1 % 8 or p % 16:
-            raise ValueError(f"{name}: channels must be contiguous, the other strides and the start multiples of 16 bytes")
-        if written and not (s1 == self.head_dim and s0 == s1 * sh[1]) and not _apart(sh[:2], (s0, s1), self.head_dim):
-            raise ValueError(f"{name}: rows that are written must not overlap")
+        if s2 != 1 or s1 != sh[2] or s0 != s1 * sh[1]:           # (contiguous rows meet all that is asked for below)
+            if sh[0] == 1:
+                s0 = 0
+            if sh[1] == 1:
+                s1 = 0
+            if s2 != 1 or s0 % 8 or s1 % 8:
+                raise ValueError(f"{name}: channels must be contiguous and the other strides multiples of 16 bytes")
+            if written and not _apart(sh[:2], (s0, s1), self.head_dim):
+                raise ValueError(f"{name}: rows that are written must not overlap")
+        if p % 16:
+            raise ValueError(f"{name} must start at a multiple of 16 bytes")
         return zx_rows(p, s0, s1)
 
     def _common(self, batch: PagedBatch, err: Optional[torch.Tensor]):
@@ -322,9 +326,11 @@ class PagedKVCache:
             return _int32(err, "err", self._index).data_ptr()
         return None
 
-    def _group(self, q: torch.Tensor) -> None:
-        if q.dim() != 3 or q.shape[1] == 0 or q.shape[1] % self.kv_heads:
+    def _group(self, q: torch.Tensor) -> Tuple[int, int]:
+        sh = q.shape
+        if len(sh) != 3 or sh[1] == 0 or sh[1] % self.kv_heads:
             raise ValueError(f"q must be [tokens, heads, {self.head_dim}] with a multiple of {self.kv_heads} heads")
+        return sh[0], sh[1]
 
     def _away(self, stream) -> bool:
         """Whether a call has to change the current device or stream first."""
@@ -424,8 +430,7 @@ class PagedKVCache:
             return self._elsewhere(stream, batch, (q, out, lse, err, blocks),
                                    lambda s: self.attend(q, batch, scale, causal, window, blocks, out, lse, err, s))
         e = self._common(batch, err)
-        self._group(q)
-        n, heads = q.shape[0], q.shape[1]
+        n, heads = self._group(q)
         cq = self._rows(q, "q", None, None)
         if out is None:
             out = torch.empty((n, heads, self.head_dim), dtype=torch.bfloat16, device=self.device)
@@ -457,9 +462,9 @@ class PagedKVCache:
         need = batch._needs.get(key)
         if need is None:
             need = batch._needs[key] = L.zx_paged_attend_workspace_bytes(self._ref, batch._ref, n, heads, window, nb)
-        pw = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
+        ws = self._bytes.new_empty(need) if need else None
         st = L.zx_paged_attend(self._ref, batch._ref, n, C.byref(cq), heads, C.byref(co), pl, scale, causal, window, pb, nb,
-                               None if pw is None else pw.data_ptr(), need, e, self._raw(stream))
+                               ws.data_ptr() if need else None, need, e, self._raw(stream))
         if st != 0:
             raise _zx.ZxError("zx_paged_attend", st)
         return out
@@ -476,8 +481,7 @@ class PagedKVCache:
             return self._elsewhere(stream, batch, (q, blocks, err),
                                    lambda s: self.select(q, batch, top_k, keep_first, keep_last, blocks, err, s))
         e = self._common(batch, err)
-        self._group(q)
-        n, heads = q.shape[0], q.shape[1]
+        n, heads = self._group(q)
         cq = self._rows(q, "q", None, None)
         if self.block_tokens is None:
             raise ValueError("select needs a cache with block_tokens")
@@ -494,9 +498,9 @@ class PagedKVCache:
         need = batch._needs.get((self._key, n))
         if need is None:
             need = batch._needs[(self._key, n)] = L.zx_paged_select_workspace_bytes(self._ref, batch._ref, n)
-        pw = torch.empty(need, dtype=torch.uint8, device=self.device) if need else None
+        ws = self._bytes.new_empty(need) if need else None
         st = L.zx_paged_select(self._ref, batch._ref, n, C.byref(cq), heads, top_k, keep_first, keep_last, blocks.data_ptr(),
-                               None if pw is None else pw.data_ptr(), need, e, self._raw(stream))
+                               ws.data_ptr() if need else None, need, e, self._raw(stream))
         if st != 0:
             raise _zx.ZxError("zx_paged_select", st)
         return blocks
