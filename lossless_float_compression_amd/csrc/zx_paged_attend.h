@@ -2,6 +2,8 @@
 // arguments, how the tokens are split between workgroups, and the kernel that joins the pieces.
 #pragma once
 
+#include <type_traits>
+
 #include "zx_paged.h"
 
 namespace zxp {
@@ -216,25 +218,26 @@ static __global__ __launch_bounds__(256) void k_join(AttendArgs g)
     auto where = [&](uint32_t piece, uint32_t row) { return ((uint64_t)(base_slot + piece) * g.c.heads + h) * ROWS + row; };
     auto place = [&](uint32_t row) { return sv.q0 + (int64_t)(tok0 + (row0 + row) / G); };
     auto head = [&](uint32_t row) { return h * G + (row0 + row) % G; };
-    if (nch <= 8) {
-        // few pieces: GR rows at a time, a lane adds up its four channels
+    // few pieces: GR rows at a time, a lane adds up its four channels
+    auto few = [&](auto most) {
+        constexpr uint32_t N = decltype(most)::value;
         for (uint32_t row = blockIdx.z * GR + gr; row < nrows; row += gridDim.z * GR) {
             // (reads past the last piece repeat it: all are under way at once)
-            f4 y[8];
-            float pm[8], pl[8], mm = -kInf, ll = 0.0f;
+            f4 y[N];
+            float pm[N], pl[N], mm = -kInf, ll = 0.0f;
 #pragma unroll
-            for (uint32_t i = 0; i < 8; ++i) {
+            for (uint32_t i = 0; i < N; ++i) {
                 const uint64_t at = where(i < nch ? i : nch - 1, row);
                 pm[i] = g.stat[at * 2];
                 pl[i] = g.stat[at * 2 + 1];
                 y[i] = *reinterpret_cast<const f4 *>(g.part + at * D + 4 * ln);
             }
 #pragma unroll
-            for (uint32_t i = 0; i < 8; ++i) mm = fmaxf(mm, pm[i]);
+            for (uint32_t i = 0; i < N; ++i) mm = fmaxf(mm, pm[i]);
             const float base = mm == -kInf ? 0.0f : mm;
             f4 x = {0, 0, 0, 0};
 #pragma unroll
-            for (uint32_t i = 0; i < 8; ++i) {
+            for (uint32_t i = 0; i < N; ++i) {
                 if (i >= nch) break;
                 const float f = __builtin_amdgcn_exp2f(pm[i] - base);
                 ll += pl[i] * f;
@@ -245,8 +248,9 @@ static __global__ __launch_bounds__(256) void k_join(AttendArgs g)
                 u2{pack2(x[0] * inv, x[1] * inv), pack2(x[2] * inv, x[3] * inv)};
             if (g.lse && ln == 0) g.lse[place(row) * g.q_heads + head(row)] = ll == 0.0f ? -kInf : (mm + log2f(ll)) * kLn2;
         }
-        return;
-    }
+    };
+    if (nch <= 3) return few(std::integral_constant<uint32_t, 3>{});
+    if (nch <= 8) return few(std::integral_constant<uint32_t, 8>{});
     for (uint32_t row = blockIdx.z; row < nrows; row += gridDim.z) {
         float mm = -kInf;
         for (uint32_t i = threadIdx.x & 63u; i < nch; i += 64) mm = fmaxf(mm, g.stat[where(i, row) * 2]);
@@ -297,10 +301,11 @@ inline void plan_split(uint32_t tiles, uint32_t room, uint32_t many, uint32_t le
     g.one_round = 2 * tiles <= room;
     g.goal = g.one_round ? room : many * room;
     g.least = g.one_round ? least : least_many;
-    g.slots = cap > (uint64_t)g.least * unit ? 2 * g.goal : 0;
+    const uint64_t each = ceil_div(cap, (uint64_t)g.least * unit), all = tiles * each;       // pieces that lengths up to cap may make
+    g.slots = each <= 1 ? 0 : all < 2 * g.goal ? (uint32_t)all : 2 * g.goal;
 }
 // Items of the kernel, and row tiles for its join (0: nothing can be split).
-inline uint32_t split_items(uint32_t tiles, const AttendArgs &g) { return g.slots ? g.goal + tiles : tiles; }
+inline uint32_t split_items(uint32_t tiles, const AttendArgs &g) { return !g.slots ? tiles : g.slots < g.goal + tiles ? g.slots : g.goal + tiles; }
 inline uint32_t split_tiles(uint32_t tiles, const AttendArgs &g) { return !g.slots ? 0 : tiles < g.goal ? tiles : g.goal; }
 
 // Workgroups of k_join that share the rows of a row tile: about a thousand in all.
