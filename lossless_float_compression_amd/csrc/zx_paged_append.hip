@@ -1,13 +1,24 @@
 // zx_paged_append.hip -- new keys and values into a paged K/V cache, with the position
 // rotation on the way, and the checks that all entry points of the paged cache share.
 //
+// A pair (a, b) of channels of a row at place p becomes (a cos - b sin, b cos + a sin) of the angle
+// p * inv_freq, times a magnitude.  Bound by the bytes: every row is read once and written once.
+//
 // A workgroup takes one segment of a sequence's new tokens (the tokens of one bounded
-// block, or of 32 places where the cache has no bounds) and a group of heads: of the
+// block, or of 32 places where the cache has no bounds) and a group of eight heads: of the
 // keys, of the values or of the queries.  It computes the cosines and sines of the
-// segment's positions once, in LDS, and turns the rows of all its heads with them.  A
-// thread holds 16 channels, eight rotated pairs.  One workgroup owns a block's bounds
-// for its heads, so they are reduced in registers and LDS with no atomics and do not
-// depend on any order.
+// segment's positions once, in LDS, and turns the rows of all its heads with them (with one
+// head a workgroup the sines would cost more than the rows).  A thread holds 16 channels, eight
+// rotated pairs, of two rows of keys or four of values and queries at a time, all read before
+// the sines are worked out: 71 us for five prompts of up to 2900 tokens (BF16, 8 K/V and 32 query
+// heads of 128 channels, 233 MB) with one role after the other, 55 us with the roles in workgroups of their own, 4.2 TB/s
+// of the 5.15 TB/s of a large copy.  (More waves a SIMD spill: 63 us at five, 82 at six; 16 heads a
+// workgroup 62.)  One token: 4.5 us, a launch; 256 tokens with bounds, E4M3: 10 us.
+// One workgroup owns a block's bounds for its heads, so they are reduced in registers and
+// LDS with no atomics and do not depend on any order.
+//
+// Rounding: keys and queries are turned in 32 bits and rounded once, to what is stored.  The angle is taken in
+// 64 bits and its whole turns dropped there: in 32 bits a place of a million would be off by a sixteenth of a radian.
 #include "zx_paged.h"
 
 namespace zxp {
