@@ -402,19 +402,30 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_chunk(AttendArgs 
         }
     }
 
-    if (!live || wr + lr >= w9) return;
+    if (!live) return;
+    const bool mine = wr + lr < w9;              // (both lanes of a row are, or neither)
     l = sum_halves(l);
     if (nch == 1) {
         const float inv = l == 0.0f ? 0.0f : (g.c.v_scale ? g.c.v_scale[h] : 1.0f) / l;
-        __bf16 *op = g.out.p + at * g.out.token + (int64_t)qh * g.out.head + 4 * lh;
+        // A lane has channels 8 i + 4 lh .. + 3 of each 32; with the lane of the row's other half it trades four for
+        // four, so that both write 16 bytes, next to each other.
+        __bf16 *op = g.out.p + at * g.out.token + (int64_t)qh * g.out.head + 8 * lh;
 #pragma unroll
         for (int d = 0; d < ND; ++d)
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                *reinterpret_cast<u2 *>(op + 32 * d + 8 * i) =
-                    u2{pack2(o[d][4 * i] * inv, o[d][4 * i + 1] * inv), pack2(o[d][4 * i + 2] * inv, o[d][4 * i + 3] * inv)};
-        if (g.lse && lh == 0) g.lse[at * g.q_heads + qh] = l == 0.0f ? -kInf : (m + log2f(l)) * kLn2;
-    } else {
+            for (int i = 0; i < 4; i += 2) {
+                u4 y;
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const auto r = __builtin_amdgcn_permlane32_swap(pack2(o[d][4 * i + 2 * j] * inv, o[d][4 * i + 2 * j + 1] * inv),
+                                                                    pack2(o[d][4 * i + 4 + 2 * j] * inv, o[d][4 * i + 5 + 2 * j] * inv), false, false);
+                    y[j] = (uint32_t)r[0];
+                    y[2 + j] = (uint32_t)r[1];
+                }
+                if (mine) *reinterpret_cast<u4 *>(op + 32 * d + 8 * i) = y;
+            }
+        if (g.lse && mine && lh == 0) g.lse[at * g.q_heads + qh] = l == 0.0f ? -kInf : (m + log2f(l)) * kLn2;
+    } else if (mine) {
         const uint64_t r = ((uint64_t)slot * g.c.heads + h) * ROWS + (row - row0);
         float *dst = g.part + r * D + 4 * lh;
 #pragma unroll
