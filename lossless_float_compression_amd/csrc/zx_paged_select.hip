@@ -337,8 +337,10 @@ template <int D>
 __global__ __launch_bounds__(kPickThreads) void k_pick(SelectArgs g)
 {
     constexpr uint32_t LB = D / 8, PB = kPickThreads / LB;
+    constexpr uint32_t P = kPickThreads / D;             // threads of a channel of the group's sums
     __shared__ uint64_t held[kHeld];
     __shared__ Picking sh;
+    __shared__ __align__(16) double parts[2][P][D], total[2][D];
     const uint32_t h = blockIdx.x % g.c.heads, row = blockIdx.x / g.c.heads;
     uint32_t seq, local, unused, seen;
     Seq sv;
@@ -351,14 +353,40 @@ __global__ __launch_bounds__(kPickThreads) void k_pick(SelectArgs g)
     uint64_t least = ~0ull, most = 0;
     Fetched f;
     fetch<D, PB>(g, table, h, f0 + slot, f1, ln, f);                 // under way while the queries are added up
-    double up[1][8], dn[1][8];
-    group_sums<1>(g, sv.q0 + (int64_t)local, 1, h, ln, up, dn);
+    // the sums over the group's heads, once for the workgroup (every lane for itself: 2 us more with eight heads)
+    {
+        const uint32_t ch = threadIdx.x % D, p = threadIdx.x / D;
+        const __bf16 *qp = g.q.p + (sv.q0 + (int64_t)local) * g.q.token + (int64_t)(h * g.group) * g.q.head + ch;
+        double a = 0.0, b = 0.0;
+        for (uint32_t e = p; e < g.group; e += P) {
+            const float y = (float)qp[(int64_t)e * g.q.head];
+            a += (double)(y < 0.0f ? 0.0f : y);
+            b += (double)(y > 0.0f ? 0.0f : y);
+        }
+        parts[0][p][ch] = a;
+        parts[1][p][ch] = b;
+        __syncthreads();
+        if (threadIdx.x < 2 * D) {
+            const uint32_t side = threadIdx.x / D;
+            a = parts[side][0][ch];
+#pragma unroll
+            for (uint32_t i = 1; i < P; ++i) a += parts[side][i][ch];
+            total[side][ch] = a;
+        }
+        __syncthreads();
+    }
+    double up[8], dn[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        up[i] = total[0][8 * ln + i];
+        dn[i] = total[1][8 * ln + i];
+    }
     for (uint32_t j = f0 + slot; j < f1; j += kUnroll * PB) {
         const Fetched now = f;
         if (j + kUnroll * PB < f1) fetch<D, PB>(g, table, h, j + kUnroll * PB, f1, ln, f);
 #pragma unroll
         for (int u = 0; u < kUnroll; ++u) {
-            const double s = block_sum<(int)LB>(now, u, up[0], dn[0]);
+            const double s = block_sum<(int)LB>(now, u, up, dn);
             if (j + u * PB < f1) {
                 const uint64_t x = now.none >> u & 1u ? 0 : order_key(s);
                 if (ln == 0) held[j + u * PB - f0] = x;
