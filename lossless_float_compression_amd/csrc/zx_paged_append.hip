@@ -94,7 +94,7 @@ namespace {
 constexpr uint32_t kThreads = 256;
 constexpr uint32_t kSeg = 32;          // places of a segment where there are no bounds
 constexpr uint32_t kTab = 32;          // tokens whose cosines and sines are held at a time
-constexpr uint32_t kGroup = 8;         // heads of a workgroup
+constexpr uint32_t kLogGroup = 3, kGroup = 1u << kLogGroup;   // heads of a workgroup
 
 typedef int16_t i16x2 __attribute__((ext_vector_type(2)));
 
@@ -111,7 +111,7 @@ struct AppendArgs {
     Batch b;
     Rows k, v, q, qo;
     Turn turn;
-    uint32_t kv_groups, kv_lanes;      // K/V head groups and heads of one (a power of two up to kGroup)
+    uint32_t kv_groups, kv_log;        // K/V head groups; log2 of the heads of one (up to kLogGroup)
     uint32_t q_heads, log_seg;
 };
 
@@ -193,12 +193,13 @@ __device__ __forceinline__ void append_rows(const AppendArgs &g, const Segment &
     constexpr uint32_t ROWS = kThreads / TPR;           // rows at a time
     constexpr int kBatch = ROLE == KEYS ? 2 : 4;        // rows of a thread that are read together
     const uint32_t tid = threadIdx.x;
-    const uint32_t lanes = ROLE == QUERIES ? kGroup : g.kv_lanes, heads = ROLE == QUERIES ? g.q_heads : g.c.heads;   // lanes: heads side by side
-    const uint32_t h0 = group * lanes;
+    const uint32_t log_lanes = ROLE == QUERIES ? kLogGroup : g.kv_log, lanes = 1u << log_lanes;      // lanes: heads side by side
+    const uint32_t heads = ROLE == QUERIES ? g.q_heads : g.c.heads;
+    const uint32_t h0 = group << log_lanes;
     const uint32_t slot = tid / TPR, c = tid % TPR;
-    const uint32_t tslot = slot / lanes, tstep = ROWS / lanes;
-    const bool live = h0 + slot % lanes < heads;
-    const uint32_t head = live ? h0 + slot % lanes : heads - 1;
+    const uint32_t tslot = slot >> log_lanes, tstep = ROWS >> log_lanes;
+    const bool live = h0 + (slot & (lanes - 1u)) < heads;
+    const uint32_t head = live ? h0 + (slot & (lanes - 1u)) : heads - 1;
     const uint32_t half = ROLE == VALUES ? 0 : g.turn.half;
     const bool turned = 8 * c < half;
     // a thread's two pieces: the two sides of eight pairs, or 16 channels that are not turned or hold whole pairs
@@ -443,9 +444,8 @@ extern "C" zx_status zx_paged_append(const zx_paged_cache *cache, const zx_paged
         g.turn = Turn{rot->inv_freq, positions, rot->dims / 2, rot->interleaved, rot->magnitude};
     }
     g.log_seg = g.c.bounds ? g.c.log_block : log2_of(kSeg);
-    g.kv_lanes = 1;
-    while (g.kv_lanes < kGroup && g.kv_lanes < g.c.heads) g.kv_lanes *= 2;
-    g.kv_groups = ceil_div(g.c.heads, g.kv_lanes);
+    while (g.kv_log < kLogGroup && (1u << g.kv_log) < g.c.heads) ++g.kv_log;
+    g.kv_groups = ceil_div(g.c.heads, 1u << g.kv_log);
     const uint64_t by_len = ((uint64_t)n_tokens >> g.log_seg) + 2ull * batch->n_seqs;
     const uint32_t segs = (uint32_t)(by_len < n_tokens ? by_len : n_tokens);
     const dim3 grid(segs, 2 * g.kv_groups + ceil_div(g.q_heads, kGroup));
