@@ -218,30 +218,36 @@ static __global__ __launch_bounds__(256) void k_join(AttendArgs g)
     auto where = [&](uint32_t piece, uint32_t row) { return ((uint64_t)(base_slot + piece) * g.c.heads + h) * ROWS + row; };
     auto place = [&](uint32_t row) { return sv.q0 + (int64_t)(tok0 + (row0 + row) / G); };
     auto head = [&](uint32_t row) { return h * G + (row0 + row) % G; };
-    // few pieces: GR rows at a time, a lane adds up its four channels
-    auto few = [&](auto most) {
+    // GR rows at a time, a lane adds up its four channels, N pieces under way at once
+    auto rows = [&](auto most) {
         constexpr uint32_t N = decltype(most)::value;
         for (uint32_t row = blockIdx.z * GR + gr; row < nrows; row += gridDim.z * GR) {
-            // (reads past the last piece repeat it: all are under way at once)
-            f4 y[N];
-            float pm[N], pl[N], mm = -kInf, ll = 0.0f;
-#pragma unroll
-            for (uint32_t i = 0; i < N; ++i) {
-                const uint64_t at = where(i < nch ? i : nch - 1, row);
-                pm[i] = g.stat[at * 2];
-                pl[i] = g.stat[at * 2 + 1];
-                y[i] = *reinterpret_cast<const f4 *>(g.part + at * D + 4 * ln);
-            }
-#pragma unroll
-            for (uint32_t i = 0; i < N; ++i) mm = fmaxf(mm, pm[i]);
-            const float base = mm == -kInf ? 0.0f : mm;
             f4 x = {0, 0, 0, 0};
+            float mm = -kInf, ll = 0.0f;
+            for (uint32_t i0 = 0; i0 < nch; i0 += N) {
+                // (reads past the last piece repeat it)
+                f4 y[N];
+                float pm[N], pl[N], nm = mm;
 #pragma unroll
-            for (uint32_t i = 0; i < N; ++i) {
-                if (i >= nch) break;
-                const float f = __builtin_amdgcn_exp2f(pm[i] - base);
-                ll += pl[i] * f;
-                x += y[i] * f;
+                for (uint32_t i = 0; i < N; ++i) {
+                    const uint64_t at = where(i0 + i < nch ? i0 + i : nch - 1, row);
+                    pm[i] = g.stat[at * 2];
+                    pl[i] = g.stat[at * 2 + 1];
+                    y[i] = *reinterpret_cast<const f4 *>(g.part + at * D + 4 * ln);
+                }
+#pragma unroll
+                for (uint32_t i = 0; i < N; ++i) nm = fmaxf(nm, pm[i]);
+                const float base = nm == -kInf ? 0.0f : nm, old = __builtin_amdgcn_exp2f(mm - base);
+                mm = nm;
+                ll *= old;
+                x *= old;
+#pragma unroll
+                for (uint32_t i = 0; i < N; ++i) {
+                    if (i0 + i >= nch) break;
+                    const float f = __builtin_amdgcn_exp2f(pm[i] - base);
+                    ll += pl[i] * f;
+                    x += y[i] * f;
+                }
             }
             const float inv = ll == 0.0f ? 0.0f : vs / ll;
             *reinterpret_cast<u2 *>(g.out.p + place(row) * g.out.token + (int64_t)head(row) * g.out.head + 4 * ln) =
@@ -249,8 +255,9 @@ static __global__ __launch_bounds__(256) void k_join(AttendArgs g)
             if (g.lse && ln == 0) g.lse[place(row) * g.q_heads + head(row)] = ll == 0.0f ? -kInf : (mm + log2f(ll)) * kLn2;
         }
     };
-    if (nch <= 3) return few(std::integral_constant<uint32_t, 3>{});
-    if (nch <= 8) return few(std::integral_constant<uint32_t, 8>{});
+    if (nch <= 3) return rows(std::integral_constant<uint32_t, 3>{});
+    if (nch <= 8 || gridDim.z < nrows) return rows(std::integral_constant<uint32_t, 8>{});
+    // many pieces and a workgroup for every row: its pieces are shared between GR groups of lanes
     for (uint32_t row = blockIdx.z; row < nrows; row += gridDim.z) {
         float mm = -kInf;
         for (uint32_t i = threadIdx.x & 63u; i < nch; i += 64) mm = fmaxf(mm, g.stat[where(i, row) * 2]);
@@ -258,6 +265,7 @@ static __global__ __launch_bounds__(256) void k_join(AttendArgs g)
         const float base = mm == -kInf ? 0.0f : mm;
         f4 x = {0, 0, 0, 0};
         float ll = 0.0f;
+#pragma unroll 4
         for (uint32_t i = gr; i < nch; i += GR) {
             const uint64_t at = where(i, row);
             const float f = __builtin_amdgcn_exp2f(g.stat[at * 2] - base);

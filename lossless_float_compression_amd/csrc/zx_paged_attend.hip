@@ -63,7 +63,7 @@ __global__ __launch_bounds__(64 * NW, rows_waves(D, MT) * 4 >= NW ? rows_waves(D
     constexpr int KL = D * 16 * ES / 64 / 16;        // 16-byte loads a lane makes of 16 keys
     constexpr int OS = D + 4;                        // LDS row of the join, in floats
     __shared__ __align__(16) float ods[NW * 16 * OS];
-    __shared__ float mls[2][NW][16];
+    __shared__ float mls[2][MT][NW][16];
 
     const uint32_t lane = threadIdx.x & 63u;
     const uint32_t wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -414,14 +414,19 @@ __global__ __launch_bounds__(64 * NW, rows_waves(D, MT) * 4 >= NW ? rows_waves(D
     // join the waves, 16 rows at a time
     const float vs = g.c.v_scale ? g.c.v_scale[h] : 1.0f;
     const uint64_t slot = ((uint64_t)piece_slot * g.c.heads + h) * ROWS;
+    // (all statistics first: what stays in registers across the loops below is then the sums alone, which lie
+    // in accumulation registers and are not moved about)
+#pragma unroll
+    for (int t = 0; t < MT; ++t) {
+        l[t] = sum_quarters(l[t]);
+        if (lq == 0) {
+            mls[0][t][wave][lr] = m[t];
+            mls[1][t][wave][lr] = l[t];
+        }
+    }
 #pragma unroll
     for (int t = 0; t < MT; ++t) {
         if (t) __syncthreads();
-        l[t] = sum_quarters(l[t]);
-        if (lq == 0) {
-            mls[0][wave][lr] = m[t];
-            mls[1][wave][lr] = l[t];
-        }
         // a lane has, of row lr, channels n * 16 VW + (4 lq + i) VW + j
         float *dst = ods + (wave * 16 + lr) * OS;
 #pragma unroll
@@ -438,13 +443,13 @@ __global__ __launch_bounds__(64 * NW, rows_waves(D, MT) * 4 >= NW ? rows_waves(D
             if (row >= nrows) continue;
             float mm = -kInf;
 #pragma unroll
-            for (int w = 0; w < NW; ++w) mm = fmaxf(mm, mls[0][w][r]);
+            for (int w = 0; w < NW; ++w) mm = fmaxf(mm, mls[0][t][w][r]);
             const float base = mm == -kInf ? 0.0f : mm;
             float ll = 0.0f, x[8] = {};
 #pragma unroll
             for (int w = 0; w < NW; ++w) {
-                const float f = __builtin_amdgcn_exp2f(mls[0][w][r] - base);
-                ll += mls[1][w][r] * f;
+                const float f = __builtin_amdgcn_exp2f(mls[0][t][w][r] - base);
+                ll += mls[1][t][w][r] * f;
                 const float *src = ods + (w * 16 + r) * OS + ch;
 #pragma unroll
                 for (int i = 0; i < 8; ++i) x[i] += src[i] * f;
@@ -531,7 +536,10 @@ Plan make_plan(const zx_paged_cache *c, const zx_paged_batch *b, uint32_t n, uin
         // but beside 64 of them 193 / 174, and beside 16 over 16000 449 / 352.
         p.rows = !p.chunk || (seqs > 1 && (cap > 4096 || (uint64_t)seqs * H > 256));
         if (p.rows) {
-            p.mt = D == 64 && most > 32 ? 3 : D <= 128 && most > 16 ? 2 : 1;
+            // 16, 32 or 48 rows a tile, so that keys and values are read once for a sequence's rows (48 only where the registers
+            // hold them): 90 sequences of 7 x 4 rows, 256 channels, E4M3, 54 us in tiles of 32, 65 of 16; 16 of 5 x 8 rows, 64 channels,
+            // 23 us in tiles of 48, 30 of 32.
+            p.mt = D == 64 && most > 32 ? 3 : most > 16 ? 2 : 1;
             const uint32_t R = 16 * p.mt, tiles = p.chunk ? seqs * ceil_div(kFewRows, R) : bound_tiles(n, seqs, G, R);
             plan_split(tiles, ceil_div(rows_groups(D, p.mt), H), 2, 1, 1, cap, kStep, p.r);
             p.wide = D <= 128 && p.mt <= 2 && p.r.one_round && p.r.slots && 2 * cap * D * es <= wide_bytes((uint64_t)tiles * H);
@@ -588,7 +596,7 @@ void run_plan(Plan &p, uint32_t n_blocks, uint8_t *ws, hipStream_t stream)
         } else if (p.mt == 1) {
             launch_rows<DT, D, 1, false, (int)kStep>(p, a, grid, jgrid, stream);
         } else if (p.mt == 2) {
-            if constexpr (D <= 128) launch_rows<DT, D, 2, false, (int)kStep>(p, a, grid, jgrid, stream);
+            launch_rows<DT, D, 2, false, (int)kStep>(p, a, grid, jgrid, stream);
         } else if constexpr (D == 64) {
             launch_rows<DT, D, 3, false, (int)kStep>(p, a, grid, jgrid, stream);
         }

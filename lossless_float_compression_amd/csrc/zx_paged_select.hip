@@ -98,34 +98,39 @@ __device__ __forceinline__ void fetch(const SelectArgs &g, const int32_t *table,
     }
 }
 
-// Sums over the group's heads of the positive and of the negative parts of eight channels, for TT tokens
-// from packed row `row` on (those past nt repeat the last).  A NaN stays one in both sums.
-template <int TT>
-__device__ __forceinline__ void group_sums(const SelectArgs &g, int64_t row, uint32_t nt, uint32_t h, uint32_t ln, double (&up)[TT][8], double (&dn)[TT][8])
+// Sums over the group's heads of the positive and of the negative parts of every channel, for nt tokens from packed
+// row `row` on, into sh.total.  By a whole workgroup of NT threads, once (every lane for itself would
+// take 2 us more with eight heads, and 25 with sixteen and four tokens).  A NaN stays one in both sums.
+template <int D, int TT, int NT>
+struct Sums {
+    static constexpr uint32_t P = NT / D;                // threads of a channel
+    double parts[P][2][D], total[TT][2][D];
+};
+template <int D, int TT, int NT>
+__device__ __forceinline__ void group_sums(const SelectArgs &g, int64_t row, uint32_t nt, uint32_t h, Sums<D, TT, NT> &sh)
 {
-    constexpr int kQ = TT == 1 ? 4 : 2;                  // heads read at a time, for each token
+    constexpr uint32_t P = Sums<D, TT, NT>::P;
+    const uint32_t ch = threadIdx.x % D, p = threadIdx.x / D;
+    const __bf16 *qp = g.q.p + row * g.q.token + (int64_t)(h * g.group) * g.q.head + ch;
 #pragma unroll
-    for (int t = 0; t < TT; ++t)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) up[t][i] = dn[t][i] = 0.0;
-    for (uint32_t e = 0; e < g.group; e += kQ) {
-        bf8 x[TT][kQ];
-#pragma unroll
-        for (int t = 0; t < TT; ++t) {
-            const __bf16 *qp = g.q.p + (row + ((uint32_t)t < nt ? (uint32_t)t : nt - 1)) * g.q.token + (int64_t)(h * g.group) * g.q.head + 8 * ln;
-#pragma unroll
-            for (int k = 0; k < kQ; ++k) x[t][k] = *reinterpret_cast<const bf8 *>(qp + (int64_t)(e + k < g.group ? e + k : e) * g.q.head);
+    for (uint32_t t = 0; t < (uint32_t)TT; ++t) {
+        if (t >= nt) break;
+        double a = 0.0, b = 0.0;
+        for (uint32_t e = p; e < g.group; e += P) {
+            const float y = (float)qp[t * g.q.token + (int64_t)e * g.q.head];
+            a += (double)(y < 0.0f ? 0.0f : y);
+            b += (double)(y > 0.0f ? 0.0f : y);
         }
+        sh.parts[p][0][ch] = a;
+        sh.parts[p][1][ch] = b;
+        __syncthreads();
+        for (uint32_t i = threadIdx.x; i < 2 * D; i += NT) {
+            a = (&sh.parts[0][0][0])[i];
 #pragma unroll
-        for (int t = 0; t < TT; ++t)
-#pragma unroll
-            for (int k = 0; k < kQ; ++k)
-#pragma unroll
-                for (int i = 0; i < 8; ++i) {
-                    const float y = e + k < g.group ? (float)x[t][k][i] : 0.0f;
-                    up[t][i] += (double)(y < 0.0f ? 0.0f : y);
-                    dn[t][i] += (double)(y > 0.0f ? 0.0f : y);
-                }
+            for (uint32_t j = 1; j < P; ++j) a += (&sh.parts[j][0][0])[i];
+            (&sh.total[t][0][0])[i] = a;
+        }
+        __syncthreads();
     }
 }
 
@@ -145,6 +150,7 @@ __global__ __launch_bounds__(kThreads) void k_score(SelectArgs g)
 {
     constexpr uint32_t LB = D / 8;                       // lanes of a block
     constexpr uint32_t PB = kThreads / LB;               // blocks at a time
+    __shared__ __align__(16) Sums<D, TT, kThreads> sums;
     const uint32_t h = blockIdx.x % g.c.heads, grp = blockIdx.x / g.c.heads;
     uint32_t seq, local, unused;
     Seq sv;
@@ -161,8 +167,15 @@ __global__ __launch_bounds__(kThreads) void k_score(SelectArgs g)
     const int32_t *table = g.b.table + (uint64_t)seq * g.b.width;
     Fetched f;
     fetch<D, PB>(g, table, h, j0 + slot, j1, ln, f);                 // under way while the queries are added up
+    group_sums(g, sv.q0 + (int64_t)tok, nt, h, sums);
     double up[TT][8], dn[TT][8];
-    group_sums<TT>(g, sv.q0 + (int64_t)tok, nt, h, ln, up, dn);
+#pragma unroll
+    for (int t = 0; t < TT; ++t)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            up[t][i] = sums.total[(uint32_t)t < nt ? t : 0][0][8 * ln + i];
+            dn[t][i] = sums.total[(uint32_t)t < nt ? t : 0][1][8 * ln + i];
+        }
     for (uint32_t j = j0 + slot; j < j1; j += kUnroll * PB) {
         double s[kUnroll][TT];
 #pragma unroll
@@ -337,10 +350,9 @@ template <int D>
 __global__ __launch_bounds__(kPickThreads) void k_pick(SelectArgs g)
 {
     constexpr uint32_t LB = D / 8, PB = kPickThreads / LB;
-    constexpr uint32_t P = kPickThreads / D;             // threads of a channel of the group's sums
     __shared__ uint64_t held[kHeld];
     __shared__ Picking sh;
-    __shared__ __align__(16) double parts[2][P][D], total[2][D];
+    __shared__ __align__(16) Sums<D, 1, kPickThreads> sums;
     const uint32_t h = blockIdx.x % g.c.heads, row = blockIdx.x / g.c.heads;
     uint32_t seq, local, unused, seen;
     Seq sv;
@@ -353,33 +365,12 @@ __global__ __launch_bounds__(kPickThreads) void k_pick(SelectArgs g)
     uint64_t least = ~0ull, most = 0;
     Fetched f;
     fetch<D, PB>(g, table, h, f0 + slot, f1, ln, f);                 // under way while the queries are added up
-    // the sums over the group's heads, once for the workgroup (every lane for itself: 2 us more with eight heads)
-    {
-        const uint32_t ch = threadIdx.x % D, p = threadIdx.x / D;
-        const __bf16 *qp = g.q.p + (sv.q0 + (int64_t)local) * g.q.token + (int64_t)(h * g.group) * g.q.head + ch;
-        double a = 0.0, b = 0.0;
-        for (uint32_t e = p; e < g.group; e += P) {
-            const float y = (float)qp[(int64_t)e * g.q.head];
-            a += (double)(y < 0.0f ? 0.0f : y);
-            b += (double)(y > 0.0f ? 0.0f : y);
-        }
-        parts[0][p][ch] = a;
-        parts[1][p][ch] = b;
-        __syncthreads();
-        if (threadIdx.x < 2 * D) {
-            const uint32_t side = threadIdx.x / D;
-            a = parts[side][0][ch];
-#pragma unroll
-            for (uint32_t i = 1; i < P; ++i) a += parts[side][i][ch];
-            total[side][ch] = a;
-        }
-        __syncthreads();
-    }
+    group_sums(g, sv.q0 + (int64_t)local, 1, h, sums);
     double up[8], dn[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
-        up[i] = total[0][8 * ln + i];
-        dn[i] = total[1][8 * ln + i];
+        up[i] = sums.total[0][0][8 * ln + i];
+        dn[i] = sums.total[0][1][8 * ln + i];
     }
     for (uint32_t j = f0 + slot; j < f1; j += kUnroll * PB) {
         const Fetched now = f;

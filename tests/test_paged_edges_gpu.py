@@ -49,6 +49,38 @@ def test_mixed_batch_with_room(dtype, H, G, D, T):
         check_out(s, out, lse, dense(s, causal, window), before)
 
 
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("G", [1, 5, 16])
+def test_every_row_of_a_few(dtype, D, G):
+    """16, 32 and 48 rows a tile, full and not, split and not: statistics and sums of each row tile by themselves."""
+    for new, total in (([7, 12, 3], [40, 12, 300]), ([4, 4, 2], [2000, 16, 17]), ([10, 9, 11], [128, 129, 1100])):
+        s = Scene(dtype, 2, G, D, 32, new, total, seed=44, pad=1)
+        out, lse = torch.full_like(s.q, 7.0), torch.full(s.q.shape[:2], 5.0, device="cuda")
+        before = out.clone()
+        s.cache().attend(s.q, s.batch(), out=out, lse=lse)
+        check_out(s, out, lse, dense(s), before)
+
+
+def test_joins_of_many_pieces():
+    """One long sequence among short ones: more pieces than a join reads at once, for few rows and for many."""
+    for new in ([1, 1, 1], [5, 1, 2], [40, 3, 70]):
+        for D in (64, 128):
+            s = Scene(BF16, 1, 4, D, 64, new, [40, 30000, 100], seed=45)
+            out, lse = torch.zeros_like(s.q), torch.zeros(s.q.shape[:2], device="cuda")
+            s.cache().attend(s.q, s.batch(), out=out, lse=lse)
+            check_out(s, out, lse, dense(s))
+
+
+@pytest.mark.parametrize("G", [1, 3, 16, 40])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_select_of_groups(D, G):
+    """Sums over groups that do and do not fill the threads of a channel, with both forms of the selection."""
+    for width in (1, 2600):
+        s = Scene(BF16, 2, G, D, 32, [5, 1, 2], [700, 333, 90], C=16, seed=46, pad=1, width=width)
+        assert torch.equal(s.cache().select(s.q, s.batch(), 6).cpu()[:s.N], blocks_reference(s, 6, 1, 1)[:s.N])
+
+
 def test_many_sequences():
     """More sequences than a search step holds, most of them with nothing new."""
     n = 1500
