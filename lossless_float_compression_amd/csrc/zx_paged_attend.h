@@ -255,7 +255,9 @@ static __global__ __launch_bounds__(256) void k_join(AttendArgs g)
             if (g.lse && ln == 0) g.lse[place(row) * g.q_heads + head(row)] = ll == 0.0f ? -kInf : (mm + log2f(ll)) * kLn2;
         }
     };
+    // (repeated reads are not free: five or six pieces of 13 x 256 rows 22 us at six, 28 at eight)
     if (nch <= 3) return rows(std::integral_constant<uint32_t, 3>{});
+    if (nch <= 6) return rows(std::integral_constant<uint32_t, 6>{});
     if (nch <= 8 || gridDim.z < nrows) return rows(std::integral_constant<uint32_t, 8>{});
     // many pieces and a workgroup for every row: its pieces are shared between GR groups of lanes
     for (uint32_t row = blockIdx.z; row < nrows; row += gridDim.z) {
