@@ -255,6 +255,8 @@ class PagedKVCache:
                 raise ValueError(f"{name}: channels must be contiguous and the other strides multiples of 16 bytes")
             if t.stride(2) < self.head_dim or not _apart(t.shape[:3], t.stride()[:3], self.head_dim):
                 raise ValueError(f"{name}: rows must not overlap")
+        if k.data_ptr() == v.data_ptr():
+            raise ValueError("k and v must be pages of their own")
         self.k, self.v = k, v
         self.k_scale, self.v_scale = (self._scale(s, n) for s, n in ((k_scale, "k_scale"), (v_scale, "v_scale")))
         if self.block_tokens is not None:

@@ -170,6 +170,42 @@ def test_shared_pages():
     check_out(s, s.cache().attend(s.q, s.batch()), None, dense(s))
 
 
+def test_one_batch_for_several_caches():
+    """Workspaces follow the cache and the call, not the batch they were first asked for with."""
+    a = Scene(BF16, 2, 4, 128, 32, [1, 70], [3000, 400], C=32, seed=47, width=300)
+    b = Scene(FP8, 2, 4, 128, 32, [1, 70], [3000, 400], C=32, seed=47, width=300)
+    c = Scene(BF16, 2, 4, 256, 32, [1, 70], [3000, 400], C=32, seed=47, width=300)
+    shared = a.batch()
+    for s in (a, b, c, a):
+        for window in (0, 40, 100000):
+            assert torch.equal(s.cache().attend(s.q, shared, window=window), s.cache().attend(s.q, s.batch(), window=window))
+        assert torch.equal(s.cache().attend(s.q[:1], zx.PagedBatch(s.q_start[:2].contiguous(), s.kv_len[:1].contiguous(), s.table[:1].contiguous())),
+                           s.cache().attend(s.q, shared)[:1])
+        assert torch.equal(s.cache().select(s.q, shared, 5), s.cache().select(s.q, s.batch(), 5))
+
+
+def test_append_past_32_bits():
+    """Pages and bounds more than 4 GiB into the cache."""
+    n = 4800
+    far = zx.PagedKVCache(n, 8, 256, 512, FP8, block_tokens=16)
+    near = zx.PagedKVCache(4, 8, 256, 512, FP8, block_tokens=16)
+    g = torch.Generator(device="cuda")
+    g.manual_seed(48)
+    k, v = (torch.randn((900, 8, 256), generator=g, device="cuda").to(torch.bfloat16) for _ in range(2))
+    q = torch.randn((900, 16, 256), generator=g, device="cuda").to(torch.bfloat16)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    table = torch.tensor([[0, 1], [2, 3]], **i32)
+    start, length = torch.tensor([0, 600, 900], **i32), torch.tensor([700, 1000], **i32)
+    a, b = zx.PagedBatch(start, length, table), zx.PagedBatch(start, length, n - 1 - table)
+    rot = zx.Rotary(256)
+    assert torch.equal(near.append(k, v, a, q=q, rotary=rot), far.append(k, v, b, q=q, rotary=rot))
+    ids = torch.tensor([n - 1, n - 2, n - 3, n - 4], device="cuda")
+    for x, y in ((near.k, far.k), (near.v, far.v)):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8)[ids])
+    assert torch.equal(near.bounds, far.bounds[ids])
+    assert torch.equal(near.select(q, a, 7), far.select(q, b, 7))
+
+
 def test_bounds_of_nothing():
     """max_q or max_kv of zero, tables without columns: sequences that pass them are left out and reported,
     empty ones are not."""
@@ -278,7 +314,8 @@ def test_refusals_on_the_device():
                  lambda: c.append(k[:, :1], k[:, :1], b), lambda: c.append(k, k, b, q_out=s.q), lambda: c.append(k, k, b, rotary=zx.Rotary(144)),
                  lambda: c.append(k, k, b, positions=torch.zeros(3, dtype=torch.int32, device="cuda")),
                  lambda: c.append(k, k, b, rotary=zx.Rotary(64), positions=torch.zeros(2, dtype=torch.int32, device="cuda")),
-                 lambda: zx.PagedKVCache(4, 2, 128, 16, k=over, v=over)):
+                 lambda: zx.PagedKVCache(4, 2, 128, 16, k=over, v=over),
+                 lambda: zx.PagedKVCache(4, 2, 128, 16, k=s.kraw.view(torch.bfloat16)[:4], v=s.kraw.view(torch.bfloat16)[:4])):
         with pytest.raises(ValueError):
             call()
     with torch.no_grad():
