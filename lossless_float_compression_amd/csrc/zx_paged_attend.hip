@@ -12,7 +12,7 @@
 // that the second product wants (any order of tokens will do there, if the values' order
 // is the same).
 //
-//   k_rows   few rows (single tokens, groups of a few): bound by the bytes of K and V.
+//   k_rows   few rows (single tokens, groups of a few), or little to read: bound by the bytes of K and V.
 //            Every wave reads its own tokens straight into the operand registers, with no
 //            LDS in the loop; the waves and the workgroups that share a row are joined at the end.
 //            64 single tokens over 5 .. 16384 tokens, BF16: 262 us, 5.4 TB/s; 4 over 131072, E4M3: 188 us, 5.7 TB/s
@@ -488,6 +488,14 @@ struct Plan {
 };
 
 constexpr uint32_t kFewRows = 64;    // rows of a sequence that k_rows takes
+// With a row tile of its own for every CU at most, and so many tokens met by all of them together, k_rows takes sequences of
+// any number of rows: without tiles in LDS to fill it is done sooner, until the keys and values that its row tiles read again
+// outweigh that.  Us with k_rows / k_chunk (row tiles, tokens met), 128 channels: 20 new tokens of 32 heads over 2000 (24, 48,000)
+// 15 / 25, 100 of 10 heads over 6000 (32, 192,000) 25 / 32, 4 x 50 of 32 heads over 1000 (224, 224,000) 18 / 28, but 4 x 64 (256, 256,000)
+// 32 / 29, 100 of 32 heads over 6000 (104, 624,000) 44 / 34, a prompt of 256 (256, 66,000) 18 / 15; 64 channels: 60 of 28 heads over 6000
+// (36, 216,000) 23 / 24, 8 x 30 over 3000 (160, 480,000) 28 / 25, a prompt of 512 of 32 heads (344, 176,000) 24 / 15; 256 channels: 8 x 30 of 8 heads
+// over 3000 (64, 192,000) 39 / 45, 8 x 64 (128, 384,000) 66 / 51, 6 x 272 of 8 heads (408, 115,000) 39 / 30.
+constexpr uint64_t kRowTiles = 255, kTileTokens = 250000;
 // Up to so many bytes of keys and values a row tile, one workgroup of eight waves reads them all, and there is no
 // second launch to join pieces (about 4 us).  A CU draws about 57 bytes a nanosecond, so with few row tiles
 // pieces on several CUs are sooner read from twice 128 KB on; with a workgroup for half the CUs or more, later.
@@ -529,17 +537,18 @@ Plan make_plan(const zx_paged_cache *c, const zx_paged_batch *b, uint32_t n, uin
             rows_slots = p.rows_items;
         }
     } else {
-        p.chunk = most > kFewRows;
+        // 16, 32 or 48 rows a tile, so that keys and values are read once for a few rows (48 only where the registers
+        // hold them): 90 sequences of 7 x 4 rows, 256 channels, E4M3, 54 us in tiles of 32, 65 of 16; 16 of 5 x 8 rows, 64 channels,
+        // 23 us in tiles of 48, 30 of 32.
+        p.mt = D == 64 && most > 32 ? 3 : most > 16 ? 2 : 1;
+        const uint64_t row_tiles = ceil_div(most, 16 * p.mt) * (uint64_t)seqs * H;
+        p.chunk = most > kFewRows && (row_tiles > kRowTiles || row_tiles * cap > kTileTokens);
         // A batch may mix single tokens with long chunks.  k_chunk can serve both; k_rows and its join read the
         // single tokens' caches faster but cost two launches.  Us without / with them, 8 heads of 128 channels: 4 sequences
         // of up to 100 new tokens over 1000 29 / 32, over 4000 39 / 46; 512 new beside 16 single tokens over 2000 60 / 91,
         // but beside 64 of them 193 / 174, and beside 16 over 16000 449 / 352.
         p.rows = !p.chunk || (seqs > 1 && (cap > 4096 || (uint64_t)seqs * H > 256));
         if (p.rows) {
-            // 16, 32 or 48 rows a tile, so that keys and values are read once for a sequence's rows (48 only where the registers
-            // hold them): 90 sequences of 7 x 4 rows, 256 channels, E4M3, 54 us in tiles of 32, 65 of 16; 16 of 5 x 8 rows, 64 channels,
-            // 23 us in tiles of 48, 30 of 32.
-            p.mt = D == 64 && most > 32 ? 3 : most > 16 ? 2 : 1;
             const uint32_t R = 16 * p.mt, tiles = p.chunk ? seqs * ceil_div(kFewRows, R) : bound_tiles(n, seqs, G, R);
             plan_split(tiles, ceil_div(rows_groups(D, p.mt), H), 2, 1, 1, cap, kStep, p.r);
             p.wide = D <= 128 && p.mt <= 2 && p.r.one_round && p.r.slots && 2 * cap * D * es <= wide_bytes((uint64_t)tiles * H);

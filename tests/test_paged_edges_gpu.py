@@ -142,6 +142,99 @@ def test_nan_in_a_chunk(dtype, D, width):
             assert torch.equal(hit[..., rest], clean[77:][..., rest])
 
 
+# How long sequences may get decides between the kernels: with room for 4000 and for 8000 tokens many rows go
+# through the tiled one, with four waves and with eight.
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+@pytest.mark.parametrize("H,G,D,T", [(2, 4, 128, 16), (4, 1, 64, 32), (2, 3, 256, 16), (2, 5, 128, 256), (3, 2, 64, 64)])
+@pytest.mark.parametrize("causal,window", [(True, 0), (False, 0), (True, 100)])
+@pytest.mark.parametrize("room", [4000, 8000])
+def test_tiles(dtype, H, G, D, T, causal, window, room):
+    s = Scene(dtype, H, G, D, T, [63, 130, 257, 65, 1], [63, 700, 300, 64 * 9, 333], seed=49, pad=3, width=(room - 720) // T)
+    out, lse = torch.full_like(s.q, 7.0), torch.full(s.q.shape[:2], 5.0, device="cuda")
+    before = out.clone()
+    s.cache().attend(s.q, s.batch(), causal=causal, window=window, out=out, lse=lse)
+    check_out(s, out, lse, dense(s, causal, window), before)
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("width", [200, 700])
+@pytest.mark.parametrize("window", [0, 20])
+def test_nan_in_tiles(dtype, D, width, window):
+    s = Scene(dtype, 2, 4, D, 16, [300], [430], seed=50, width=width)
+    c, b = s.cache(), s.batch()
+    clean = c.attend(s.q, b, window=window)
+    at = 430 - 300 + 77
+    page, off = int(s.table[0, at // 16]), at % 16
+    seen = torch.arange(300, device="cuda") >= 77
+    if window:
+        seen &= torch.arange(300, device="cuda") < 77 + window
+    for pages, bits in ((s.vraw, 0x7FC0), (s.kraw, 0x7FC0), (s.vraw, 0x7F80)):
+        if dtype == FP8:
+            bits = 0x7F
+        old = pages[page, 1, off].clone()
+        pages[page, 1, off, D - 3] = bits
+        got = c.attend(s.q, b, window=window)
+        pages[page, 1, off] = old
+        assert torch.equal(got[:, :4], clean[:, :4]) and torch.equal(got[~seen], clean[~seen])
+        hit = got[seen][:, 4:]
+        if pages is s.kraw:
+            assert torch.isnan(hit).all()
+        else:
+            x = hit[..., D - 3].float()
+            assert (torch.isnan(x) if bits != 0x7F80 else torch.isinf(x)).all()
+            rest = [i for i in range(D) if i != D - 3]
+            assert torch.equal(hit[..., rest], clean[seen][:, 4:][..., rest])
+
+
+def test_tiles_of_bad_pages_empty_rows_and_shared_pages():
+    """What the small cases above check of one kernel, of the tiled one."""
+    s = Scene(BF16, 2, 4, 128, 16, [40, 170, 1, 200], [0, 85, 0, 300], seed=51, width=500)
+    for causal in (True, False):
+        out, lse = torch.full_like(s.q, 7.0), torch.zeros(s.q.shape[:2], device="cuda")
+        s.cache().attend(s.q, s.batch(), causal=causal, out=out, lse=lse)
+        check_out(s, out, lse, dense(s, causal))
+    s = Scene(BF16, 2, 4, 128, 16, [1, 170, 200], [100, 390, 300], seed=52, width=500)
+    s.table[2, :10] = s.table[1, :10]
+    check_out(s, s.cache().attend(s.q, s.batch()), None, dense(s))
+    good = s.cache().attend(s.q, s.batch())
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    s.table[1, 20] = s.n_pages
+    out = s.cache().attend(s.q, s.batch(), err=err)
+    assert int(err.item()) == 4 and torch.equal(out[171:], good[171:])
+
+    def see(b):
+        m = see_mask(s, b)
+        if b == 1:
+            m[:, 320:336] = False
+        return m
+    s.table[1, 20] = s.table[1, 19]       # for the reference only: these tokens are masked
+    check_out(s, out, None, reference(s, see))
+    s.kv_len[1] = -1
+    err.zero_()
+    left = s.cache().attend(s.q, s.batch(), out=torch.full_like(good, 3.0), err=err)
+    assert int(err.item()) == 4 and torch.equal(left[171:], good[171:]) and (left[1:171] == 3.0).all()
+
+
+def test_tiles_in_a_replayed_graph():
+    s = Scene(BF16, 4, 4, 128, 32, [1, 160, 90], [2000, 1500, 400], seed=53, width=200)
+    c, b = s.cache(), s.batch()
+    out = torch.zeros_like(s.q)
+    c.attend(s.q, b)
+    torch.cuda.synchronize()
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        c.attend(s.q, b, out=out)
+    for total in ([2000, 1500, 400], [64, 1400, 90], [0, 160, 333], [1, 100, 8]):
+        s.kv_len.copy_(torch.tensor(total, dtype=torch.int32))
+        want = c.attend(s.q, b)
+        out.zero_()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, want)
+
+
 def test_two_calls_at_once():
     """Two streams use one cache and one batch, each with its own queries, many times over."""
     s = Scene(BF16, 4, 4, 128, 32, [1, 130, 3], [2000, 1500, 4000], C=32, seed=36, width=200)
