@@ -488,14 +488,16 @@ struct Plan {
 };
 
 constexpr uint32_t kFewRows = 64;    // rows of a sequence that k_rows takes
-// With a row tile of its own for every CU at most, and so many tokens met by all of them together, k_rows takes sequences of
-// any number of rows: without tiles in LDS to fill it is done sooner, until the keys and values that its row tiles read again
-// outweigh that.  Us with k_rows / k_chunk (row tiles, tokens met), 128 channels: 20 new tokens of 32 heads over 2000 (24, 48,000)
-// 15 / 25, 100 of 10 heads over 6000 (32, 192,000) 25 / 32, 4 x 50 of 32 heads over 1000 (224, 224,000) 18 / 28, but 4 x 64 (256, 256,000)
-// 32 / 29, 100 of 32 heads over 6000 (104, 624,000) 44 / 34, a prompt of 256 (256, 66,000) 18 / 15; 64 channels: 60 of 28 heads over 6000
-// (36, 216,000) 23 / 24, 8 x 30 over 3000 (160, 480,000) 28 / 25, a prompt of 512 of 32 heads (344, 176,000) 24 / 15; 256 channels: 8 x 30 of 8 heads
-// over 3000 (64, 192,000) 39 / 45, 8 x 64 (128, 384,000) 66 / 51, 6 x 272 of 8 heads (408, 115,000) 39 / 30.
-constexpr uint64_t kRowTiles = 255, kTileTokens = 250000;
+// With a row tile of its own for every CU at most (every second with 256 channels, whose workgroups fill a CU), and so many
+// tokens met by all of them together, k_rows takes sequences of any number of rows: without tiles in LDS to fill it is done
+// sooner, until the keys and values that its row tiles read again outweigh that.  Us with k_rows / k_chunk (row tiles, tokens
+// met), 128 channels: 20 new tokens of 32 heads over 2000 (24, 48,000) 15 / 25, 100 of 10 heads over 6000 (32, 192,000) 25 / 32, 4 x 50 of 32
+// heads over 1000 (224, 224,000) 18 / 28, but 4 x 64 (256, 256,000) 32 / 29, 100 of 32 heads over 6000 (104, 624,000) 44 / 34, a prompt
+// of 256 (256, 66,000) 18 / 15; 64 channels, 28 heads: 4 x 60 over 1000 (144, 144,000) 19 / 21, 6 x 50 (192, 192,000) 23 / 22, 8 x 30 over 3000 (160,
+// 480,000) 28 / 25; 256 channels, 8 heads: 400 over 1500 (100, 150,000) 37 / 48, 8 x 30 over 3000 (64, 192,000) 39 / 45, 3 x 169 over 1283
+// (132, 169,000) 60 / 43, 8 x 64 over 3000 (128, 384,000) 66 / 51.
+constexpr uint64_t most_row_tiles(uint32_t d) { return d == 256 ? 128 : 255; }
+constexpr uint64_t most_tile_tokens(uint32_t d) { return d == 64 ? 160000 : 250000; }
 // Up to so many bytes of keys and values a row tile, one workgroup of eight waves reads them all, and there is no
 // second launch to join pieces (about 4 us).  A CU draws about 57 bytes a nanosecond, so with few row tiles
 // pieces on several CUs are sooner read from twice 128 KB on; with a workgroup for half the CUs or more, later.
@@ -542,7 +544,7 @@ Plan make_plan(const zx_paged_cache *c, const zx_paged_batch *b, uint32_t n, uin
         // 23 us in tiles of 48, 30 of 32.
         p.mt = D == 64 && most > 32 ? 3 : most > 16 ? 2 : 1;
         const uint64_t row_tiles = ceil_div(most, 16 * p.mt) * (uint64_t)seqs * H;
-        p.chunk = most > kFewRows && (row_tiles > kRowTiles || row_tiles * cap > kTileTokens);
+        p.chunk = most > kFewRows && (row_tiles > most_row_tiles(D) || row_tiles * cap > most_tile_tokens(D));
         // A batch may mix single tokens with long chunks.  k_chunk can serve both; k_rows and its join read the
         // single tokens' caches faster but cost two launches.  Us without / with them, 8 heads of 128 channels: 4 sequences
         // of up to 100 new tokens over 1000 29 / 32, over 4000 39 / 46; 512 new beside 16 single tokens over 2000 60 / 91,
