@@ -487,7 +487,7 @@ struct Plan {
     uint64_t rows_part, rows_stat, chunk_part, chunk_stat, bytes;   // offsets into the workspace
 };
 
-constexpr uint32_t kFewRows = 64;    // rows of a sequence that k_rows takes
+constexpr uint32_t kFewRows = 64;    // rows of a sequence that k_rows takes in any case
 // With a row tile of its own for every CU at most (every second with 256 channels, whose workgroups fill a CU), and so many
 // tokens met by all of them together, k_rows takes sequences of any number of rows: without tiles in LDS to fill it is done
 // sooner, until the keys and values that its row tiles read again outweigh that.  Us with k_rows / k_chunk (row tiles, tokens
