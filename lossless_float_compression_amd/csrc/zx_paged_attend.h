@@ -314,8 +314,15 @@ inline void plan_split(uint32_t tiles, uint32_t room, uint32_t many, uint32_t le
     const uint64_t each = ceil_div(cap, (uint64_t)g.least * unit), all = tiles * each;       // pieces that lengths up to cap may make
     g.slots = each <= 1 ? 0 : all < 2 * g.goal ? (uint32_t)all : 2 * g.goal;
 }
-// Items of the kernel, and row tiles for its join (0: nothing can be split).
-inline uint32_t split_items(uint32_t tiles, const AttendArgs &g) { return !g.slots ? tiles : g.slots < g.goal + tiles ? g.slots : g.goal + tiles; }
+// Items of the kernel, and row tiles for its join (0: nothing can be split).  Row tiles that are not split are items
+// too but have no slot: steps / chunk, rounded up for each of them, makes at most goal + tiles, and no more than all
+// pieces that lengths up to cap may make, which slots holds where that is below 2 * goal (elsewhere goal + tiles is less).
+inline uint32_t split_items(uint32_t tiles, const AttendArgs &g)
+{
+    if (!g.slots) return tiles;
+    const uint32_t most = g.goal + tiles;
+    return g.slots < 2 * g.goal && g.slots < most ? g.slots : most;
+}
 inline uint32_t split_tiles(uint32_t tiles, const AttendArgs &g) { return !g.slots ? 0 : tiles < g.goal ? tiles : g.goal; }
 
 // Workgroups of k_join that share the rows of a row tile: about a thousand in all.
