@@ -335,7 +335,10 @@ class PagedKVCache:
         return sh[0], sh[1]
 
     def _away(self, stream) -> bool:
-        """Whether a call has to change the current device or stream first."""
+        """Whether a call has to change the current device or stream first.  Workspaces and outputs are allocated on the
+        stream that uses them, so a raw handle will not do: memory that the current stream let go would be shared with it."""
+        if stream is not None and not isinstance(stream, torch.Stream):
+            raise ValueError("stream must be a torch stream (torch.cuda.ExternalStream makes one of a raw handle)")
         return torch.cuda.current_device() != self._index or (stream is not None and _zx._side_stream(stream) is not None)
 
     def _elsewhere(self, stream, batch, tensors, call):
@@ -353,11 +356,6 @@ class PagedKVCache:
                 t.record_stream(stream)
         with torch.cuda.stream(stream):
             return call(None)
-
-    def _raw(self, stream) -> int:
-        if isinstance(stream, C.c_void_p):
-            return stream.value
-        return _zx._raw_stream(self.device)
 
     # ---- operators
     def append(self, k: torch.Tensor, v: torch.Tensor, batch: PagedBatch, q: Optional[torch.Tensor] = None,
@@ -377,7 +375,7 @@ class PagedKVCache:
         sequences that are out of range are skipped, their rows of q_out left as they are.
 
         err: device int32 word, 4 where lengths or page ids were out of range.  `stream`: a
-        torch stream to run on after the work already enqueued on the current one."""
+        torch stream (no raw handle) to run on after the work already enqueued on the current one."""
         if self._away(stream):
             return self._elsewhere(stream, batch, (k, v, q, q_out, positions, err, None if rotary is None else rotary.inv_freq),
                                    lambda s: self.append(k, v, batch, q, rotary, positions, q_out, err, s))
@@ -407,7 +405,7 @@ class PagedKVCache:
                 raise ValueError("positions must be [tokens], and need a rotary")
             cp = positions.data_ptr()
         st = _lib().zx_paged_append(self._ref, batch._ref, n, C.byref(ck), C.byref(cv), cr, cp, cq, heads, co, e,
-                                    self._raw(stream))
+                                    _zx._raw_stream(self.device))
         if st != 0:
             raise _zx.ZxError("zx_paged_append", st)
         return q_out
@@ -466,7 +464,7 @@ class PagedKVCache:
             need = batch._needs[key] = L.zx_paged_attend_workspace_bytes(self._ref, batch._ref, n, heads, window, nb)
         ws = self._bytes.new_empty(need) if need else None
         st = L.zx_paged_attend(self._ref, batch._ref, n, C.byref(cq), heads, C.byref(co), pl, scale, causal, window, pb, nb,
-                               ws.data_ptr() if need else None, need, e, self._raw(stream))
+                               ws.data_ptr() if need else None, need, e, _zx._raw_stream(self.device))
         if st != 0:
             raise _zx.ZxError("zx_paged_attend", st)
         return out
@@ -502,7 +500,7 @@ class PagedKVCache:
             need = batch._needs[(self._key, n)] = L.zx_paged_select_workspace_bytes(self._ref, batch._ref, n)
         ws = self._bytes.new_empty(need) if need else None
         st = L.zx_paged_select(self._ref, batch._ref, n, C.byref(cq), heads, top_k, keep_first, keep_last, blocks.data_ptr(),
-                               ws.data_ptr() if need else None, need, e, self._raw(stream))
+                               ws.data_ptr() if need else None, need, e, _zx._raw_stream(self.device))
         if st != 0:
             raise _zx.ZxError("zx_paged_select", st)
         return blocks
