@@ -8,6 +8,8 @@
 // bounds: bound by those bytes.  Which blocks are taken is a yes or no, and two ways of
 // adding up in 32 bits would now and then say differently for blocks next to the border,
 // so the sums are taken in 64 bits (the vector units' 64-bit multiply-add has the rate of the 32-bit one).
+// With finite bounds and queries the two forms are one sum.  An infinite bound (a key that overflowed) times a part that is
+// zero is NaN in the second form only, so a row with a sum that is infinite or NaN has those taken again by the first.
 //
 //   k_pick   one workgroup for a token and K/V head: a key (the sum, as an integer that orders like it)
 //            for each block, in LDS, then the top_k-th largest by radix selection and the
@@ -37,6 +39,7 @@ struct SelectArgs {
     uint32_t nb;                        // blocks of the longest sequence
     uint32_t slab0, slab;               // token groups of this launch: slab0 .. slab0 + slab - 1
     uint32_t per;                       // blocks of a workgroup of k_score
+    uint32_t head_dim;
 };
 
 // An integer that orders like the double; NaN below everything.
@@ -46,6 +49,8 @@ __device__ __forceinline__ uint64_t order_key(double x)
     if (x != x) return 0;
     return b < 0 ? ~(uint64_t)b : (uint64_t)b | 0x8000000000000000ull;
 }
+
+__device__ __forceinline__ bool finite_key(uint64_t x) { return x > 0x000FFFFFFFFFFFFFull && x < 0xFFF0000000000000ull; }
 
 // x of the lane that DPP pattern CTRL names
 template <int CTRL>
@@ -202,13 +207,37 @@ struct Picking {
     uint32_t pick[3];
 };
 
-// Blocks f0 .. f0 + n - 1 compete with their keys for `want` < n places of `out`; the rest of
-// a row's top_k are the blocks in front of them and behind them.  By all NT threads.
-template <uint32_t NT, class Key>
-__device__ __forceinline__ void pick_row(const SelectArgs &g, Key key, uint32_t f0, uint32_t n, uint32_t want, uint64_t least, uint64_t most, int32_t *out, Picking &sh)
+// What a row of the result is about: its token's packed row and sequence, its head.
+struct Place {
+    int64_t row;
+    const int32_t *table;
+    uint32_t h;
+};
+
+// The key of block j from its sum by definition, NaN where any product is; 0 where the block has no page.  By one wave.
+__device__ __forceinline__ uint64_t defined_key(const SelectArgs &g, const Place &at, uint32_t j)
 {
-    constexpr uint32_t NWV = NT / 64;
-    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6, K = g.top_k;
+    const uint32_t lp = g.c.log_page - g.c.log_block, nbp = 1u << lp, D = g.head_dim, page = (uint32_t)at.table[j >> lp];
+    if (page >= g.c.n_pages) return 0;
+    const __bf16 *bp = g.c.bounds + (((uint64_t)page * g.c.heads + at.h) * nbp + (j & (nbp - 1u))) * (2 * D);
+    double s = 0.0;
+    for (uint32_t ch = threadIdx.x & 63u; ch < D; ch += 64) {
+        const double lo = (double)(float)bp[ch], hi = (double)(float)bp[D + ch];
+        const __bf16 *qp = g.q.p + at.row * g.q.token + (int64_t)(at.h * g.group) * g.q.head + ch;
+        for (uint32_t e = 0; e < g.group; ++e) {
+            const double q = (double)(float)qp[(int64_t)e * g.q.head], a = q * lo, b = q * hi;
+            s += a != a ? a : a > b ? a : b;             // (b where it is NaN)
+        }
+    }
+    for (int w = 32; w >= 1; w >>= 1) s += __shfl_xor(s, w, 64);
+    return order_key(s);
+}
+
+// The smallest and the largest key of all NT threads, in all of them.
+template <uint32_t NT>
+__device__ __forceinline__ void join_range(uint64_t &least, uint64_t &most, Picking &sh)
+{
+    const uint32_t lane = threadIdx.x & 63u, wave = threadIdx.x >> 6;
     for (int w = 32; w >= 1; w >>= 1) {
         const uint64_t a = __shfl_xor(least, w, 64), b = __shfl_xor(most, w, 64);
         least = a < least ? a : least;
@@ -219,9 +248,40 @@ __device__ __forceinline__ void pick_row(const SelectArgs &g, Key key, uint32_t 
         sh.wide[1][wave] = most;
     }
     __syncthreads();
-    for (uint32_t w = 0; w < NWV; ++w) {
+    for (uint32_t w = 0; w < NT / 64; ++w) {
         least = sh.wide[0][w] < least ? sh.wide[0][w] : least;
         most = sh.wide[1][w] > most ? sh.wide[1][w] : most;
+    }
+}
+
+// Blocks f0 .. f0 + n - 1 compete with their keys for `want` < n places of `out`; the rest of
+// a row's top_k are the blocks in front of them and behind them.  By all NT threads.
+template <uint32_t NT>
+__device__ __forceinline__ void pick_row(const SelectArgs &g, const Place &place, uint64_t *keys, uint32_t f0, uint32_t n, uint32_t want, uint64_t least, uint64_t most, int32_t *out, Picking &sh)
+{
+    constexpr uint32_t NWV = NT / 64;
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6, K = g.top_k;
+    auto key = [&](uint32_t i) { return keys[i]; };
+    join_range<NT>(least, most, sh);
+    if (!finite_key(least) || !finite_key(most)) {
+        // some sum is infinite or NaN, or some block has no page
+        __syncthreads();
+        least = ~0ull;
+        most = 0;
+        for (uint32_t i0 = 64 * wave; i0 < n; i0 += NT) {
+            const bool in = i0 + lane < n;
+            uint64_t x = in ? key(i0 + lane) : 0;
+            for (uint64_t odd = __ballot(in && !finite_key(x)); odd; odd &= odd - 1) {
+                const uint32_t l = (uint32_t)__builtin_ctzll(odd);
+                const uint64_t y = defined_key(g, place, f0 + i0 + l);
+                if (lane == l) keys[i0 + l] = x = y;
+            }
+            if (in) {
+                least = x < least ? x : least;
+                most = x > most ? x : most;
+            }
+        }
+        join_range<NT>(least, most, sh);
     }
     // keys at or above `cut` in the bits of `mask` are taken, but of those equal to it in
     // these bits only the first `want`
@@ -330,7 +390,7 @@ __global__ __launch_bounds__(kThreads) void k_top(SelectArgs g)
     if (local >= (uint32_t)sv.nq || all_taken(g, sv, local, h, seen, out)) return;
     // blocks f0 .. f0 + n - 1 compete; those before and behind are taken anyway
     const uint32_t f0 = g.keep_first, n = seen - g.keep_last - f0;
-    const uint64_t *src = g.keys + ((uint64_t)row * g.c.heads + h) * g.nb + f0;
+    uint64_t *src = g.keys + ((uint64_t)row * g.c.heads + h) * g.nb + f0;
     const bool in_lds = n <= kHeld;
     uint64_t least = ~0ull, most = 0;
     for (uint32_t i = threadIdx.x; i < n; i += kThreads) {
@@ -340,8 +400,9 @@ __global__ __launch_bounds__(kThreads) void k_top(SelectArgs g)
         most = x > most ? x : most;
     }
     const uint32_t want = g.top_k - g.keep_first - g.keep_last;
-    if (in_lds) pick_row<kThreads>(g, [&](uint32_t i) { return held[i]; }, f0, n, want, least, most, out, sh);
-    else pick_row<kThreads>(g, [&](uint32_t i) { return src[i]; }, f0, n, want, least, most, out, sh);
+    const Place place{sv.q0 + (int64_t)local, g.b.table + (uint64_t)seq * g.b.width, h};
+    if (in_lds) pick_row<kThreads>(g, place, held, f0, n, want, least, most, out, sh);
+    else pick_row<kThreads>(g, place, src, f0, n, want, least, most, out, sh);
 }
 
 constexpr uint32_t kPickThreads = 512;
@@ -387,7 +448,7 @@ __global__ __launch_bounds__(kPickThreads) void k_pick(SelectArgs g)
         }
     }
     __syncthreads();
-    pick_row<kPickThreads>(g, [&](uint32_t i) { return held[i]; }, f0, n, g.top_k - g.keep_first - g.keep_last, least, most, out, sh);
+    pick_row<kPickThreads>(g, Place{sv.q0 + (int64_t)local, table, h}, held, f0, n, g.top_k - g.keep_first - g.keep_last, least, most, out, sh);
 }
 
 // Tokens that share a read of the bounds: with one new token a sequence there is nothing to share.
@@ -473,6 +534,7 @@ extern "C" zx_status zx_paged_select(const zx_paged_cache *cache, const zx_paged
     g.keep_first = keep_first;
     g.keep_last = keep_last;
     g.nb = s.nb;
+    g.head_dim = cache->head_dim;
     g.slab = s.slab;
     if (s.fused) {
         if ((uint64_t)n_tokens * cache->kv_heads * kPickThreads > 0xFFFFFFFFull) return ZX_E_LIMIT;

@@ -69,7 +69,7 @@ class AttendArgs(C.Structure):
 
 class SelectArgs(C.Structure):
     _fields_ = [("c", Cache), ("b", Batch), ("q", Rows), ("blocks", P), ("keys", P), ("group", U32), ("top_k", U32), ("keep_first", U32),
-                ("keep_last", U32), ("nb", U32), ("slab0", U32), ("slab", U32), ("per", U32)]
+                ("keep_last", U32), ("nb", U32), ("slab0", U32), ("slab", U32), ("per", U32), ("head_dim", U32)]
 
 
 class Turn(C.Structure):

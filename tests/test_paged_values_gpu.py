@@ -1,0 +1,103 @@
+"""Infinities, NaN and extreme scales in what the paged K/V cache's operators are given."""
+import math
+import sys
+
+import pytest
+import torch
+
+import lossless_float_compression_amd as zx
+from paged_util import Scene
+
+pytestmark = pytest.mark.gpu
+BF16, FP8 = zx.BF16, zx.FP8_E4M3FN
+INF, NAN = math.inf, math.nan
+
+
+@pytest.fixture(autouse=True)
+def gpu(request):
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    print(request.node.name, file=sys.stderr, flush=True)
+    yield
+    torch.cuda.synchronize()
+
+
+def ranked(s, b, i, h, top_k, keep_first, keep_last):
+    """The blocks of one new token and head by the definition in 64 bits, on the host: sum over heads and channels of
+    max(q lo, q hi), NaN last, ties to the earlier block."""
+    p = s.total[b] - s.new[b] + i
+    last, per = p // s.C, s.T // s.C
+    j = torch.arange(last + 1)
+    bd = s.bounds.cpu()[s.table[b].cpu()[j // per].long(), h, j % per].double()                  # [blocks, 2, D]
+    q = s.q[sum(s.new[:b]) + i].cpu().double().view(s.H, s.G, s.D)[h]
+    z = torch.maximum(q[None] * bd[:, None, 0], q[None] * bd[:, None, 1]).sum((1, 2)).tolist()
+    kept = lambda x: x < keep_first or x > last - keep_last   # noqa: E731
+    order = sorted(range(last + 1), key=lambda x: (not kept(x), math.isnan(z[x]), 0.0 if math.isnan(z[x]) else -z[x], x))
+    got = sorted(order[:top_k])
+    return got + [-1] * (top_k - len(got))
+
+
+def check_select(s, top_k, keep_first=1, keep_last=1, **kw):
+    got = s.cache().select(s.q, s.batch(**kw), top_k, keep_first, keep_last).cpu()
+    for b in range(len(s.new)):
+        for i in range(s.new[b]):
+            for h in range(s.H):
+                want = ranked(s, b, i, h, top_k, keep_first, keep_last)
+                assert got[sum(s.new[:b]) + i, h].tolist() == want, (b, i, h)
+
+
+# what a channel's bounds become (smallest, largest): an overflowed key, two of them, nothing but NaN, nothing but infinities
+ODD_BOUNDS = [(None, INF), (-INF, None), (-INF, INF), (INF, -INF), (INF, INF), (-INF, -INF), (None, NAN), (0.0, INF)]
+# what the queries of the channel are in all heads of the group: one sign, the other, both, none, and odd ones
+QUERIES = {"positive": lambda q: q.abs() + 0.125, "negative": lambda q: -q.abs() - 0.125, "both": lambda q: q, "zero": lambda q: q * 0.0,
+           "infinite": lambda q: q * 0.0 + INF, "NaN": lambda q: q * NAN}
+
+
+@pytest.mark.parametrize("queries", list(QUERIES))
+@pytest.mark.parametrize("G,D,width,new", [(1, 128, 1, [1, 2]), (4, 64, 1, [1, 6]), (3, 256, 1, [1, 1]), (2, 128, 2600, [1, 1]), (4, 128, 2600, [5, 2]),
+                                           (1, 256, 2600, [9, 1])])
+def test_select_of_infinite_bounds(queries, G, D, width, new):
+    s = Scene(BF16, 2, G, D, 32, new, [900, 333], C=16, seed=70, width=width)
+    s.q[..., 5] = QUERIES[queries](s.q[..., 5])
+    for n, (lo, hi) in enumerate(ODD_BOUNDS):
+        for page in s.table[0, 3 + n:20:8].tolist() + s.table[1, n:n + 1].tolist():
+            if lo is not None:
+                s.bounds[page, :, n % 2, 0, 5] = lo
+            if hi is not None:
+                s.bounds[page, :, n % 2, 1, 5] = hi
+    for top_k in (2, 9, 20, 40):
+        check_select(s, top_k, max_q=max(new))
+    check_select(s, 9, 0, 0, max_q=max(new))
+    # the queries' other channels one way too, so that finite sums and their order are left to tell the blocks apart
+    s.q[..., 6:] = s.q[..., 6:].abs()
+    check_select(s, 12, max_q=max(new))
+
+
+def test_appended_infinite_key_keeps_its_block():
+    """A key that overflowed in one channel does not hide its block from queries that are negative there."""
+    s = Scene(BF16, 1, 4, 128, 64, [1], [64 * 12], C=64, seed=71)
+    c, b = s.cache(), s.batch()
+    k = torch.zeros((12 * 64, 1, 128), dtype=torch.bfloat16, device="cuda")
+    k[5 * 64 + 7, 0, 3] = INF
+    k[5 * 64 + 9, 0, 10] = 100.0
+    k[8 * 64 + 1, 0, 10] = 50.0
+    whole = zx.PagedBatch(torch.tensor([0, 12 * 64], dtype=torch.int32, device="cuda"), s.kv_len, s.table)
+    c.append(k, k, whole)
+    s.q.zero_()
+    s.q[..., 10] = 1.0
+    s.q[..., 3] = -1.0
+    assert c.select(s.q, b, 2, 0, 0).cpu().tolist() == [[[5, 8]]]
+
+
+@pytest.mark.parametrize("width", [1, 3000])
+def test_many_blocks_without_pages_and_with_nan(width):
+    """Blocks that have no page come last with those whose bounds are NaN, the earlier first; err is set."""
+    s = Scene(BF16, 1, 2, 64, 16, [1], [16 * 1000], C=16, seed=72, width=width)
+    page = s.table[0, 700].item()
+    s.bounds[page] = NAN
+    s.table[0, 100:400] = -1
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    got = s.cache().select(s.q, s.batch(), 900, 0, 0, err=err).cpu()[0, 0].tolist()
+    assert int(err.item()) == 4
+    last = [j for j in range(1000) if 100 <= j < 400 or j == 700]
+    assert got == sorted([j for j in range(1000) if j not in last] + last[:900 - 699])
