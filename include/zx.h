@@ -441,7 +441,8 @@ zx_status zx_paged_append(const zx_paged_cache *cache, const zx_paged_batch *bat
  * q_heads query heads (a multiple of kv_heads; query head i reads K/V head
  * i / (q_heads / kv_heads)), over the tokens of its sequence up to its own position
  * (causal) or all of them, and, with window > 0, only those less than `window` places
- * before its own.  A row that sees no token is zero, its lse -inf.
+ * before its own.  A row that sees no token is zero, its lse -inf.  Table entries of pages that no row sees (behind
+ * every window) may hold anything.
  *   out     BF16 rows [n_tokens][q_heads][head_dim]
  *   lse     float[n_tokens][q_heads]: ln of the sum of exp(scaled scores), or NULL
  *   scale   positive

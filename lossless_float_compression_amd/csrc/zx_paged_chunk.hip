@@ -101,7 +101,8 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_chunk(AttendArgs 
     auto settle = [&](uint32_t id) {
         const uint32_t t = base * kTile + 16 * lane;
         const bool none = id >= g.c.n_pages;
-        if (none && t < (uint32_t)sv.kv) report(g.b.err, ZX_E_CORRUPT);
+        // (tiles begin at multiples of 64: pages of 16 or 32 tokens that no row sees may have been given away)
+        if (none && t < (uint32_t)hi_max && t + 16 > (uint32_t)lo_min) report(g.b.err, ZX_E_CORRUPT);
         if (none) id = 0;
         kat = (uint64_t)kmem + (uint64_t)((int64_t)id * g.c.k_page) + (uint64_t)(t & pmask) * g.c.k_token;
         vat = (uint64_t)vmem + (uint64_t)((int64_t)id * g.c.v_page) + (uint64_t)(t & pmask) * g.c.v_token;

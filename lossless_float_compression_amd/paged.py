@@ -416,8 +416,8 @@ class PagedKVCache:
         """softmax(scale q.k) v of the new tokens' queries (bf16 [tokens, heads, head_dim], heads a
         multiple of kv_heads; neighbouring heads share a K/V head) over their sequence's tokens:
         up to their own place (causal) or all, and with `window` only those less than `window`
-        places before it.  scale defaults to head_dim^-1/2.  A row that sees no token is zero.  `out`
-        may be q itself.
+        places before it (table entries of pages behind every window may hold anything).  scale defaults to
+        head_dim^-1/2.  A row that sees no token is zero.  `out` may be q itself.
 
         blocks: int32 [tokens, kv_heads, n] (from `select`, or any list): only these blocks of
         block_tokens tokens, counted from the sequence's start, are read; a list ends at its first

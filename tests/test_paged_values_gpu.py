@@ -101,3 +101,27 @@ def test_many_blocks_without_pages_and_with_nan(width):
     assert int(err.item()) == 4
     last = [j for j in range(1000) if 100 <= j < 400 or j == 700]
     assert got == sorted([j for j in range(1000) if j not in last] + last[:900 - 699])
+
+
+@pytest.mark.parametrize("dtype", [BF16, FP8])
+@pytest.mark.parametrize("T", [16, 32, 64])
+@pytest.mark.parametrize("H,new,total,width", [(2, [1], [700], 1), (2, [7], [700], 1), (2, [170], [700], 1), (8, [170, 200], [700, 931], 1),
+                                               (8, [170, 1, 190], [5000, 400, 3333], 900), (8, [300], [20011], 2)])
+@pytest.mark.parametrize("window", [17, 50, 129])
+def test_pages_behind_the_window_given_away(dtype, T, H, new, total, width, window):
+    """Table entries of pages that no new token sees any more may hold anything; one page later is missed."""
+    s = Scene(dtype, H, 4, 128, T, new, total, seed=73, width=width)
+    c, b = s.cache(), s.batch()
+    for causal in (True, False):
+        want = c.attend(s.q, b, window=window, causal=causal)
+        keep = s.table.clone()
+        gone = [max(0, y - n - window + 1) // T for n, y in zip(new, total)]
+        for i, n in enumerate(gone):
+            s.table[i, :n] = -1
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        got = c.attend(s.q, b, window=window, causal=causal, err=err)
+        assert int(err.item()) == 0 and torch.equal(got, want)
+        s.table[0, gone[0]] = -1
+        c.attend(s.q, b, window=window, causal=causal, err=err)
+        assert int(err.item()) == 4
+        s.table.copy_(keep)
