@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import lossless_float_compression_amd as zx
-from paged_util import Scene
+from paged_util import Scene, check_out, reference, see_mask
 
 pytestmark = pytest.mark.gpu
 BF16, FP8 = zx.BF16, zx.FP8_E4M3FN
@@ -125,3 +125,14 @@ def test_pages_behind_the_window_given_away(dtype, T, H, new, total, width, wind
         c.attend(s.q, b, window=window, causal=causal, err=err)
         assert int(err.item()) == 4
         s.table.copy_(keep)
+
+
+@pytest.mark.parametrize("H,new,total", [(2, [1, 3], [700, 90]), (8, [300, 200], [400, 931])])
+def test_scales_whose_product_is_below_any_float(H, new, total):
+    """Scores of zero, by a scale and a k_scale that are both positive: every seen token weighs the same, masked ones nothing."""
+    s = Scene(FP8, H, 4, 128, 64, new, total, seed=74)
+    s.ks.fill_(1e-30)
+    for causal, window in ((True, 0), (False, 0), (True, 100)):
+        out, lse = torch.full_like(s.q, NAN), torch.full(s.q.shape[:2], NAN, device="cuda")
+        s.cache().attend(s.q, s.batch(), scale=1e-20, causal=causal, window=window, out=out, lse=lse)
+        check_out(s, out, lse, reference(s, lambda b: see_mask(s, b, causal, window), 1e-20))
