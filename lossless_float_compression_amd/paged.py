@@ -22,6 +22,7 @@ import math
 from typing import Optional, Tuple, Union
 
 import torch
+import torch.autograd.forward_ad as _forward
 
 from . import zx as _zx
 
@@ -93,6 +94,14 @@ def _int32(t, name: str, index: Optional[int] = None) -> torch.Tensor:
     if index is not None and t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, the cache on cuda:{index}")
     return t
+
+
+def _no_gradient(t: torch.Tensor, name: str) -> None:
+    """Refuse a tensor that autograd, of either mode, would want the result to follow from."""
+    if (t.requires_grad and torch.is_grad_enabled()) or (
+            _forward._current_level >= 0 and _forward.unpack_dual(t).tangent is not None):
+        raise ValueError(f"{name} requires a gradient, which these operators do not have: detach it or use torch.no_grad() "
+                         "(a tangent is carried there too)")
 
 
 def _apart(sizes, strides, width: int) -> bool:
@@ -304,8 +313,8 @@ class PagedKVCache:
                              f"{'heads' if heads is None else heads}, {self.head_dim}], got {t.dtype} {list(sh)}")
         if t.get_device() != self._index:
             raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
-        if t.requires_grad and torch.is_grad_enabled():
-            raise ValueError(f"{name} requires a gradient, which these operators do not have: detach it or use torch.no_grad()")
+        if t.requires_grad or _forward._current_level >= 0:
+            _no_gradient(t, name)
         s0, s1, s2 = t.stride()
         p = t.data_ptr()
         if s2 != 1 or s1 != sh[2] or s0 != s1 * sh[1]:           # (contiguous rows meet all that is asked for below)
@@ -324,6 +333,9 @@ class PagedKVCache:
     def _common(self, batch: PagedBatch, err: Optional[torch.Tensor]):
         if batch._index != self._index:
             raise ValueError(f"the batch is on {batch.device}, the cache on {self.device}")
+        for t in self._tensors:
+            if t.requires_grad:
+                _no_gradient(t, "a tensor of the cache")
         if err is not None:
             return _int32(err, "err", self._index).data_ptr()
         return None
@@ -398,6 +410,7 @@ class PagedKVCache:
         if rotary is not None:
             if rotary.dims > self.head_dim or rotary.inv_freq.device != self.device:
                 raise ValueError("rotary turns more channels than a head has, or is on another device")
+            _no_gradient(rotary.inv_freq, "inv_freq")
             cr = rotary._ref
         cp = None
         if positions is not None:
@@ -445,6 +458,7 @@ class PagedKVCache:
         if lse is not None:
             if lse.dtype is not torch.float32 or lse.shape != (n, heads) or lse.get_device() != self._index or not lse.is_contiguous():
                 raise ValueError("lse must be a contiguous float32 device tensor [tokens, heads]")
+            _no_gradient(lse, "lse")
             pl = lse.data_ptr()
         nb = 0
         if blocks is not None:

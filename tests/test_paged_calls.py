@@ -22,3 +22,31 @@ def test_raw_streams_are_refused(stream):
     for call in (lambda: c.append(t, t, None, stream=stream), lambda: c.attend(t, None, stream=stream), lambda: c.select(t, None, 4, stream=stream)):
         with pytest.raises(ValueError, match="torch stream"):
             call()
+
+
+def test_gradients_are_refused():
+    """Inputs that autograd follows, in either mode, and a cache whose own tensors it follows."""
+    import torch.autograd.forward_ad as forward
+
+    c, t = bare(), torch.zeros((3, 4, 128), dtype=torch.bfloat16)
+    assert c._rows(t, "q", None, None).token_stride == 4 * 128
+    wants = t.clone().requires_grad_()
+    with pytest.raises(ValueError, match="gradient"):
+        c._rows(wants, "q", None, None)
+    with torch.no_grad():
+        c._rows(wants, "q", None, None)
+    with forward.dual_level():
+        dual = forward.make_dual(t, torch.ones_like(t))
+        with pytest.raises(ValueError, match="gradient"):
+            c._rows(dual, "q", None, None)
+        with torch.no_grad(), pytest.raises(ValueError, match="gradient"):       # (tangents are carried without grad mode)
+            c._rows(dual, "q", None, None)
+        c._rows(t, "q", None, None)
+    batch = type("Batch", (), dict(_index=-1, device="cpu"))
+    c._tensors = (t, torch.ones(2))
+    assert c._common(batch, None) is None
+    c._tensors = (t, torch.ones(2, requires_grad=True))
+    with pytest.raises(ValueError, match="gradient"):
+        c._common(batch, None)
+    with torch.no_grad():
+        assert c._common(batch, None) is None
