@@ -27,6 +27,7 @@ import torch.autograd.forward_ad as _forward
 from . import zx as _zx
 
 _ANY = 0x7FFFFFFF
+_MOST_NEEDS = 256                        # workspace sizes that a batch remembers
 
 
 class zx_paged_cache(C.Structure):
@@ -211,6 +212,13 @@ class PagedBatch:
                                  _ANY if max_kv is None else min(int(max_kv), _ANY), q_start.data_ptr(),
                                  kv_len.data_ptr(), page_table.data_ptr())
         self._ref = C.byref(self._c)
+
+    def _ask(self, key, f, *args) -> int:
+        """The workspace size `f(*args)`, remembered under `key` (the oldest is let go when there are many)."""
+        need = self._needs[key] = f(*args)
+        if len(self._needs) > _MOST_NEEDS:
+            del self._needs[next(iter(self._needs))]
+        return need
 
 
 class PagedKVCache:
@@ -475,7 +483,7 @@ class PagedKVCache:
         key = (self._key, n, heads, window, nb)
         need = batch._needs.get(key)
         if need is None:
-            need = batch._needs[key] = L.zx_paged_attend_workspace_bytes(self._ref, batch._ref, n, heads, window, nb)
+            need = batch._ask(key, L.zx_paged_attend_workspace_bytes, self._ref, batch._ref, n, heads, window, nb)
         ws = self._bytes.new_empty(need) if need else None
         st = L.zx_paged_attend(self._ref, batch._ref, n, C.byref(cq), heads, C.byref(co), pl, scale, causal, window, pb, nb,
                                ws.data_ptr() if need else None, need, e, _zx._raw_stream(self.device))
@@ -511,7 +519,7 @@ class PagedKVCache:
         L = _lib()
         need = batch._needs.get((self._key, n))
         if need is None:
-            need = batch._needs[(self._key, n)] = L.zx_paged_select_workspace_bytes(self._ref, batch._ref, n)
+            need = batch._ask((self._key, n), L.zx_paged_select_workspace_bytes, self._ref, batch._ref, n)
         ws = self._bytes.new_empty(need) if need else None
         st = L.zx_paged_select(self._ref, batch._ref, n, C.byref(cq), heads, top_k, keep_first, keep_last, blocks.data_ptr(),
                                ws.data_ptr() if need else None, need, e, _zx._raw_stream(self.device))

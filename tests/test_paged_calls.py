@@ -50,3 +50,12 @@ def test_gradients_are_refused():
         c._common(batch, None)
     with torch.no_grad():
         assert c._common(batch, None) is None
+
+
+def test_a_batch_remembers_only_so_many_sizes():
+    """A long-lived batch that is called with ever other numbers of rows."""
+    b = object.__new__(zx.PagedBatch)
+    b._needs = {}
+    for n in range(2000):
+        assert b._ask(("sizes", n), lambda x: 3 * x, n) == 3 * n and b._needs[("sizes", n)] == 3 * n
+    assert len(b._needs) <= 256
