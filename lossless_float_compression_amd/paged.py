@@ -214,10 +214,10 @@ class PagedBatch:
         self._ref = C.byref(self._c)
 
     def _ask(self, key, f, *args) -> int:
-        """The workspace size `f(*args)`, remembered under `key` (the oldest is let go when there are many)."""
+        """The workspace size `f(*args)`, remembered under `key` (all are let go when there are many)."""
+        if len(self._needs) >= _MOST_NEEDS:
+            self._needs.clear()
         need = self._needs[key] = f(*args)
-        if len(self._needs) > _MOST_NEEDS:
-            del self._needs[next(iter(self._needs))]
         return need
 
 
