@@ -115,6 +115,22 @@ def _apart(sizes, strides, width: int) -> bool:
     return True
 
 
+def _meet(a, b, offset: int, width: int) -> bool:
+    """Whether rows of `width` elements at the strides of `a` and, `offset` elements on, of `b` may share memory.  `a` and
+    `b` are lists of (stride, n) that are apart in themselves, the largest stride first.  Layouts that step alike from the
+    outside in are followed to the rows; where they part, what is left of each counts as one stretch."""
+    reach = lambda x: sum(st * (n - 1) for st, n in x) + width   # noqa: E731
+    if offset >= reach(a) or -offset >= reach(b):
+        return False
+    if not a or not b or a[0] != b[0]:
+        return True
+    st, n = a[0]
+    a, b = a[1:], b[1:]
+    least = -((offset + reach(b) - 1) // st)                  # steps of b less those of a for which the rest may meet
+    most = (reach(a) - 1 - offset) // st
+    return any(_meet(a, b, offset + m * st, width) for m in range(max(least, 1 - n), min(most, n - 1) + 1))
+
+
 class Rotary:
     """Rotary positions: in the first `dims` channels of a head (a multiple of 16), pair j
     is turned by position * inv_freq[j] and scaled by `magnitude`.  Pairs are channels
@@ -272,7 +288,8 @@ class PagedKVCache:
                 raise ValueError(f"{name}: channels must be contiguous and the other strides multiples of 16 bytes")
             if t.stride(2) < self.head_dim or not _apart(t.shape[:3], t.stride()[:3], self.head_dim):
                 raise ValueError(f"{name}: rows must not overlap")
-        if k.data_ptr() == v.data_ptr():
+        steps = lambda t: sorted(((st, n) for st, n in zip(t.stride()[:3], shape[:3]) if n > 1), reverse=True)   # noqa: E731
+        if _meet(steps(k), steps(v), (v.data_ptr() - k.data_ptr()) // k.element_size(), self.head_dim):
             raise ValueError("k and v must be pages of their own")
         self.k, self.v = k, v
         self.k_scale, self.v_scale = (self._scale(s, n) for s, n in ((k_scale, "k_scale"), (v_scale, "v_scale")))

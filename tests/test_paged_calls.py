@@ -59,3 +59,41 @@ def test_a_batch_remembers_only_so_many_sizes():
     for n in range(2000):
         assert b._ask(("sizes", n), lambda x: 3 * x, n) == 3 * n and b._needs[("sizes", n)] == 3 * n
     assert len(b._needs) <= 256
+
+
+def rows_of(shape, strides, offset, width):
+    """Every element of the rows, as a set."""
+    at = [offset]
+    for n, st in zip(shape, strides):
+        at = [x + i * st for x in at for i in range(n)]
+    return {x + c for x in at for c in range(width)}
+
+
+def test_keys_and_values_that_share_memory():
+    """Pages side by side, one inside the other's strides, and any offset between: none that share is taken for apart, and the
+    layouts that keep keys and values of a page, a token or a head together are not taken for shared."""
+    steps = lambda shape, strides: sorted(((st, n) for st, n in zip(strides, shape) if n > 1), reverse=True)   # noqa: E731
+    P, H, T, D = 3, 2, 4, 8
+    shape = (P, H, T)
+    heads, tokens = (H * T * D, T * D, D), (H * T * D, D, H * D)
+    good = [(heads, heads, P * H * T * D), (tokens, tokens, P * H * T * D), (heads, tokens, P * H * T * D),         # two allocations
+            ((2 * H * T * D, T * D, D), (2 * H * T * D, T * D, D), H * T * D),                                      # [page, 2, head, token, D]
+            ((2 * H * T * D, T * D, D), (2 * H * T * D, D, H * D), H * T * D),                                      # the same, values by token
+            ((2 * H * T * D, 2 * T * D, D), (2 * H * T * D, 2 * T * D, D), T * D),                                  # [page, head, 2, token, D]
+            ((2 * H * T * D, D, 2 * H * D), (2 * H * T * D, D, 2 * H * D), H * D),                                  # [page, token, 2, head, D]
+            ((2 * H * T * D, 2 * D, 2 * H * D), (2 * H * T * D, 2 * D, 2 * H * D), D)]                              # [page, token, head, 2, D]
+    for a, b, off in good:
+        assert not rows_of(shape, a, 0, D) & rows_of(shape, b, off, D)
+        assert not zx.paged._meet(steps(shape, a), steps(shape, b), off, D), (a, b, off)
+        assert not zx.paged._meet(steps(shape, b), steps(shape, a), -off, D), (a, b, off)
+    layouts = {x for g in good for x in g[:2]}
+    for a in layouts:
+        mine = rows_of(shape, a, 0, D)
+        for b in layouts:
+            for off in range(-2 * P * H * T * D, 2 * P * H * T * D, 4):
+                shared = bool(mine & rows_of(shape, b, off, D))
+                meet = zx.paged._meet(steps(shape, a), steps(shape, b), off, D)
+                assert meet or not shared, (a, b, off)
+                if a == b:                                      # exact where both step alike
+                    assert meet == shared, (a, b, off)
+    assert zx.paged._meet([], [], 0, 8) and zx.paged._meet([], [], 7, 8) and not zx.paged._meet([], [], 8, 8)

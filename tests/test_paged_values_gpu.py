@@ -136,3 +136,13 @@ def test_scales_whose_product_is_below_any_float(H, new, total):
         out, lse = torch.full_like(s.q, NAN), torch.full(s.q.shape[:2], NAN, device="cuda")
         s.cache().attend(s.q, s.batch(), scale=1e-20, causal=causal, window=window, out=out, lse=lse)
         check_out(s, out, lse, reference(s, lambda b: see_mask(s, b, causal, window), 1e-20))
+
+
+def test_keys_and_values_that_share_pages_are_refused():
+    both = torch.zeros((6, 2, 16, 128), dtype=torch.bfloat16, device="cuda")
+    pair = torch.zeros((5, 2, 2, 16, 128), dtype=torch.bfloat16, device="cuda")
+    for k, v in ((both[:5], both[:5]), (both[:5], both[1:]), (both[1:], both[:5]), (pair[:4, 0], pair[1:, 0]), (pair[:, 0], pair[:, 0])):
+        with pytest.raises(ValueError, match="of their own"):
+            zx.PagedKVCache(k.shape[0], 2, 128, 16, k=k, v=v)
+    for k, v in ((both[:3], both[3:]), (pair[:, 0], pair[:, 1]), (pair[:, 1], pair[:, 0]), (pair[:3, 1], pair[2:, 0])):
+        zx.PagedKVCache(k.shape[0], 2, 128, 16, k=k, v=v)
