@@ -556,6 +556,8 @@ class PagedKVCache:
         """(which ids are pages, the ids with any page for the others, the slots with none for the others)"""
         if pool.dtype != self.dtype:
             raise TypeError("the pool has another dtype than the cache")
+        if pool.signmant.device != self.device:
+            raise ValueError(f"the pool is on {pool.signmant.device}, the cache on {self.device}")
         if not torch.is_tensor(pages) or pages.dtype not in (torch.int32, torch.int64) or pages.dim() != 1 or pages.device != self.device:
             raise ValueError("pages must be a device integer tensor [n]")
         _int32(slots, "slots", self._index)
@@ -576,7 +578,11 @@ class PagedKVCache:
         pages[i] into slots[0, i], its values into slots[1, i] (device int32 [2, n, blocks_per_page()],
         distinct).  Returns (status, bounds): status [2, n, blocks_per_page()] is 0, or 6 for a block
         that did not fit its slot (keep that page), or 1 where the page or the slot is none; bounds are the pages' rows of `self.bounds`,
-        for `restore` (None without bounds).  The pages themselves are left as they are."""
+        for `restore` (None without bounds).  The pages themselves are left as they are.  Runs on the current stream of the
+        cache's device."""
+        if torch.cuda.current_device() != self._index:
+            with torch.cuda.device(self.device):
+                return self.stow(pages, pool, slots, err)
         _, ids, slots = self._page_ids(pages, pool, slots)
         if slots.numel() == 0:
             return torch.empty_like(slots), None if self.bounds is None else self.bounds[ids]
@@ -587,7 +593,10 @@ class PagedKVCache:
                 err: Optional[torch.Tensor] = None) -> None:
         """Bring stowed pages back, bit for bit, into pages pages[i] (any free ones, distinct), and
         their bounds with them.  A block whose slot is empty keeps what the page holds; ids that are
-        no page are left out, with 4 in `err`."""
+        no page are left out, with 4 in `err`.  Stream: as `stow`."""
+        if torch.cuda.current_device() != self._index:
+            with torch.cuda.device(self.device):
+                return self.restore(pages, pool, slots, bounds, err)
         ok, ids, slots = self._page_ids(pages, pool, slots)
         if (bounds is None) != (self.bounds is None):
             raise ValueError("give the bounds that stow returned")

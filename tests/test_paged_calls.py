@@ -97,3 +97,47 @@ def test_keys_and_values_that_share_memory():
                 if a == b:                                      # exact where both step alike
                     assert meet == shared, (a, b, off)
     assert zx.paged._meet([], [], 0, 8) and zx.paged._meet([], [], 7, 8) and not zx.paged._meet([], [], 8, 8)
+
+
+class Pool:
+    """What stow and restore need of a slot pool, noting the device that is current when its launches would run."""
+
+    def __init__(self, current):
+        self.dtype, self.signmant, self.current, self.ran = zx.BF16, torch.zeros(1), current, []
+
+    def append(self, blocks, slots, err=None):
+        self.ran.append(self.current[0])
+        return torch.zeros_like(slots)
+
+    def decode(self, slots, out, err=None):
+        self.ran.append(self.current[0])
+
+
+def test_stow_and_restore_run_on_the_device_of_the_cache(monkeypatch):
+    """With another device current, the pool's launches would go to that one's stream; a pool on another device is refused."""
+    current = [0]
+
+    class Device:
+        def __init__(self, d):
+            self.d = 1
+
+        def __enter__(self):
+            self.old, current[0] = current[0], self.d
+
+        def __exit__(self, *a):
+            current[0] = self.old
+
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: current[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(zx.paged, "_int32", lambda t, *a: t)
+    raw = torch.zeros((2, 1, 512, 128), dtype=torch.bfloat16)
+    c = bare(_index=1, k=raw, v=raw.clone(), bounds=None, n_pages=2, kv_heads=1, page_tokens=512, torch_dtype=torch.bfloat16)
+    pool = Pool(current)
+    pages, slots = torch.tensor([1]), torch.tensor([[[0]], [[1]]], dtype=torch.int32)
+    c.stow(pages, pool, slots)
+    c.restore(pages, pool, slots)
+    assert pool.ran == [1, 1] and current == [0]
+    pool.signmant = torch.zeros(1, device="meta")
+    for call in (lambda: c.stow(pages, pool, slots), lambda: c.restore(pages, pool, slots)):
+        with pytest.raises(ValueError, match="the pool is on"):
+            call()
