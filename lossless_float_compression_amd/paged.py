@@ -338,7 +338,7 @@ class PagedKVCache:
                              f"{'heads' if heads is None else heads}, {self.head_dim}], got {t.dtype} {list(sh)}")
         if t.get_device() != self._index:
             raise ValueError(f"{name} is on {t.device}, the cache on {self.device}")
-        if t.requires_grad or _forward._current_level >= 0:
+        if t.requires_grad:
             _no_gradient(t, name)
         s0, s1, s2 = t.stride()
         p = t.data_ptr()
@@ -355,12 +355,16 @@ class PagedKVCache:
             raise ValueError(f"{name} must start at a multiple of 16 bytes")
         return zx_rows(p, s0, s1)
 
-    def _common(self, batch: PagedBatch, err: Optional[torch.Tensor]):
+    def _common(self, batch: PagedBatch, err: Optional[torch.Tensor], *given: Optional[torch.Tensor]):
         if batch._index != self._index:
             raise ValueError(f"the batch is on {batch.device}, the cache on {self.device}")
         for t in self._tensors:
             if t.requires_grad:
                 _no_gradient(t, "a tensor of the cache")
+        if _forward._current_level >= 0:
+            for t in (*given, *self._tensors):
+                if t is not None:
+                    _no_gradient(t, "an argument")
         if err is not None:
             return _int32(err, "err", self._index).data_ptr()
         return None
@@ -416,7 +420,7 @@ class PagedKVCache:
         if self._away(stream):
             return self._elsewhere(stream, batch, (k, v, q, q_out, positions, err, None if rotary is None else rotary.inv_freq),
                                    lambda s: self.append(k, v, batch, q, rotary, positions, q_out, err, s))
-        e = self._common(batch, err)
+        e = self._common(batch, err, k, v, q, q_out, None if rotary is None else rotary.inv_freq)
         n = k.shape[0]
         ck, cv = self._rows(k, "k", self.kv_heads, None), self._rows(v, "v", self.kv_heads, n)
         cq = co = None
@@ -435,7 +439,8 @@ class PagedKVCache:
         if rotary is not None:
             if rotary.dims > self.head_dim or rotary.inv_freq.device != self.device:
                 raise ValueError("rotary turns more channels than a head has, or is on another device")
-            _no_gradient(rotary.inv_freq, "inv_freq")
+            if rotary.inv_freq.requires_grad:
+                _no_gradient(rotary.inv_freq, "inv_freq")
             cr = rotary._ref
         cp = None
         if positions is not None:
@@ -467,7 +472,7 @@ class PagedKVCache:
         if self._away(stream):
             return self._elsewhere(stream, batch, (q, out, lse, err, blocks),
                                    lambda s: self.attend(q, batch, scale, causal, window, blocks, out, lse, err, s))
-        e = self._common(batch, err)
+        e = self._common(batch, err, q, out, lse)
         n, heads = self._group(q)
         cq = self._rows(q, "q", None, None)
         if out is None:
@@ -483,7 +488,8 @@ class PagedKVCache:
         if lse is not None:
             if lse.dtype is not torch.float32 or lse.shape != (n, heads) or lse.get_device() != self._index or not lse.is_contiguous():
                 raise ValueError("lse must be a contiguous float32 device tensor [tokens, heads]")
-            _no_gradient(lse, "lse")
+            if lse.requires_grad:
+                _no_gradient(lse, "lse")
             pl = lse.data_ptr()
         nb = 0
         if blocks is not None:
@@ -519,7 +525,7 @@ class PagedKVCache:
         if self._away(stream):
             return self._elsewhere(stream, batch, (q, blocks, err),
                                    lambda s: self.select(q, batch, top_k, keep_first, keep_last, blocks, err, s))
-        e = self._common(batch, err)
+        e = self._common(batch, err, q)
         n, heads = self._group(q)
         cq = self._rows(q, "q", None, None)
         if self.block_tokens is None:

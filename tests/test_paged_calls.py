@@ -24,10 +24,11 @@ def test_raw_streams_are_refused(stream):
             call()
 
 
-def test_gradients_are_refused():
+def test_gradients_are_refused(monkeypatch):
     """Inputs that autograd follows, in either mode, and a cache whose own tensors it follows."""
     import torch.autograd.forward_ad as forward
 
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: -1)
     c, t = bare(), torch.zeros((3, 4, 128), dtype=torch.bfloat16)
     assert c._rows(t, "q", None, None).token_stride == 4 * 128
     wants = t.clone().requires_grad_()
@@ -35,14 +36,17 @@ def test_gradients_are_refused():
         c._rows(wants, "q", None, None)
     with torch.no_grad():
         c._rows(wants, "q", None, None)
+    batch = type("Batch", (), dict(_index=-1, device="cpu"))
+    c._tensors = (t,)
     with forward.dual_level():
         dual = forward.make_dual(t, torch.ones_like(t))
-        with pytest.raises(ValueError, match="gradient"):
-            c._rows(dual, "q", None, None)
-        with torch.no_grad(), pytest.raises(ValueError, match="gradient"):       # (tangents are carried without grad mode)
-            c._rows(dual, "q", None, None)
-        c._rows(t, "q", None, None)
-    batch = type("Batch", (), dict(_index=-1, device="cpu"))
+        for call in (lambda: c.append(dual, t, batch), lambda: c.append(t, t, batch, q=dual), lambda: c.attend(dual, batch),
+                     lambda: c.attend(t, batch, out=dual), lambda: c.select(dual, batch, 4)):
+            with pytest.raises(ValueError, match="gradient"):
+                call()
+            with torch.no_grad(), pytest.raises(ValueError, match="gradient"):   # (tangents are carried without grad mode)
+                call()
+        assert c._common(batch, None, t, None) is None
     c._tensors = (t, torch.ones(2))
     assert c._common(batch, None) is None
     c._tensors = (t, torch.ones(2, requires_grad=True))
