@@ -310,6 +310,7 @@ class PagedKVCache:
                                  ptr(bounds))
         self._ref = C.byref(self._c)
         self._bytes = torch.empty(0, dtype=torch.uint8, device=self.device)     # what workspaces are allocated like
+        self._gradients = any(t is not None and t.requires_grad for t in (k, v, bounds, self.k_scale, self.v_scale))
         self._tensors = tuple(t for t in (self.k, self.v, self.k_scale, self.v_scale, self.bounds) if t is not None)
 
     def _scale(self, s, name: str) -> Optional[torch.Tensor]:
@@ -355,19 +356,18 @@ class PagedKVCache:
             raise ValueError(f"{name} must start at a multiple of 16 bytes")
         return zx_rows(p, s0, s1)
 
-    def _common(self, batch: PagedBatch, err: Optional[torch.Tensor], *given: Optional[torch.Tensor]):
+    def _common(self, batch: PagedBatch, err: Optional[torch.Tensor]):
         if batch._index != self._index:
             raise ValueError(f"the batch is on {batch.device}, the cache on {self.device}")
-        for t in self._tensors:
-            if t.requires_grad:
-                _no_gradient(t, "a tensor of the cache")
-        if _forward._current_level >= 0:
-            for t in (*given, *self._tensors):
-                if t is not None:
-                    _no_gradient(t, "an argument")
         if err is not None:
             return _int32(err, "err", self._index).data_ptr()
         return None
+
+    def _followed(self, *given: Optional[torch.Tensor]) -> None:
+        """Refuse what autograd follows."""
+        for t in (*given, *self._tensors):
+            if t is not None:
+                _no_gradient(t, "an argument or a tensor of the cache")
 
     def _group(self, q: torch.Tensor) -> Tuple[int, int]:
         sh = q.shape
@@ -420,7 +420,9 @@ class PagedKVCache:
         if self._away(stream):
             return self._elsewhere(stream, batch, (k, v, q, q_out, positions, err, None if rotary is None else rotary.inv_freq),
                                    lambda s: self.append(k, v, batch, q, rotary, positions, q_out, err, s))
-        e = self._common(batch, err, k, v, q, q_out, None if rotary is None else rotary.inv_freq)
+        if self._gradients or _forward._current_level >= 0:
+            self._followed(k, v, q, q_out, None if rotary is None else rotary.inv_freq)
+        e = self._common(batch, err)
         n = k.shape[0]
         ck, cv = self._rows(k, "k", self.kv_heads, None), self._rows(v, "v", self.kv_heads, n)
         cq = co = None
@@ -472,7 +474,9 @@ class PagedKVCache:
         if self._away(stream):
             return self._elsewhere(stream, batch, (q, out, lse, err, blocks),
                                    lambda s: self.attend(q, batch, scale, causal, window, blocks, out, lse, err, s))
-        e = self._common(batch, err, q, out, lse)
+        if self._gradients or _forward._current_level >= 0:
+            self._followed(q, out, lse)
+        e = self._common(batch, err)
         n, heads = self._group(q)
         cq = self._rows(q, "q", None, None)
         if out is None:
@@ -525,7 +529,9 @@ class PagedKVCache:
         if self._away(stream):
             return self._elsewhere(stream, batch, (q, blocks, err),
                                    lambda s: self.select(q, batch, top_k, keep_first, keep_last, blocks, err, s))
-        e = self._common(batch, err, q)
+        if self._gradients or _forward._current_level >= 0:
+            self._followed(q)
+        e = self._common(batch, err)
         n, heads = self._group(q)
         cq = self._rows(q, "q", None, None)
         if self.block_tokens is None:

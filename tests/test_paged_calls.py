@@ -10,7 +10,7 @@ import lossless_float_compression_amd as zx
 def bare(**kw):
     """A cache without device memory, for what happens before any of it is touched."""
     c = object.__new__(zx.PagedKVCache)
-    for k, v in {**dict(_index=-1, device=torch.device("cpu"), head_dim=128, kv_heads=2, block_tokens=16, dtype=zx.BF16), **kw}.items():
+    for k, v in {**dict(_index=-1, device=torch.device("cpu"), head_dim=128, kv_heads=2, block_tokens=16, dtype=zx.BF16, _gradients=False), **kw}.items():
         setattr(c, k, v)
     return c
 
@@ -46,14 +46,13 @@ def test_gradients_are_refused(monkeypatch):
                 call()
             with torch.no_grad(), pytest.raises(ValueError, match="gradient"):   # (tangents are carried without grad mode)
                 call()
-        assert c._common(batch, None, t, None) is None
-    c._tensors = (t, torch.ones(2))
-    assert c._common(batch, None) is None
-    c._tensors = (t, torch.ones(2, requires_grad=True))
-    with pytest.raises(ValueError, match="gradient"):
-        c._common(batch, None)
+        c._followed(t, None)
+    c._gradients, c._tensors = True, (t, torch.ones(2, requires_grad=True))
+    for call in (lambda: c.append(t, t, batch), lambda: c.attend(t, batch), lambda: c.select(t, batch, 4)):
+        with pytest.raises(ValueError, match="gradient"):
+            call()
     with torch.no_grad():
-        assert c._common(batch, None) is None
+        c._followed(t, None)
 
 
 def test_a_batch_remembers_only_so_many_sizes():

@@ -146,3 +146,20 @@ def test_keys_and_values_that_share_pages_are_refused():
             zx.PagedKVCache(k.shape[0], 2, 128, 16, k=k, v=v)
     for k, v in ((both[:3], both[3:]), (pair[:, 0], pair[:, 1]), (pair[:, 1], pair[:, 0]), (pair[:3, 1], pair[2:, 0])):
         zx.PagedKVCache(k.shape[0], 2, 128, 16, k=k, v=v)
+
+
+def test_a_cache_that_autograd_follows_is_refused():
+    s = Scene(FP8, 2, 2, 128, 16, [1, 2], [30, 20], C=16, seed=76)
+    b = s.batch()
+    rows = torch.zeros((3, 2, 128), dtype=torch.bfloat16, device="cuda")
+    want = s.cache().attend(s.q, b)
+    s.ks.requires_grad_()
+    c = s.cache()
+    for call in (lambda: c.attend(s.q, b), lambda: c.select(s.q, b, 2), lambda: c.append(rows, rows, b)):
+        with pytest.raises(ValueError, match="gradient"):
+            call()
+    rotary = zx.Rotary(64, inv_freq=torch.ones(32, dtype=torch.float64, device="cuda").requires_grad_())
+    with pytest.raises(ValueError, match="gradient"):
+        Scene(BF16, 2, 2, 128, 16, [1, 2], [30, 20], seed=76).cache().append(rows, rows, b, rotary=rotary)
+    with torch.no_grad():
+        assert torch.equal(c.attend(s.q, b), want)
