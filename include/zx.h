@@ -424,7 +424,7 @@ typedef struct zx_rotary {
 
 /* Append the new tokens' keys and values to the cache, rotated on the way (`rot` not
  * NULL), and write the queries rotated the same way to q_out (q not NULL; q_out may be
- * q itself).  Keys are rotated in 32 bits and rounded once, to BF16 or, divided by the
+ * q itself, and must not overlap it otherwise).  Keys are rotated in 32 bits and rounded once, to BF16 or, divided by the
  * head's scale, to E4M3 (saturating; NaN stays NaN); angles are taken in 64 bits.
  *   n_tokens    packed rows of k, v and q
  *   positions   int32[n_tokens] for the rotation, or NULL: the tokens' places
@@ -453,7 +453,8 @@ zx_status zx_paged_append(const zx_paged_cache *cache, const zx_paged_batch *bat
  *   workspace  zx_paged_attend_workspace_bytes(...) bytes, 16-byte aligned; its contents
  *           do not matter before the call or after it
  * Scores, the softmax's sums and the output are accumulated in 32 bits; weights are
- * rounded to BF16 before they meet the values.  Equal inputs give equal bits.  out may be q. */
+ * rounded to BF16 before they meet the values.  Equal inputs give equal bits.  out may be q, and must not overlap
+ * it otherwise. */
 size_t zx_paged_attend_workspace_bytes(const zx_paged_cache *cache, const zx_paged_batch *batch,
                                        uint32_t n_tokens, uint32_t q_heads, uint32_t window, uint32_t n_blocks);
 zx_status zx_paged_attend(const zx_paged_cache *cache, const zx_paged_batch *batch, uint32_t n_tokens,

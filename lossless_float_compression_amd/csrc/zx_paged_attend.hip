@@ -22,9 +22,10 @@
 //            4096 new tokens 151 us, 910 TFLOP/s; 2 x 777 over 32768 620 us, 870 TFLOP/s (a large matrix product: 1140 to 1370).
 //   k_join   adds up what the workgroups of one row left.
 //
-// Roundings: weights go into the second product as BF16, the matrix unit's type (2^-9 each, half of it lost
-// again in the sum over tokens; 32-bit weights would take two products and halve the rate), the result is
-// rounded to BF16; scores, maxima, sums and products are 32-bit.
+// Roundings: weights go into the second product as BF16, the matrix unit's type: up to 2^-8 of each, either way, so
+// an output is off by at most 2^-8 of sum w |v| for it beside the 2^-8 of its own rounding to BF16 (rms against 64 bits over the
+// cases timed here: 0.0023 of the output, 0.0016 with weights of 32 bits).  Weights of 32 bits would take two products
+// and halve the rate.  Scores, maxima, the sums of the weights (of the unrounded ones) and products are 32-bit.
 #include "zx_paged_attend.h"
 
 namespace zxp {

@@ -242,7 +242,7 @@ class PagedKVCache:
     head_dim (64, 128 or 256) channels, BF16 or FP8 E4M3.
 
     k, v           the pages, [n_pages, kv_heads, page_tokens, head_dim]; allocated (zeroed) here, or
-                   given: any strides that are multiples of 16 bytes, channels contiguous
+                   given, apart from each other: any strides that are multiples of 16 bytes, channels contiguous
                    (so [n_pages, page_tokens, kv_heads, head_dim] pages are given as `.transpose(1, 2)`)
     k_scale, v_scale  FP8: a stored value x stands for x * scale[head] (a positive number, or a
                    device float32 tensor [kv_heads])
@@ -406,7 +406,7 @@ class PagedKVCache:
         places, keys rotated by `rotary`, rounded to the cache's type (FP8: divided by the
         head's scale, saturating), and widen the bounds of the blocks they fall into.  With
         `q` (bf16 [tokens, heads, head_dim]) the queries are rotated too, into q_out (allocated
-        when None; q itself is fine), which is returned.
+        when None; q itself is fine, another overlap is not), which is returned.
 
         positions: device int32 [tokens] to rotate by, instead of the tokens' places.  Pages
         that are written must belong to one sequence only.  A token written at a place that
@@ -462,7 +462,7 @@ class PagedKVCache:
         multiple of kv_heads; neighbouring heads share a K/V head) over their sequence's tokens:
         up to their own place (causal) or all, and with `window` only those less than `window`
         places before it (table entries of pages behind every window may hold anything).  scale defaults to
-        head_dim^-1/2.  A row that sees no token is zero.  `out` may be q itself.
+        head_dim^-1/2.  A row that sees no token is zero.  `out` may be q itself, and must not overlap it otherwise.
 
         blocks: int32 [tokens, kv_heads, n] (from `select`, or any list): only these blocks of
         block_tokens tokens, counted from the sequence's start, are read; a list ends at its first
