@@ -208,7 +208,7 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : 2) void k_chunk(AttendArgs 
 #pragma unroll
         for (int i = 0; i < 16; ++i) o[d][i] = 0.0f;
     // (not zero where a tiny scale meets a tiny k_scale: a masked score is -inf until it is multiplied)
-    const float c = fmaxf(g.scale * (g.c.k_scale ? g.c.k_scale[h] : 1.0f), 0x1p-149f);
+    const float c0 = g.scale * (g.c.k_scale ? g.c.k_scale[h] : 1.0f), c = c0 == 0.0f ? 0x1p-149f : c0;
 
     typedef __attribute__((address_space(3))) const uint8_t *lds_ptr;
     const lds_ptr kp = (lds_ptr)&kl[0][0] + lr * KS + 16 * lh;

@@ -163,3 +163,12 @@ def test_a_cache_that_autograd_follows_is_refused():
         Scene(BF16, 2, 2, 128, 16, [1, 2], [30, 20], seed=76).cache().append(rows, rows, b, rotary=rotary)
     with torch.no_grad():
         assert torch.equal(c.attend(s.q, b), want)
+
+
+@pytest.mark.parametrize("H,new,total", [(2, [1, 3], [700, 90]), (8, [300, 200], [400, 931])])
+def test_a_scale_that_is_nan_shows(H, new, total):
+    s = Scene(FP8, H, 4, 128, 64, new, total, seed=77)
+    want = s.cache().attend(s.q, s.batch())
+    s.ks[1] = NAN
+    out = s.cache().attend(s.q, s.batch())
+    assert torch.isnan(out[:, 4:8]).all() and torch.equal(out[:, :4], want[:, :4]) and torch.equal(out[:, 8:], want[:, 8:])
