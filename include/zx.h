@@ -81,9 +81,10 @@ typedef enum {
     ZX_E_CODEBOOK = 3,     /* max_len infeasible, or data/codebook mismatch        */
     ZX_E_CORRUPT = 4,      /* container inconsistent (device-detected)             */
     ZX_E_HIP = 5,          /* a HIP launch failed                                  */
-    ZX_E_NOSPACE = 6,      /* K/V slots: a block's code bits exceed its slot         */
+    ZX_E_NOSPACE = 6,      /* K/V slots: a block's code bits exceed its slot; pages:
+                              fewer are free than a call needs                       */
     ZX_E_LIMIT = 7         /* request larger than the fixed scratch of an entry point
-                              that allocates nothing                                 */
+                              that allocates nothing, or than an entry point's counts */
 } zx_status;
 
 typedef enum {
@@ -476,6 +477,125 @@ zx_status zx_paged_select(const zx_paged_cache *cache, const zx_paged_batch *bat
                           const zx_rows *q, uint32_t q_heads, uint32_t top_k, uint32_t keep_first,
                           uint32_t keep_last, int32_t *blocks, void *workspace, size_t ws_bytes, uint32_t *err,
                           hipStream_t stream);
+
+/* Attention over parts of a context joined: with out_i and lse_i a row's attention over part i (zx_paged_attend),
+ * lse = ln sum_i e^lse_i and out = sum_i e^(lse_i - lse) out_i.  So sequences that share the pages of a prompt
+ * read them once, as the rows of one sequence (causal 0), and their own pages each.
+ *   parts    n_parts (1..16) BF16 rows [n_tokens][heads][head_dim] (a host array); head_dim 64, 128 or 256
+ *   lses     n_parts device float[n_tokens][heads] (a host array of device pointers)
+ *   out, out_lse  as the parts; out_lse may be NULL; each may be one of the parts' own, and must not overlap
+ *            them otherwise
+ * A part whose lse is -inf is not looked at; where all are, the row is zero and its lse -inf.  A NaN or +inf lse makes
+ * its row NaN.  Weights and sums are held in 32 bits; the result is rounded once (the parts have been rounded before). */
+zx_status zx_attention_merge(const zx_rows *parts, const float *const *lses, uint32_t n_parts, uint32_t n_tokens, uint32_t heads,
+                             uint32_t head_dim, const zx_rows *out, float *out_lse, hipStream_t stream);
+
+/* ---- pages of the paged K/V cache: shared, given out, copied, taken back, brought together ----
+ * All that is kept of a pool's pages is refs[page], the number of table rows that hold it; a page with 0 (or
+ * less) is free.  A pool's pages may be those of many caches (a model's layers).  Row s of a table holds the pages of its first
+ * ceil(held[s] / page_tokens) entries; what stands behind them is neither looked at nor changed, save where pages are given out.
+ * Everything is read on the device when the work runs; a row whose length is negative or more than the table has room for
+ * is left out, and an entry that is no page is skipped; both set err to ZX_E_CORRUPT.  Calls on one pool are ordered by the caller. */
+typedef struct zx_page_pool {
+    uint32_t n_pages;              /* at most 2^23                                      */
+    uint32_t page_tokens;          /* a power of two, 16..4096                          */
+    int32_t *refs;                 /* [n_pages]                                         */
+} zx_page_pool;
+
+typedef struct zx_page_rows {
+    int32_t *page_table;           /* [n_seqs][table_width]                             */
+    int32_t *held;                 /* [n_seqs]: tokens of each row                      */
+    uint32_t n_seqs;               /* at most 65536                                     */
+    uint32_t table_width;          /* times page_tokens: below 2^30                     */
+} zx_page_rows;
+
+/* What is to be copied: pair i < *count moves the first pairs[i][2] tokens of page pairs[i][0] to page pairs[i][1].  Entries
+ * from *count on are not looked at, nor written by the calls that fill the list. */
+typedef struct zx_page_copies {
+    int32_t *pairs;                /* [cap][3]                                          */
+    int32_t *count;                /* [1]                                               */
+    uint32_t cap;
+    uint32_t reserved_;
+} zx_page_copies;
+
+/* Rows go on from other rows: in each group of `beams` (1..2048) neighbouring rows, row r takes what row parents[r]
+ * (counted within the group) held before the call; -1: nothing, it is empty afterwards.  No page is copied: a page's
+ * count grows or shrinks by the rows that hold it.  A group with a length or a parent out of range is left as it is
+ * (ZX_E_CORRUPT). */
+zx_status zx_pages_fork(const zx_page_pool *pool, const zx_page_rows *rows, uint32_t beams, const int32_t *parents, uint32_t *err,
+                        hipStream_t stream);
+
+/* Rows keep their first keep[s] tokens (keep NULL: none) and give back the pages behind them; a row that has no more than that
+ * stays as it is.  A negative keep[s] leaves its row out (ZX_E_CORRUPT). */
+zx_status zx_pages_trim(const zx_page_pool *pool, const zx_page_rows *rows, const int32_t *keep, uint32_t *err, hipStream_t stream);
+
+/* Pages for new tokens: row s gets room for q_start[s+1] - q_start[s] more tokens, held[s] and kv_len[s] become what it then
+ * has (kv_len is what zx_paged_batch wants).  New pages are the lowest free ones, in order of row and place.  A row that goes
+ * on in a page that has tokens and that other rows hold too gets a page of its own there, and an entry in `copies`, in order of rows; unless all
+ * rows that hold the page go on in it in this call, when the first of them keeps it.  Carry the copies out (zx_paged_copy) before
+ * anything is appended.
+ *   n_seqs   at most 2048; copies->cap at least n_seqs
+ *   max_q, max_kv  a row with more new tokens, or that would hold more, is left out
+ *   workspace  zx_pages_extend_workspace_bytes(...) bytes, 16-byte aligned
+ * Rows left out (also one that goes on in a page that is none, or that nobody is said to hold) keep what they have, with
+ * kv_len 0, which makes zx_paged_append and zx_paged_attend skip their tokens; ZX_E_CORRUPT.  Where fewer pages are free than the call needs, no row gets any: all kv_len are 0, *copies->count is 0, nothing else
+ * changes, and err is set to ZX_E_NOSPACE. */
+size_t zx_pages_extend_workspace_bytes(const zx_page_pool *pool, uint32_t n_seqs);
+zx_status zx_pages_extend(const zx_page_pool *pool, const zx_page_rows *rows, const int32_t *q_start, uint32_t max_q, uint32_t max_kv,
+                          int32_t *kv_len, const zx_page_copies *copies, void *workspace, size_t ws_bytes, uint32_t *err,
+                          hipStream_t stream);
+
+/* The L pages in use become pages 0 .. L - 1: those behind move, in order, into the free ones ahead, and the rows' tables follow.
+ *   remap    out, int32[n_pages]: where each page is afterwards, -1 for one that was free
+ *   copies   out: whole pages, none both read and written; cap at least n_pages / 2.  Carry them out before
+ *            anything else is done with the caches
+ *   rows     the table that follows (n_seqs 0: none; others can be rewritten by remap)
+ *   workspace  zx_pages_compact_workspace_bytes(...) bytes, 16-byte aligned */
+size_t zx_pages_compact_workspace_bytes(const zx_page_pool *pool);
+zx_status zx_pages_compact(const zx_page_pool *pool, const zx_page_rows *rows, int32_t *remap, const zx_page_copies *copies,
+                           void *workspace, size_t ws_bytes, uint32_t *err, hipStream_t stream);
+
+/* Carry copies out in n_caches caches (a host array; of one dtype and shape, strides and memory their own): for each pair the first tokens of the keys and of the
+ * values of all heads, bit for bit, and the bounds of the blocks that they reach into.  Pages that are written must be neither
+ * read nor written by another pair.  A pair whose pages are none, or with a count of tokens that no page has, is left out, and a
+ * *count outside [0, cap] is taken as the nearest of the two; both set err to ZX_E_CORRUPT. */
+zx_status zx_paged_copy(const zx_paged_cache *caches, uint32_t n_caches, const zx_page_copies *copies, uint32_t *err,
+                        hipStream_t stream);
+
+/* ---- the choice of the next beams -------------------------------------------------
+ * Beam b of group g has scored score[g][b] so far.  With x its logits, s the scale and lse = ln sum_t e^(s x_t) over the tokens
+ * that it may take, candidate (b, t) scores score[g][b] + s x_t - lse; a beam that is finished has the one candidate (b, end), which scores
+ * score[g][b].  Of each group the n_out candidates with the largest weight[g][b] * score are taken, the best
+ * first; of equal ones that of the earlier beam, then the earlier token.  Logits of -inf and tokens that `allowed` leaves out (whatever
+ * their logits are) are no candidates; a beam with score -inf is not there.  Beams with a NaN or +inf among their logits or as
+ * score, or with a weight that is not positive and finite, have no candidates and set err to ZX_E_CORRUPT. */
+typedef enum { ZX_LOGITS_BF16 = 0, ZX_LOGITS_F16 = 1, ZX_LOGITS_F32 = 2 } zx_logit_type;
+
+typedef struct zx_beam_logits {    /* logit (g, b, t) at g * group_stride + b * beam_stride + t */
+    const void *logits;            /* aligned to one element                            */
+    uint64_t group_stride, beam_stride;    /* in elements                               */
+    int32_t type;                  /* zx_logit_type                                     */
+    uint32_t n_groups;
+    uint32_t beams;                /* 1..64                                             */
+    uint32_t vocab;                /* 1..2^24                                           */
+} zx_beam_logits;
+
+/*   scores    float[n_groups][beams]
+ *   weights   float[n_groups][beams], or NULL: 1 (one over a power of the length ranks by length)
+ *   finished  u8[n_groups][beams], or NULL: none; needs end >= 0
+ *   end       the token that ends a beam, or -1
+ *   allowed   u32[n_groups][beams][ceil(vocab / 32)], bit t % 32 of word t / 32 for token t, or NULL: all
+ *   scale     positive, at most 1e30 (one over a temperature)
+ *   n_out     1..64
+ *   out_scores, parents, tokens, out_finished   float, int32, int32, u8 [n_groups][n_out]: a candidate's score, its beam
+ *             (-1 behind the last candidate, with score -inf and token -1), its token, and whether it is finished: its beam was, or
+ *             its token is `end`
+ *   workspace zx_beam_select_workspace_bytes(...) bytes, 16-byte aligned; its contents do not matter
+ * Exponentials are summed in 32 bits over a few dozen logits and in 64 bits from there on; scores are formed and compared in 64 bits. */
+size_t zx_beam_select_workspace_bytes(int32_t type, uint32_t n_groups, uint32_t beams, uint32_t vocab, uint32_t n_out);
+zx_status zx_beam_select(const zx_beam_logits *in, const float *scores, const float *weights, const uint8_t *finished, int32_t end,
+                         const uint32_t *allowed, double scale, uint32_t n_out, float *out_scores, int32_t *parents, int32_t *tokens,
+                         uint8_t *out_finished, void *workspace, size_t ws_bytes, uint32_t *err, hipStream_t stream);
 
 /* ---- dominant-range codec ---------------------------------------------------------
  * A second codec behind the same conventions (ZipFloat page, sections 3.1-3.3): blocks

@@ -13,3 +13,5 @@ from .zx import (  # noqa: F401
 from .kvslots import KVSlotPool  # noqa: F401,E402
 from .pipeline import LayerPipeline  # noqa: F401,E402
 from .paged import PagedBatch, PagedKVCache, Rotary  # noqa: F401,E402
+from .pages import PageCopies, PagedLayers, PagePool  # noqa: F401,E402
+from .beams import Beams, beam_select, merge_attention  # noqa: F401,E402

@@ -1559,8 +1559,8 @@ extern "C" const char *zx_status_string(zx_status s)
     case ZX_E_CODEBOOK: return "codebook error (length limit infeasible or data without a code)";
     case ZX_E_CORRUPT: return "corrupt container";
     case ZX_E_HIP: return "HIP launch failure";
-    case ZX_E_NOSPACE: return "block does not fit its slot";
-    case ZX_E_LIMIT: return "request larger than the library's fixed scratch";
+    case ZX_E_NOSPACE: return "block does not fit its slot, or too few pages are free";
+    case ZX_E_LIMIT: return "request larger than the library's fixed scratch or counts";
     }
     return "unknown status";
 }

@@ -1,0 +1,615 @@
+// zx_pages.hip -- who holds which page of a paged K/V cache: rows of the table that go on from other
+// rows, pages given out and taken back, pages brought together at the front of the pool.
+//
+// All there is to keep is refs[page], the number of rows that hold a page; a page with none is free, and free
+// pages are given out from the lowest up.  So nothing has to be kept in step with refs, and what a call does follows from its
+// arguments alone: counts are added up with atomics on whole numbers, whose order does not show, and ranks come
+// from prefix sums over the pool, which a launch ahead has counted by segments of kSegment pages.
+//
+// Bound by launches (one to three of a few us) for the pools and tables of a serving step; the bytes are the table's entries in
+// use and refs, read and written once.
+#include "zx_paged.h"
+
+namespace zxg {
+
+using zxk::report;
+using zxp::ceil_div;
+using zxp::div_up;
+
+constexpr uint32_t kMostPages = 1u << 23;
+constexpr uint32_t kMostSeqs = 2048;             // of one call that gives out pages, and beams of a group
+constexpr uint32_t kSegment = 4096;              // pages whose free ones a workgroup counts
+constexpr uint32_t kThreads = 256;
+constexpr uint32_t kEach = kSegment / kThreads;
+
+struct Pool {
+    int32_t *refs;
+    uint32_t n_pages, log_page;
+    uint32_t *err;
+};
+
+struct Rows {
+    int32_t *table, *held;
+    uint32_t n, width;
+    int32_t cap;                                 // tokens that a row of the table has room for
+};
+
+__device__ __forceinline__ uint32_t pages_of(const Pool &p, int32_t tokens) { return ((uint32_t)tokens + (1u << p.log_page) - 1u) >> p.log_page; }
+
+// Sum over the workgroup, and the sum over the threads ahead of this one.
+template <int NT>
+__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *sums, uint32_t &total)
+{
+    uint32_t wave_total;
+    uint32_t ex = zxk::wave_excl_scan(v, wave_total);
+    __syncthreads();
+    if ((threadIdx.x & 63u) == 63u) sums[threadIdx.x >> 6] = wave_total;
+    __syncthreads();
+    total = 0;
+    for (int i = 0; i < NT / 64; ++i) {
+        if (i < (int)(threadIdx.x >> 6)) ex += sums[i];
+        total += sums[i];
+    }
+    return ex;
+}
+
+// ---------------------------------------------------------------- rows go on from other rows
+
+struct ForkArgs {
+    Pool p;
+    Rows r;
+    const int32_t *parents;
+    uint32_t beams, log_strip;                   // columns that a workgroup holds at a time
+    int32_t write_held;                          // one workgroup a group: it writes the lengths too
+};
+
+// The lengths and parents of a group into LDS, and the most pages that a row has; whether all are in range.
+__device__ __forceinline__ bool load_group(const ForkArgs &g, uint32_t group, int32_t *held, int32_t *parent, uint32_t *bad, uint32_t *cols)
+{
+    if (threadIdx.x == 0) *bad = *cols = 0;
+    __syncthreads();
+    for (uint32_t i = threadIdx.x; i < g.beams; i += blockDim.x) {
+        const int32_t h = g.r.held[(uint64_t)group * g.beams + i], q = g.parents[(uint64_t)group * g.beams + i];
+        held[i] = h;
+        parent[i] = q;
+        if (h < 0 || h > g.r.cap || q < -1 || q >= (int32_t)g.beams) *bad = 1;
+        else atomicMax(cols, pages_of(g.p, h));
+    }
+    __syncthreads();
+    if (*bad && threadIdx.x == 0) report(g.p.err, ZX_E_CORRUPT);
+    return !*bad;
+}
+
+// Old rows are read into LDS strip by strip, then written where they go on, so rows may trade places.  A page's
+// count changes by (rows that go on from a row that holds it) - 1 for each such row; a thread adds
+// these up down a column as long as neighbouring rows hold the same page there (beams of one prompt mostly
+// do), and most sums are zero.
+__global__ __launch_bounds__(1024) void k_pages_fork(ForkArgs g)
+{
+    extern __shared__ int32_t lds[];
+    __shared__ uint32_t bad, cols;
+    int32_t *held = lds, *parent = held + g.beams, *children = parent + g.beams, *strip = children + g.beams;
+    const uint32_t group = blockIdx.y, tid = threadIdx.x, ls = g.log_strip, ns = 1u << ls;
+    if (!load_group(g, group, held, parent, &bad, &cols)) return;
+    for (uint32_t i = tid; i < g.beams; i += blockDim.x) children[i] = 0;
+    __syncthreads();
+    for (uint32_t i = tid; i < g.beams; i += blockDim.x)
+        if (parent[i] >= 0) atomicAdd(&children[parent[i]], 1);
+    int32_t *table = g.r.table + (uint64_t)group * g.beams * g.r.width;
+    for (uint32_t c0 = blockIdx.x * ns; c0 < cols; c0 += gridDim.x * ns) {
+        const uint32_t nc = cols - c0 < ns ? cols - c0 : ns;
+        __syncthreads();
+        for (uint32_t i = tid; i < g.beams << ls; i += blockDim.x) {
+            const uint32_t r = i >> ls, c = i & (ns - 1);
+            if (c < nc && c0 + c < pages_of(g.p, held[r])) strip[i] = table[(uint64_t)r * g.r.width + c0 + c];
+        }
+        __syncthreads();
+        for (uint32_t i = tid; i < g.beams << ls; i += blockDim.x) {
+            const uint32_t r = i >> ls, c = i & (ns - 1);
+            const int32_t q = parent[r];
+            if (q >= 0 && q != (int32_t)r && c < nc && c0 + c < pages_of(g.p, held[q]))
+                table[(uint64_t)r * g.r.width + c0 + c] = strip[((uint32_t)q << ls) + c];
+        }
+        // columns shared out over the threads, each in runs of up to 64 rows
+        const uint32_t runs = div_up(g.beams, 64);
+        for (uint32_t i = tid; i < runs << ls; i += blockDim.x) {
+            const uint32_t c = i & (ns - 1), r0 = (i >> ls) * 64, r1 = r0 + 64 < g.beams ? r0 + 64 : g.beams;
+            if (c >= nc) continue;
+            uint32_t page = 0xFFFFFFFFu;
+            int32_t sum = 0;
+            auto add = [&] {
+                if (sum == 0) return;
+                if (page >= g.p.n_pages) report(g.p.err, ZX_E_CORRUPT);
+                else if (atomicAdd(&g.p.refs[page], sum) + sum < 0) report(g.p.err, ZX_E_CORRUPT);
+            };
+            for (uint32_t r = r0; r < r1; ++r) {
+                if (c0 + c >= pages_of(g.p, held[r])) continue;
+                const uint32_t is = (uint32_t)strip[(r << ls) + c];
+                if (is != page) {
+                    add();
+                    sum = 0;
+                    page = is;
+                }
+                sum += children[r] - 1;
+            }
+            add();
+        }
+    }
+    if (g.write_held)
+        for (uint32_t i = tid; i < g.beams; i += blockDim.x)
+            if (parent[i] != (int32_t)i) g.r.held[(uint64_t)group * g.beams + i] = parent[i] < 0 ? 0 : held[parent[i]];
+}
+
+// The lengths, where several workgroups of a group had to read them.
+__global__ __launch_bounds__(kThreads) void k_pages_fork_held(ForkArgs g)
+{
+    extern __shared__ int32_t lds[];
+    __shared__ uint32_t bad, cols;
+    int32_t *held = lds, *parent = held + g.beams;
+    if (!load_group(g, blockIdx.x, held, parent, &bad, &cols)) return;
+    for (uint32_t i = threadIdx.x; i < g.beams; i += blockDim.x)
+        g.r.held[(uint64_t)blockIdx.x * g.beams + i] = parent[i] < 0 ? 0 : held[parent[i]];
+}
+
+// ---------------------------------------------------------------- rows give pages back
+
+__global__ __launch_bounds__(kThreads) void k_pages_trim(Pool p, Rows r, const int32_t *keep)
+{
+    const uint32_t s = blockIdx.x;
+    const int32_t held = r.held[s], want = keep ? keep[s] : 0;
+    if (held < 0 || held > r.cap || want < 0) {
+        if (threadIdx.x == 0) report(p.err, ZX_E_CORRUPT);
+        return;
+    }
+    if (want >= held) return;
+    const uint32_t first = pages_of(p, want), end = pages_of(p, held);
+    const int32_t *row = r.table + (uint64_t)s * r.width;
+    for (uint32_t c = first + threadIdx.x; c < end; c += kThreads) {
+        const uint32_t page = (uint32_t)row[c];
+        if (page >= p.n_pages) report(p.err, ZX_E_CORRUPT);
+        else if (atomicAdd(&p.refs[page], -1) <= 0) report(p.err, ZX_E_CORRUPT);
+    }
+    __syncthreads();                             // all have read the length
+    if (threadIdx.x == 0) r.held[s] = want;
+}
+
+// ---------------------------------------------------------------- pages are given out
+
+struct Need {
+    uint32_t before;                             // pages that the sequences ahead take
+    uint32_t first;                              // first table place that is given a page
+    uint32_t pair;                               // bit 31: that place's old page is copied, as this pair
+    uint32_t tokens;                             // of it
+    int32_t held, kv;                            // lengths after the call
+    uint32_t old, left;                          // bit 31 of old: this sequence sets that page's count to `left`
+};
+constexpr uint32_t kFlag = 1u << 31;
+
+struct ExtendArgs {
+    Pool p;
+    Rows r;
+    const int32_t *q_start;
+    int32_t *kv_len, *pairs, *count;
+    uint32_t max_q;
+    Need *need;                                  // [n]
+    uint64_t *total;                             // pages wanted, and pairs
+    uint32_t *counted;                           // [segments] free pages
+    uint32_t n_segments, log_slots;
+};
+
+__device__ __forceinline__ uint32_t free_in_segment(const Pool &p, uint32_t seg, uint32_t *sums)
+{
+    uint32_t n = 0;
+    const uint32_t p0 = seg * kSegment + threadIdx.x;
+#pragma unroll
+    for (uint32_t i = 0; i < kEach; ++i) {
+        const uint32_t page = p0 + i * kThreads;
+        n += page < p.n_pages && p.refs[page] <= 0;
+    }
+    uint32_t total;
+    (void)block_scan<(int)kThreads>(n, sums, total);
+    return total;
+}
+
+// Free pages counted by segments; and, by workgroup 0, what every sequence needs.  A sequence that goes on in a page which
+// others hold too may not write there: it gets a page of its own and a copy of what it has, unless all that hold the page go on
+// in this call, when the first of them keeps it.  How many go on in a page, and who is first, is counted in a
+// hash table in LDS; neither depends on the order of entry.
+__global__ __launch_bounds__(kThreads) void k_pages_need(ExtendArgs g)
+{
+    extern __shared__ uint32_t slots[];          // [slot][3]: page + 1, sequences that write it, the first of them
+    __shared__ uint32_t sums[kThreads / 64];
+    __shared__ unsigned long long wanted;
+    const uint32_t tid = threadIdx.x;
+    if (blockIdx.x > 0) {
+        const uint32_t seg = blockIdx.x - 1, n = free_in_segment(g.p, seg, sums);
+        if (tid == 0) g.counted[seg] = n;
+        return;
+    }
+    const uint32_t n_slots = 1u << g.log_slots, mask = n_slots - 1;
+    for (uint32_t i = tid; i < n_slots; i += kThreads) {
+        slots[3 * i] = slots[3 * i + 1] = 0;
+        slots[3 * i + 2] = 0xFFFFFFFFu;
+    }
+    if (tid == 0) wanted = 0;
+    __syncthreads();
+    auto slot_of = [&](uint32_t page) { return (page * 0x9E3779B1u) >> (32 - g.log_slots); };
+    const uint32_t T = 1u << g.p.log_page;
+    struct Seq {
+        int32_t nq, held;
+        uint32_t page, refs;                     // refs > 0 where it goes on in a page that has tokens
+        bool ok;
+    };
+    auto load = [&](uint32_t s) {
+        Seq v{0, 0, 0, 0, false};
+        const int32_t q0 = g.q_start[s], q1 = g.q_start[s + 1], held = g.r.held[s];
+        // (differences in 64 bits: lengths that are nonsense must not wrap into sense)
+        const int64_t nq = (int64_t)q1 - q0, all = nq + held;
+        if (q0 < 0 || nq < 0 || nq > (int64_t)g.max_q || held < 0 || all > (int64_t)g.r.cap) return v;
+        v.nq = (int32_t)nq;
+        v.held = held;
+        v.ok = true;
+        if (nq > 0 && held % (int32_t)T) {
+            v.page = (uint32_t)g.r.table[(uint64_t)s * g.r.width + ((uint32_t)held >> g.p.log_page)];
+            const int32_t refs = v.page < g.p.n_pages ? g.p.refs[v.page] : 0;
+            if (refs <= 0) v.ok = false;         // no page, or one that nobody is said to hold
+            else v.refs = (uint32_t)refs;
+        }
+        return v;
+    };
+    for (uint32_t s = tid; s < g.r.n; s += kThreads) {
+        const Seq v = load(s);
+        if (!v.ok) report(g.p.err, ZX_E_CORRUPT);
+        if (!v.ok || v.refs == 0) continue;
+        uint32_t i = slot_of(v.page);
+        for (;;) {                               // (twice as many slots as sequences: one is free)
+            const uint32_t was = atomicCAS(&slots[3 * i], 0u, v.page + 1);
+            if (was == 0 || was == v.page + 1) break;
+            i = (i + 1) & mask;
+        }
+        atomicAdd(&slots[3 * i + 1], 1u);
+        atomicMin(&slots[3 * i + 2], s);
+    }
+    __syncthreads();
+    uint32_t taken = 0, copied = 0;              // by the sequences ahead
+    for (uint32_t s0 = 0; s0 < g.r.n; s0 += kThreads) {
+        const uint32_t s = s0 + tid;
+        Seq v{0, 0, 0, 0, false};
+        if (s < g.r.n) v = load(s);
+        uint32_t slot = 0;
+        if (v.ok && v.refs > 0) {
+            slot = slot_of(v.page);
+            while (slots[3 * slot] != v.page + 1 && slots[3 * slot] != 0) slot = (slot + 1) & mask;
+            if (slots[3 * slot] == 0) v.ok = false;          // (only if the table is written meanwhile)
+        }
+        Need d{};
+        uint32_t n = 0;
+        bool copy = false;
+        if (v.ok) {
+            d.held = d.kv = v.held + v.nq;
+            d.first = pages_of(g.p, v.held);
+            if (v.refs > 0) {
+                const uint32_t writers = slots[3 * slot + 1];
+                const bool leads = slots[3 * slot + 2] == s;
+                copy = !(leads && writers >= v.refs);
+                d.old = v.page;
+                if (leads) {
+                    d.old |= kFlag;
+                    d.left = writers >= v.refs ? 1 : v.refs - writers;
+                }
+                d.tokens = (uint32_t)v.held & (T - 1);
+                if (copy) --d.first;
+            }
+            n = v.nq > 0 ? pages_of(g.p, d.held) - d.first : 0;
+        } else if (s < g.r.n) {
+            d.held = g.r.held[s];                // left out: it stays as it is
+        }
+        // sums are only used where all is no more than the pool: a sequence's part is cut to what makes it more
+        const uint32_t most = kMostPages + 1;
+        uint32_t total, pairs;
+        const uint32_t ahead = block_scan<(int)kThreads>(n < most ? n : most, sums, total);
+        const uint32_t nth = block_scan<(int)kThreads>(copy ? 1u : 0u, sums, pairs);
+        d.before = taken + ahead;
+        d.pair = copy ? kFlag | (copied + nth) : 0;
+        if (s < g.r.n) g.need[s] = d;
+        if (tid == 0) wanted += total;           // (256 * (2^23 + 1) fits 32 bits; the sum of eight such may not)
+        taken += total;
+        copied += pairs;
+    }
+    if (tid == 0) {
+        g.total[0] = wanted;
+        g.total[1] = copied;
+    }
+}
+
+// Each workgroup gives out the free pages of its segment: the r-th free page of the pool to the sequence whose part holds r.
+__global__ __launch_bounds__(kThreads) void k_pages_give(ExtendArgs g)
+{
+    __shared__ uint32_t sums[kThreads / 64];
+    __shared__ uint32_t before[kMostSeqs];
+    const uint32_t tid = threadIdx.x, seg = blockIdx.x;
+    const uint64_t wanted = g.total[0];
+    uint32_t ahead = 0, all = 0, mine = 0;
+    for (uint32_t i = tid; i < g.n_segments; i += kThreads) {
+        const uint32_t n = g.counted[i];
+        all += n;
+        if (i < seg) mine += n;
+    }
+    uint32_t unused, total;
+    unused = block_scan<(int)kThreads>(all, sums, total);
+    unused = block_scan<(int)kThreads>(mine, sums, ahead);
+    (void)unused;
+    const bool enough = wanted <= total;
+    if (seg == 0) {
+        if (!enough && tid == 0) report(g.p.err, ZX_E_NOSPACE);
+        if (tid == 0) *g.count = enough ? (int32_t)g.total[1] : 0;
+        for (uint32_t s = tid; s < g.r.n; s += kThreads) {
+            const Need d = g.need[s];
+            g.kv_len[s] = enough ? d.kv : 0;
+            if (!enough) continue;
+            g.r.held[s] = d.held;
+            // (counts of pages that others hold stay above zero: no one here takes them for free ones)
+            if (d.old & kFlag) g.p.refs[d.old & ~kFlag] = (int32_t)d.left;
+        }
+    }
+    if (!enough || wanted <= ahead || g.counted[seg] == 0) return;
+    for (uint32_t s = tid; s < g.r.n; s += kThreads) before[s] = g.need[s].before;
+    // a thread's kEach pages lie side by side, so ranks ascend with the page
+    const uint32_t p0 = seg * kSegment + tid * kEach;
+    uint32_t is_free = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < kEach; ++i)
+        if (p0 + i < g.p.n_pages && g.p.refs[p0 + i] <= 0) is_free |= 1u << i;
+    uint32_t r = ahead + block_scan<(int)kThreads>((uint32_t)__builtin_popcount(is_free), sums, total);
+    for (; is_free && r < wanted; is_free &= is_free - 1, ++r) {
+        const uint32_t page = p0 + (uint32_t)__builtin_ctz(is_free);
+        uint32_t lo = 0, hi = g.r.n;             // the last sequence with before <= r
+        while (hi - lo > 1) {
+            const uint32_t m = (lo + hi) / 2;
+            if (before[m] <= r) lo = m;
+            else hi = m;
+        }
+        const Need d = g.need[lo];
+        const uint32_t at = d.first + (r - d.before);
+        g.r.table[(uint64_t)lo * g.r.width + at] = (int32_t)page;
+        g.p.refs[page] = 1;
+        if ((d.pair & kFlag) && at == d.first) {
+            int32_t *pr = g.pairs + 3 * (uint64_t)(d.pair & ~kFlag);
+            pr[0] = (int32_t)(d.old & ~kFlag);
+            pr[1] = (int32_t)page;
+            pr[2] = (int32_t)d.tokens;
+        }
+    }
+}
+
+// ---------------------------------------------------------------- pages in use are brought together
+
+struct CompactArgs {
+    Pool p;
+    Rows r;
+    int32_t *remap, *pairs, *count, *nth;        // nth[page]: which pair moves it, or -1
+    uint32_t *counted;
+    uint32_t n_segments;
+};
+
+__global__ __launch_bounds__(kThreads) void k_pages_count(CompactArgs g)
+{
+    __shared__ uint32_t sums[kThreads / 64];
+    const uint32_t n = free_in_segment(g.p, blockIdx.x, sums);
+    if (threadIdx.x == 0) g.counted[blockIdx.x] = n;
+}
+
+// With L pages in use, those of them at L or behind go into the free ones ahead of L, in order: the j-th such page into the
+// j-th hole.  There are as many of the one as of the other.
+__global__ __launch_bounds__(kThreads) void k_pages_pair(CompactArgs g)
+{
+    __shared__ uint32_t sums[kThreads / 64];
+    const uint32_t tid = threadIdx.x, seg = blockIdx.x;
+    uint32_t all = 0, ahead = 0, total, mine = 0;
+    for (uint32_t i = tid; i < g.n_segments; i += kThreads) {
+        const uint32_t n = g.counted[i];
+        all += n;
+        if (i < seg) mine += n;
+    }
+    (void)block_scan<(int)kThreads>(all, sums, total);
+    (void)block_scan<(int)kThreads>(mine, sums, ahead);
+    const uint32_t L = g.p.n_pages - total;      // pages in use
+    // holes: free pages ahead of L
+    const uint32_t ls = L / kSegment;
+    uint32_t n = 0, holes;
+    for (uint32_t i = tid; i < ls && i < g.n_segments; i += kThreads) n += g.counted[i];
+    for (uint32_t i = ls * kSegment + tid; i < L; i += kThreads) n += g.p.refs[i] <= 0;
+    (void)block_scan<(int)kThreads>(n, sums, holes);
+    if (seg == 0 && tid == 0) *g.count = (int32_t)holes;
+    const uint32_t most = g.p.n_pages / 2;       // (never more, unless refs is written meanwhile)
+    const uint32_t p0 = seg * kSegment + tid * kEach;
+    uint32_t is_free = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < kEach; ++i)
+        if (p0 + i < g.p.n_pages && g.p.refs[p0 + i] <= 0) is_free |= 1u << i;
+    uint32_t f = ahead + block_scan<(int)kThreads>((uint32_t)__builtin_popcount(is_free), sums, total);    // free pages ahead
+    for (uint32_t i = 0; i < kEach; ++i) {
+        const uint32_t page = p0 + i;
+        if (page >= g.p.n_pages) break;
+        const bool empty = is_free >> i & 1u;
+        int32_t to = empty ? -1 : (int32_t)page, j = -1;
+        if (empty && page < L && f < most) {
+            g.pairs[3 * (uint64_t)f + 1] = (int32_t)page;
+            g.pairs[3 * (uint64_t)f + 2] = 1 << g.p.log_page;
+        } else if (!empty && page >= L) {
+            j = (int32_t)((page - f) - (L - holes));         // pages in use ahead of it, less those ahead of L
+            if ((uint32_t)j < most) g.pairs[3 * (uint64_t)j] = (int32_t)page;
+            else j = -1;
+        }
+        g.nth[page] = j;
+        if (j < 0) g.remap[page] = to;
+        f += empty;
+    }
+}
+
+// The pairs' counts and new places; and the tables, whose entries find their new place through nth and the pairs.
+__global__ __launch_bounds__(kThreads) void k_pages_move(CompactArgs g, uint32_t for_pairs, uint32_t per_row)
+{
+    if (blockIdx.x < for_pairs) {
+        const uint32_t said = (uint32_t)*g.count, n = said < g.p.n_pages / 2 ? said : g.p.n_pages / 2;
+        for (uint32_t j = blockIdx.x * kThreads + threadIdx.x; j < n; j += for_pairs * kThreads) {
+            const uint32_t from = (uint32_t)g.pairs[3 * (uint64_t)j], to = (uint32_t)g.pairs[3 * (uint64_t)j + 1];
+            if (from >= g.p.n_pages || to >= g.p.n_pages) continue;
+            g.remap[from] = (int32_t)to;
+            g.p.refs[to] = g.p.refs[from];
+            g.p.refs[from] = 0;
+        }
+        return;
+    }
+    const uint32_t item = blockIdx.x - for_pairs, s = item / per_row;
+    const int32_t held = g.r.held[s];
+    if (held < 0 || held > g.r.cap) {
+        if (threadIdx.x == 0) report(g.p.err, ZX_E_CORRUPT);
+        return;
+    }
+    const uint32_t n = pages_of(g.p, held);
+    int32_t *row = g.r.table + (uint64_t)s * g.r.width;
+    for (uint32_t c = (item % per_row) * kThreads + threadIdx.x; c < n; c += per_row * kThreads) {
+        const uint32_t page = (uint32_t)row[c];
+        if (page >= g.p.n_pages) {
+            report(g.p.err, ZX_E_CORRUPT);
+            continue;
+        }
+        const int32_t j = g.nth[page];
+        if (j >= 0) row[c] = g.pairs[3 * (uint64_t)j + 1];
+        else if (g.remap[page] < 0) report(g.p.err, ZX_E_CORRUPT);       // a page that nobody is said to hold
+    }
+}
+
+// ---- host side
+zx_status make_pool(const zx_page_pool *p, uint32_t *err, Pool &o)
+{
+    if (!p || !p->refs || p->n_pages == 0 || !zxp::pow2_in(p->page_tokens, 16, 4096)) return ZX_E_INVAL;
+    if (p->n_pages > kMostPages) return ZX_E_LIMIT;
+    o = Pool{p->refs, p->n_pages, zxp::log2_of(p->page_tokens), err};
+    return ZX_OK;
+}
+
+zx_status make_rows(const zx_page_rows *r, const zx_page_pool *p, Rows &o)
+{
+    if (!r) return ZX_E_INVAL;
+    if (r->n_seqs && (!r->held || (r->table_width && !r->page_table))) return ZX_E_INVAL;
+    const uint64_t room = (uint64_t)r->table_width * p->page_tokens;
+    if (room > 0x3FFFFFFFu || r->n_seqs > 65536) return ZX_E_LIMIT;
+    o = Rows{r->page_table, r->held, r->n_seqs, r->table_width, (int32_t)room};
+    return ZX_OK;
+}
+
+inline bool good_copies(const zx_page_copies *c, uint32_t least) { return c && c->count && c->cap >= least && (c->pairs || least == 0); }
+
+inline zx_status launched() { return hipGetLastError() == hipSuccess ? ZX_OK : ZX_E_HIP; }
+
+}  // namespace zxg
+
+using namespace zxg;
+
+extern "C" zx_status zx_pages_fork(const zx_page_pool *pool, const zx_page_rows *rows, uint32_t beams, const int32_t *parents,
+                                   uint32_t *err, hipStream_t stream)
+{
+    ForkArgs g{};
+    zx_status st = make_pool(pool, err, g.p);
+    if (st == ZX_OK) st = make_rows(rows, pool, g.r);
+    if (st != ZX_OK) return st;
+    if (beams == 0 || rows->n_seqs % beams) return ZX_E_INVAL;
+    if (beams > kMostSeqs) return ZX_E_LIMIT;
+    if (rows->n_seqs == 0) return ZX_OK;
+    if (!parents) return ZX_E_INVAL;
+    g.parents = parents;
+    g.beams = beams;
+    const uint32_t groups = rows->n_seqs / beams;
+    // 32 KB of table entries at a time, four columns at least
+    g.log_strip = 10;
+    while (g.log_strip > 2 && ((uint64_t)beams << g.log_strip) > 8192) --g.log_strip;
+    const uint32_t n_strips = ceil_div(rows->table_width, 1u << g.log_strip);
+    // several workgroups a group, and a launch more for the lengths, where there are few groups and many strips
+    uint32_t wgs = 1;
+    while (wgs * 4 <= n_strips && wgs * groups < 256) wgs *= 2;
+    g.write_held = wgs == 1;
+    const uint32_t lds = (3 * beams + (beams << g.log_strip)) * 4;
+    hipLaunchKernelGGL(k_pages_fork, dim3(wgs, groups), dim3(1024), lds, stream, g);
+    if (wgs > 1) hipLaunchKernelGGL(k_pages_fork_held, dim3(groups), dim3(kThreads), 2 * beams * 4, stream, g);
+    return launched();
+}
+
+extern "C" zx_status zx_pages_trim(const zx_page_pool *pool, const zx_page_rows *rows, const int32_t *keep, uint32_t *err,
+                                   hipStream_t stream)
+{
+    Pool p;
+    Rows r;
+    zx_status st = make_pool(pool, err, p);
+    if (st == ZX_OK) st = make_rows(rows, pool, r);
+    if (st != ZX_OK || rows->n_seqs == 0) return st;
+    hipLaunchKernelGGL(k_pages_trim, dim3(r.n), dim3(kThreads), 0, stream, p, r, keep);
+    return launched();
+}
+
+extern "C" size_t zx_pages_extend_workspace_bytes(const zx_page_pool *pool, uint32_t n_seqs)
+{
+    if (!pool || pool->n_pages > kMostPages || n_seqs > kMostSeqs) return 0;
+    return 16 + (size_t)n_seqs * sizeof(Need) + (size_t)ceil_div(pool->n_pages, kSegment) * 4;
+}
+
+extern "C" zx_status zx_pages_extend(const zx_page_pool *pool, const zx_page_rows *rows, const int32_t *q_start, uint32_t max_q,
+                                     uint32_t max_kv, int32_t *kv_len, const zx_page_copies *copies, void *workspace, size_t ws_bytes,
+                                     uint32_t *err, hipStream_t stream)
+{
+    ExtendArgs g{};
+    zx_status st = make_pool(pool, err, g.p);
+    if (st == ZX_OK) st = make_rows(rows, pool, g.r);
+    if (st != ZX_OK) return st;
+    if (rows->n_seqs > kMostSeqs) return ZX_E_LIMIT;
+    if (!good_copies(copies, rows->n_seqs)) return ZX_E_INVAL;
+    if (rows->n_seqs && (!q_start || !kv_len)) return ZX_E_INVAL;
+    if (!workspace || ((uintptr_t)workspace & 15u) || ws_bytes < zx_pages_extend_workspace_bytes(pool, rows->n_seqs)) return ZX_E_INVAL;
+    if ((uint32_t)g.r.cap > max_kv) g.r.cap = (int32_t)max_kv;
+    g.q_start = q_start;
+    g.kv_len = kv_len;
+    g.pairs = copies->pairs;
+    g.count = copies->count;
+    g.max_q = max_q;
+    g.n_segments = ceil_div(pool->n_pages, kSegment);
+    g.total = static_cast<uint64_t *>(workspace);
+    g.need = reinterpret_cast<Need *>(g.total + 2);
+    g.counted = reinterpret_cast<uint32_t *>(g.need + rows->n_seqs);
+    g.log_slots = 6;
+    while ((1u << g.log_slots) < 2 * rows->n_seqs) ++g.log_slots;
+    hipLaunchKernelGGL(k_pages_need, dim3(1 + g.n_segments), dim3(kThreads), (3u << g.log_slots) * 4, stream, g);
+    hipLaunchKernelGGL(k_pages_give, dim3(g.n_segments), dim3(kThreads), 0, stream, g);
+    return launched();
+}
+
+extern "C" size_t zx_pages_compact_workspace_bytes(const zx_page_pool *pool)
+{
+    if (!pool || pool->n_pages > kMostPages) return 0;
+    return (size_t)pool->n_pages * 4 + (size_t)ceil_div(pool->n_pages, kSegment) * 4;
+}
+
+extern "C" zx_status zx_pages_compact(const zx_page_pool *pool, const zx_page_rows *rows, int32_t *remap, const zx_page_copies *copies,
+                                      void *workspace, size_t ws_bytes, uint32_t *err, hipStream_t stream)
+{
+    CompactArgs g{};
+    zx_status st = make_pool(pool, err, g.p);
+    if (st == ZX_OK) st = make_rows(rows, pool, g.r);
+    if (st != ZX_OK) return st;
+    if (!remap || !good_copies(copies, pool->n_pages / 2)) return ZX_E_INVAL;
+    if (!workspace || ((uintptr_t)workspace & 15u) || ws_bytes < zx_pages_compact_workspace_bytes(pool)) return ZX_E_INVAL;
+    g.remap = remap;
+    g.pairs = copies->pairs;
+    g.count = copies->count;
+    g.nth = static_cast<int32_t *>(workspace);
+    g.counted = reinterpret_cast<uint32_t *>(g.nth + pool->n_pages);
+    g.n_segments = ceil_div(pool->n_pages, kSegment);
+    hipLaunchKernelGGL(k_pages_count, dim3(g.n_segments), dim3(kThreads), 0, stream, g);
+    hipLaunchKernelGGL(k_pages_pair, dim3(g.n_segments), dim3(kThreads), 0, stream, g);
+    // workgroups for the pairs, and for each row of the table
+    const uint32_t pairs = ceil_div(pool->n_pages / 2 + 1, kThreads), for_pairs = pairs < 256 ? pairs : 256;
+    const uint32_t most = ceil_div(rows->table_width, kThreads);
+    const uint32_t fair = rows->n_seqs ? 1 + 1024 / rows->n_seqs : 1, per_row = most == 0 ? 1 : most < fair ? most : fair;
+    hipLaunchKernelGGL(k_pages_move, dim3(for_pairs + rows->n_seqs * per_row), dim3(kThreads), 0, stream, g, for_pairs, per_row);
+    return launched();
+}

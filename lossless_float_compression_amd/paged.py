@@ -556,6 +556,11 @@ class PagedKVCache:
             raise _zx.ZxError("zx_paged_select", st)
         return blocks
 
+    def copy_pages(self, copies, err: Optional[torch.Tensor] = None, stream=None) -> None:
+        """Carry a list of page copies out in this cache alone (`PagedLayers` does so in all layers' at once)."""
+        from .pages import PagedLayers
+        PagedLayers([self]).copy_pages(copies, err, stream)
+
     # ---- pages in a slot pool
     def blocks_per_page(self) -> int:
         """65536-element codec blocks of the keys (and of the values) of one page."""

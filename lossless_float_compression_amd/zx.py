@@ -31,8 +31,8 @@ LIB_PATH = os.path.join(_HERE, "libzx.so")
 _lib = None
 
 _STATUS = {0: "ok", 1: "invalid argument", 2: "unsupported dtype", 3: "codebook error",
-           4: "corrupt container", 5: "HIP launch failure", 6: "block does not fit its slot",
-           7: "request larger than the library's fixed scratch"}
+           4: "corrupt container", 5: "HIP launch failure", 6: "block does not fit its slot, or too few pages are free",
+           7: "request larger than the library's fixed scratch or counts"}
 ZX_E_NOSPACE = 6
 ZX_E_LIMIT = 7
 KV_NOALLOC_MAX_BLOCKS = 1024
@@ -84,7 +84,9 @@ EXPORTS = ("zx_histogram", "zx_build_codebook", "zx_encode_size", "zx_encode", "
            "zx_zf_encode", "zx_zf_decode", "zx_histogram_accumulate", "zx_build_codebook_u64",
            "zx_kv_encode_slots_noalloc", "zx_encode_plan", "zx_kv_encode_slots_fused", "zx_encode_coded",
            "zx_paged_append", "zx_paged_attend", "zx_paged_attend_workspace_bytes", "zx_paged_select",
-           "zx_paged_select_workspace_bytes")
+           "zx_paged_select_workspace_bytes", "zx_paged_copy", "zx_pages_fork", "zx_pages_trim", "zx_pages_extend",
+           "zx_pages_extend_workspace_bytes", "zx_pages_compact", "zx_pages_compact_workspace_bytes", "zx_attention_merge",
+           "zx_beam_select", "zx_beam_select_workspace_bytes")
 
 
 def lib():
