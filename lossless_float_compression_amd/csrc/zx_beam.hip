@@ -28,9 +28,9 @@ constexpr uint32_t kMostVocab = 1u << 24;
 enum { BF16, F16, F32 };
 
 struct Stat {
-    float top;                       // the part's largest logit (-inf: none may be taken)
+    float top;                       // a wave's largest logit (-inf: none may be taken)
     uint32_t unused;
-    double sum;                      // of exp(s (x - top)) over the part
+    double sum;                      // of exp(s (x - top)) over its logits
 };
 struct Cand {
     float x;                         // -inf: none
@@ -43,7 +43,7 @@ struct BeamArgs {
     const float *scores, *weights;
     const uint8_t *finished;
     const uint32_t *allowed;
-    Stat *stat;                                  // [row][part]
+    Stat *stat;                                  // [row][part][wave]
     Cand *cand;                                  // [row][part][n_out], the largest first
     float *out_scores;
     int32_t *parents, *tokens;
@@ -51,6 +51,8 @@ struct BeamArgs {
     uint32_t *err;
     double scale;
     uint32_t groups, beams, vocab, n_out, parts, words;
+    uint32_t tiles;                              // of a part
+    uint32_t depth;                              // candidates of a part that the join looks at first
     int32_t end;
 };
 
@@ -76,12 +78,31 @@ __device__ __forceinline__ uint64_t ordered(double x)
     return b ^ ((uint64_t)((int64_t)b >> 63) | 0x8000000000000000ull);
 }
 
-// The largest t that at least n of the wave's keys reach (0 where there are fewer than n lanes' worth), or, once
-// exactly n keys reach it, a smaller one that does as well.
-__device__ __forceinline__ uint32_t nth_largest(uint32_t key, uint32_t n)
+template <class F>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t x, F f)
 {
-    uint32_t t = 0;
-    for (int bit = 31; bit >= 0; --bit) {
+    // within rows of 16 lanes by rotations, then across them
+#define ROTATE(n) x = f(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)x, 0x120 + n, 0xF, 0xF, true))
+    ROTATE(8);
+    ROTATE(4);
+    ROTATE(2);
+    ROTATE(1);
+#undef ROTATE
+    const auto r = __builtin_amdgcn_permlane16_swap(x, x, false, false);
+    const uint32_t y = f((uint32_t)r[0], (uint32_t)r[1]);
+    const auto s = __builtin_amdgcn_permlane32_swap(y, y, false, false);
+    return (uint32_t)__builtin_amdgcn_readfirstlane((int)f((uint32_t)s[0], (uint32_t)s[1]));
+}
+
+// A value that n at least of the wave's keys reach (n <= 64), and few more: the n-th largest itself, or, as soon as exactly
+// n keys reach it, a smaller one.  Found bit by bit from the first one in which any two keys differ; `top` is the largest key.
+__device__ __forceinline__ uint32_t nth_largest(uint32_t key, uint32_t top, uint32_t n)
+{
+    const uint32_t low = wave_reduce(key, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+    if (low == top) return top;
+    const int first = 31 - __builtin_clz(low ^ top);
+    uint32_t t = top & ~((2u << first) - 1u);
+    for (int bit = first; bit >= 0; --bit) {
         const uint32_t u = t | (1u << bit);
         const uint32_t c = (uint32_t)__popcll(__ballot(key >= u));
         if (c >= n) t = u;
@@ -94,24 +115,11 @@ template <int TY>
 struct Type {
     static constexpr int N = TY == F32 ? 4 : 8;  // logits of 16 bytes
     static constexpr int W = TY == F32 ? 4 : 2;  // bytes of one
+    static constexpr uint32_t LOW = TY == F32 ? 0xFF800000u : TY == BF16 ? 0xFF80u : 0xFC00u;    // -inf
 };
 
 template <int TY>
-__device__ __forceinline__ float one_logit(const uint8_t *p)
-{
-    if constexpr (TY == F32) {
-        float x;
-        __builtin_memcpy(&x, p, 4);
-        return x;
-    } else {
-        uint16_t h;
-        __builtin_memcpy(&h, p, 2);
-        return TY == BF16 ? __builtin_bit_cast(float, (uint32_t)h << 16) : (float)__builtin_bit_cast(_Float16, h);
-    }
-}
-
-template <int TY>
-__device__ __forceinline__ void unpack(u4 w, float *x)
+__device__ __forceinline__ void unpack(u4 w, float (&x)[Type<TY>::N])
 {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -128,133 +136,282 @@ __device__ __forceinline__ void unpack(u4 w, float *x)
     }
 }
 
+// Which of a row's tokens t .. t + N - 1 are there (bit i for t + i).
+__device__ __forceinline__ uint32_t there(uint32_t t, uint32_t n, uint32_t vocab)
+{
+    return t >= vocab ? 0u : t + n <= vocab ? 0xFFFFFFFFu : (1u << (vocab - t)) - 1u;
+}
+// The logits of these tokens: at the row's end the row's last 16 bytes, which `settle` moves to their places (a row shorter than that
+// is read there, one by one); it makes those that are not in `bits` -inf.
+template <int TY>
+__device__ __forceinline__ u4 fetch(const uint8_t *row, uint32_t t, uint32_t vocab)
+{
+    constexpr uint32_t N = Type<TY>::N, W = Type<TY>::W;
+    u4 r{0, 0, 0, 0};
+    if (vocab >= N) __builtin_memcpy(&r, row + (uint64_t)(t + N <= vocab ? t : vocab - N) * W, 16);
+    return r;
+}
+template <int TY>
+__device__ __forceinline__ u4 settle(u4 r, const uint8_t *row, uint32_t t, uint32_t vocab, uint32_t bits)
+{
+    constexpr uint32_t N = Type<TY>::N, W = Type<TY>::W;
+    if (t + N > vocab && t < vocab) {
+        unsigned __int128 x = __builtin_bit_cast(unsigned __int128, r);
+        if (vocab >= N) {
+            x >>= (t + N - vocab) * W * 8;
+        } else {
+#pragma unroll 1
+            for (uint32_t i = 0; i < vocab - t; ++i) {
+                uint32_t one = 0;
+                __builtin_memcpy(&one, row + (uint64_t)(t + i) * W, W);
+                x |= (unsigned __int128)one << (i * W * 8);
+            }
+        }
+        r = __builtin_bit_cast(u4, x);
+    }
+    if (bits != 0xFFFFFFFFu) {
+#pragma unroll
+        for (uint32_t i = 0; i < 4; ++i) {
+            if constexpr (W == 4) {
+                if (!(bits >> i & 1u)) r[i] = Type<TY>::LOW;
+            } else {
+                if (!(bits >> (2 * i) & 1u)) r[i] = (r[i] & 0xFFFF0000u) | Type<TY>::LOW;
+                if (!(bits >> (2 * i + 1) & 1u)) r[i] = (r[i] & 0xFFFFu) | Type<TY>::LOW << 16;
+            }
+        }
+    }
+    return r;
+}
+
 __device__ __forceinline__ float wave_max(float x)
 {
-    for (int o = 32; o >= 1; o >>= 1) x = fmaxf(x, __shfl_xor(x, o, 64));
-    return x;
+    return __builtin_bit_cast(float, wave_reduce(__builtin_bit_cast(uint32_t, x), [](uint32_t a, uint32_t b) {
+        return __builtin_bit_cast(uint32_t, fmaxf(__builtin_bit_cast(float, a), __builtin_bit_cast(float, b)));
+    }));
 }
 __device__ __forceinline__ double wave_sum(double x)
 {
-    for (int o = 32; o >= 1; o >>= 1) x += __shfl_xor(x, o, 64);
+    auto with = [](double a, uint32_t lo, uint32_t hi) { return a + __builtin_bit_cast(double, (uint64_t)hi << 32 | lo); };
+#define HALVES const uint64_t q = __builtin_bit_cast(uint64_t, x); const uint32_t lo = (uint32_t)q, hi = (uint32_t)(q >> 32)
+#define ROTATE(n) \
+    do { \
+        HALVES; \
+        x = with(x, (uint32_t)__builtin_amdgcn_update_dpp(0, (int)lo, 0x120 + n, 0xF, 0xF, true), \
+                 (uint32_t)__builtin_amdgcn_update_dpp(0, (int)hi, 0x120 + n, 0xF, 0xF, true)); \
+    } while (0)
+    ROTATE(8);
+    ROTATE(4);
+    ROTATE(2);
+    ROTATE(1);
+#undef ROTATE
+    {
+        HALVES;
+        const auto a = __builtin_amdgcn_permlane16_swap(lo, lo, false, false), b = __builtin_amdgcn_permlane16_swap(hi, hi, false, false);
+        x = with(__builtin_bit_cast(double, (uint64_t)(uint32_t)b[0] << 32 | (uint32_t)a[0]), (uint32_t)a[1], (uint32_t)b[1]);
+    }
+    {
+        HALVES;
+        const auto a = __builtin_amdgcn_permlane32_swap(lo, lo, false, false), b = __builtin_amdgcn_permlane32_swap(hi, hi, false, false);
+        x = with(__builtin_bit_cast(double, (uint64_t)(uint32_t)b[0] << 32 | (uint32_t)a[0]), (uint32_t)a[1], (uint32_t)b[1]);
+    }
+#undef HALVES
     return x;
 }
 
-constexpr uint32_t kRoom = 128;                  // logits of a part that are ranked at a time (two a lane)
+constexpr uint32_t kThreads = 256, kWaves = kThreads / 64;
+constexpr uint32_t kMostTiles = 8;               // of a part
+constexpr uint32_t kRoom = 256;                  // logits of a part that are ranked at a time
+constexpr uint32_t kHits = 256;                  // threads' shares of tiles with a logit that may be among the largest
 
-// Rank of each of a wave's n <= 128 keys (lane l's a is key l, its b key 64 + l): how many are larger.
-__device__ __forceinline__ void rank_keys(uint64_t a, uint64_t b, uint32_t n, uint32_t &ra, uint32_t &rb)
-{
-    ra = rb = 0;
-    const uint32_t first = n < 64 ? n : 64;
-    auto other = [](uint64_t k, uint32_t j) {
-        return (uint64_t)(uint32_t)__builtin_amdgcn_readlane((int)(k >> 32), (int)j) << 32 |
-               (uint32_t)__builtin_amdgcn_readlane((int)k, (int)j);
-    };
-    for (uint32_t j = 0; j < first; ++j) {
-        const uint64_t k = other(a, j);
-        ra += k > a;
-        rb += k > b;
+// Keys that order by logit, then by place within the part, the earlier first; minus zero is no smaller than zero.
+template <int TY>
+struct Key {                                     // of 16-bit logits: the logit's bits in order, and 16 bits of place
+    typedef uint32_t T;
+    static __device__ __forceinline__ T of(float x, uint32_t place)
+    {
+        uint32_t h;
+        if constexpr (TY == BF16) h = __builtin_bit_cast(uint32_t, x + 0.0f) >> 16;
+        else h = __builtin_bit_cast(uint16_t, (_Float16)(x + 0.0f));
+        return (h ^ (h & 0x8000u ? 0xFFFFu : 0x8000u)) << 16 | (0xFFFFu - place);
     }
-    for (uint32_t j = 64; j < n; ++j) {
-        const uint64_t k = other(b, j - 64);
-        ra += k > a;
-        rb += k > b;
+    static __device__ __forceinline__ Cand cand(T k, uint32_t token0)
+    {
+        const uint32_t o = k >> 16, h = o ^ (o & 0x8000u ? 0x8000u : 0xFFFFu);
+        if constexpr (TY == BF16) return Cand{__builtin_bit_cast(float, h << 16), token0 + (0xFFFFu - (k & 0xFFFFu))};
+        else return Cand{(float)__builtin_bit_cast(_Float16, (uint16_t)h), token0 + (0xFFFFu - (k & 0xFFFFu))};
     }
-}
+};
+template <>
+struct Key<F32> {
+    typedef uint64_t T;
+    static __device__ __forceinline__ T of(float x, uint32_t place) { return (uint64_t)ordered(x + 0.0f) << 32 | (0xFFFFFFFFu - place); }
+    static __device__ __forceinline__ Cand cand(T k, uint32_t token0) { return Cand{unordered((uint32_t)(k >> 32)), token0 + (0xFFFFFFFFu - (uint32_t)k)}; }
+};
 
-template <int TY, int E>
-__global__ __launch_bounds__(256) void k_beam_parts(BeamArgs g)
+// One workgroup a part of up to eight tiles; of a tile a thread has TP pieces of 16 bytes, read while the tile before is worked on.
+template <int TY, int TP, bool MASK>
+__global__ __launch_bounds__(kThreads) void k_beam_parts(BeamArgs g)
 {
-    constexpr int N = Type<TY>::N, W = Type<TY>::W, U = E / N;
-    __shared__ uint64_t room[4][kRoom];
-    const uint32_t lane = threadIdx.x & 63u, wave = (uint32_t)__builtin_amdgcn_readfirstlane((int)(threadIdx.x >> 6));
-    const uint32_t item = blockIdx.x * 4 + wave;
-    const uint32_t row = item / g.parts, part = item - row * g.parts;
-    if (row >= g.groups * g.beams || !row_runs(g, row)) return;
+    constexpr uint32_t N = Type<TY>::N, W = Type<TY>::W, kPiece = kThreads * N, kTile = TP * kPiece;
+    static_assert(kMostTiles * kTile <= 65536, "places fit 16 bits");
+    typedef typename Key<TY>::T K;
+    __shared__ float tile_top[kMostTiles][kThreads];
+    __shared__ K room[kRoom];
+    __shared__ uint32_t hits[kHits], edges[kWaves], n_hits, n_room;
+    __shared__ K edge_key;
+    const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
+    const uint32_t row = blockIdx.x / g.parts, part = blockIdx.x - row * g.parts;
     const uint8_t *p = static_cast<const uint8_t *>(g.logits) +
                        ((int64_t)(row / g.beams) * g.group_stride + (int64_t)(row % g.beams) * g.beam_stride) * W;
-    const uint32_t t0 = part * (64 * E) + lane * N;          // the lane's first token
-    float x[E];
-    {
-        u4 raw[U];
-        uint32_t bits[U];
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t t = t0 + u * (64 * N);
-            raw[u] = u4{0, 0, 0, 0};
-            if (t + N <= g.vocab) __builtin_memcpy(&raw[u], p + (uint64_t)t * W, 16);
-            bits[u] = t < g.vocab ? 0xFFFFFFFFu : 0;
-            if (g.allowed && t < g.vocab) bits[u] = g.allowed[(uint64_t)row * g.words + (t >> 5)] >> (t & 31u);
-        }
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const uint32_t t = t0 + u * (64 * N);
-            unpack<TY>(raw[u], x + u * N);
-            if (t < g.vocab && t + N > g.vocab) {            // a row's last tokens
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if (t + i < g.vocab) x[u * N + i] = one_logit<TY>(p + (uint64_t)(t + i) * W);
-                    else bits[u] &= ~(1u << i);
-            }
-            if (g.allowed || t + N > g.vocab) {
-#pragma unroll
-                for (int i = 0; i < N; ++i)
-                    if (!(bits[u] >> i & 1u)) x[u * N + i] = -kInf;
-            }
-        }
-    }
-    float mine = -kInf;
-#pragma unroll
-    for (int i = 0; i < E; ++i) mine = fmaxf(mine, x[i]);    // (NaN is left out here; it shows in the sum)
-    const float top = wave_max(mine);
-    const float base = top == -kInf ? 0.0f : top, c = (float)(g.scale * 1.4426950408889634);
-    float s[4] = {0, 0, 0, 0};
-#pragma unroll
-    for (int i = 0; i < E; ++i) s[i & 3] += __builtin_amdgcn_exp2f((x[i] - base) * c);
-    const double sum = wave_sum((double)(s[0] + s[1]) + (double)(s[2] + s[3]));
+    const uint32_t *allowed = MASK ? g.allowed + (uint64_t)row * g.words : nullptr;
+    const uint32_t token0 = part * g.tiles * kTile, left = g.vocab - token0;
+    const uint32_t n_tiles = left > g.tiles * kTile ? g.tiles : (left + kTile - 1) / kTile;
+    if (tid == 0) n_hits = n_room = 0;
 
-    const uint64_t at = (uint64_t)row * g.parts + part;
-    if (lane == 0) {
-        g.stat[at].top = top;
-        g.stat[at].sum = sum;
-    }
-    // the part's n_out largest: keys that order by logit, then by token, the earlier first
-    float edge = fmaxf(unordered(nth_largest(ordered(mine), g.n_out)), kLowest);
-    uint32_t edge_token = 0xFFFFFFFFu;           // of logits equal to the edge, those up to this token
-    uint32_t n;
-    uint64_t ka, kb;
-    uint32_t ra, rb;
-    for (;;) {
-        n = 0;
+    // a thread's maximum so far and its sum of exponentials relative to that
+    float top = -kInf, sum = 0.0f;
+    const float c = (float)(g.scale * 1.4426950408889634);
+    struct Buffer {
+        u4 raw[TP];
+        uint32_t bits[TP];
+    };
+    auto load = [&](uint32_t tile, Buffer &f) {
 #pragma unroll
-        for (int i = 0; i < E; ++i) {
-            const uint32_t t = t0 + (i / N) * (64 * N) + i % N;
-            const uint64_t m = __ballot(x[i] > edge || (x[i] == edge && t <= edge_token));
-            if (m) {
-                const uint32_t to = n + (uint32_t)__popcll(m & zxk::lanemask_lt());
-                // (+ 0: minus zero is no smaller than zero)
-                if ((m >> lane & 1u) && to < kRoom) room[wave][to] = (uint64_t)ordered(x[i] + 0.0f) << 32 | (0xFFFFFFFFu - t);
-                n += (uint32_t)__popcll(m);
+        for (int u = 0; u < TP; ++u) {
+            const uint32_t t = token0 + tile * kTile + u * kPiece + tid * N;
+            f.raw[u] = fetch<TY>(p, t, g.vocab);
+            if (MASK) f.bits[u] = t < g.vocab ? allowed[t >> 5] >> (t & 31u) | ~((1u << N) - 1u) : 0;
+        }
+    };
+    auto work = [&](uint32_t tile, Buffer &f) {
+        if (MASK || left < (tile + 1) * kTile) {
+#pragma unroll
+            for (int u = 0; u < TP; ++u) {
+                const uint32_t t = token0 + tile * kTile + u * kPiece + tid * N;
+                f.raw[u] = settle<TY>(f.raw[u], p, t, g.vocab, there(t, N, g.vocab) & (MASK ? f.bits[u] : 0xFFFFFFFFu));
             }
         }
-        zxk::wave_sync();
-        const uint32_t some = n < kRoom ? n : kRoom;
-        ka = lane < some ? room[wave][lane] : 0;
-        kb = lane + 64 < some ? room[wave][lane + 64] : 0;
-        rank_keys(ka, kb, some, ra, rb);
-        if (n <= kRoom) break;
-        // too many: the n_out-th of those that fit is an edge that leaves out kRoom - n_out of them at least
-        const uint64_t ma = __ballot(ra == g.n_out - 1), mb = __ballot(rb == g.n_out - 1);
-        const uint64_t k = ma ? ka : kb;
-        const int l = __builtin_ctzll(ma ? ma : mb);
-        edge = unordered((uint32_t)__builtin_amdgcn_readlane((int)(k >> 32), l));
-        edge_token = 0xFFFFFFFFu - (uint32_t)__builtin_amdgcn_readlane((int)k, l);
-        zxk::wave_sync();
+        float x[TP][N], best = -kInf;            // (NaN is left out of the maximum; it shows in the sum)
+#pragma unroll
+        for (int u = 0; u < TP; ++u) {
+            unpack<TY>(f.raw[u], x[u]);
+#pragma unroll
+            for (uint32_t i = 0; i < N; ++i) best = fmaxf(best, x[u][i]);
+        }
+        tile_top[tile][tid] = best;
+        const float now = fmaxf(top, best), from = now == -kInf ? 0.0f : now;
+        float s[4] = {sum * __builtin_amdgcn_exp2f((top - from) * c), 0, 0, 0};
+        top = now;
+#pragma unroll
+        for (int u = 0; u < TP; ++u)
+#pragma unroll
+            for (uint32_t i = 0; i < N; ++i) s[i & 3] += __builtin_amdgcn_exp2f((x[u][i] - from) * c);
+        sum = (s[0] + s[1]) + (s[2] + s[3]);
+    };
+    Buffer a, b;
+    load(0, a);                                  // beside the score and the flag that say whether the row is needed
+    if (!row_runs(g, row)) return;
+    for (uint32_t tile = 0; tile < n_tiles; tile += 2) {
+        if (tile + 1 < n_tiles) load(tile + 1, b);
+        work(tile, a);
+        if (tile + 1 >= n_tiles) break;
+        if (tile + 2 < n_tiles) load(tile + 2, a);
+        work(tile + 1, b);
     }
-    Cand *o = g.cand + at * g.n_out;
-    if (lane < n && ra < g.n_out) o[ra] = Cand{unordered((uint32_t)(ka >> 32)), 0xFFFFFFFFu - (uint32_t)ka};
-    if (lane + 64 < n && rb < g.n_out) o[rb] = Cand{unordered((uint32_t)(kb >> 32)), 0xFFFFFFFFu - (uint32_t)kb};
-    if (lane >= n && lane < g.n_out) o[lane] = Cand{-kInf, 0};
+    const float all = wave_max(top), from = all == -kInf ? 0.0f : all;
+    const uint32_t mine = nth_largest(ordered(top), ordered(all), g.n_out);
+    if (lane == 0) edges[wave] = mine;
+    const double total = wave_sum((double)(sum * __builtin_amdgcn_exp2f((top - from) * c)));
+    if (lane == 0) {
+        Stat &o = g.stat[(uint64_t)blockIdx.x * kWaves + wave];
+        o.top = all;
+        o.sum = total;
+    }
+    __syncthreads();
+    // n_out logits of one wave at least reach its edge, so n_out of the part reach the highest; they are hardly more
+    uint32_t high = edges[0];
+#pragma unroll
+    for (uint32_t i = 1; i < kWaves; ++i) high = edges[i] > high ? edges[i] : high;
+    const float edge = fmaxf(unordered(high), kLowest);
+    auto take = [&](const float (&y)[N], uint32_t place, K ek) {     // a piece's logits from the edge on, with keys from ek on
+        uint32_t yes = 0;
+#pragma unroll
+        for (uint32_t i = 0; i < N; ++i) yes |= (uint32_t)(y[i] >= edge && (ek == 0 || Key<TY>::of(y[i], place + i) >= ek)) << i;
+        if (!yes) return;
+        uint32_t to = atomicAdd(&n_room, (uint32_t)__builtin_popcount(yes));
+#pragma unroll
+        for (uint32_t i = 0; i < N; ++i)
+            if (yes >> i & 1u) {
+                if (to < kRoom) room[to] = Key<TY>::of(y[i], place + i);
+                ++to;
+            }
+    };
+    if (g.tiles == 1) {                          // all logits are at hand
+        if (top >= edge) {
+#pragma unroll
+            for (int u = 0; u < TP; ++u) {
+                float y[N];
+                unpack<TY>(a.raw[u], y);
+                take(y, u * kPiece + tid * N, 0);
+            }
+        }
+    } else if (top >= edge) {
+        // the threads and tiles that reach it, then their logits that do, read once more
+        for (uint32_t i = 0; i < n_tiles; ++i) {
+            if (tile_top[i][tid] < edge) continue;
+            const uint32_t to = atomicAdd(&n_hits, 1u);
+            if (to < kHits) hits[to] = i << 8 | tid;
+        }
+    }
+    __syncthreads();
+    const uint32_t v = n_hits;
+    auto sift = [&](uint32_t place, K ek) {
+        const uint32_t t = token0 + place;
+        float y[N];
+        uint32_t bits = there(t, N, g.vocab);
+        if (MASK && t < g.vocab) bits &= allowed[t >> 5] >> (t & 31u) | ~((1u << N) - 1u);
+        unpack<TY>(settle<TY>(fetch<TY>(p, t, g.vocab), p, t, g.vocab, bits), y);
+        take(y, place, ek);
+    };
+    if (g.tiles > 1 && v <= kHits) {
+        for (uint32_t i = tid; i < v * TP; i += kThreads) {
+            const uint32_t h = hits[i / TP];
+            sift((h >> 8) * kTile + (i % TP) * kPiece + (h & 255u) * N, 0);
+        }
+        __syncthreads();
+    }
+    uint32_t n = n_room;
+    auto rank = [&](uint32_t some) {
+        const K k = room[tid < some ? tid : 0];
+        uint32_t r = 0;
+#pragma unroll 8
+        for (uint32_t j = 0; j < some; ++j) r += room[j] > k;
+        return r;
+    };
+    if (v > kHits || n > kRoom) {
+        // more than there is room for, as many equal logits are: the n_out-th of those that fit is a sharper edge, which
+        // leaves out kRoom - n_out of them at least
+        K ek = 0;
+        for (;;) {
+            __syncthreads();
+            if (tid == 0) n_room = 0;
+            __syncthreads();
+            for (uint32_t i = 0; i < n_tiles * TP; ++i) sift(i * kPiece + tid * N, ek);
+            __syncthreads();
+            n = n_room;
+            if (n <= kRoom) break;
+            if (rank(kRoom) == g.n_out - 1) edge_key = room[tid];
+            __syncthreads();
+            ek = edge_key;
+        }
+    }
+    Cand *o = g.cand + (uint64_t)blockIdx.x * g.n_out;
+    if (tid < n) {
+        const uint32_t r = rank(n);
+        if (r < g.n_out) o[r] = Key<TY>::cand(room[tid], token0);
+    } else if (tid < g.n_out) {
+        o[tid] = Cand{-kInf, 0};
+    }
 }
 
 struct Best {
@@ -276,8 +433,17 @@ __global__ __launch_bounds__(NT) void k_beam_pick(BeamArgs g)
     __shared__ uint64_t edge_key, edge_place;
     const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
     const uint32_t row0 = blockIdx.x * g.beams;
+    // the parts' candidates are sorted: an edge is found among the first `depth` of each, and a part's further ones are
+    // looked at only while they reach it
+    const uint32_t lists = g.beams * g.parts, entries = lists * g.depth;
+    const Cand *cand = g.cand + (uint64_t)row0 * g.parts * g.n_out;
+    Cand mine{-kInf, 0};                         // under way while the sums are joined (rows that are not needed hold anything)
+    if (tid < entries) mine = cand[(uint64_t)(tid / g.depth) * g.n_out + tid % g.depth];
     for (uint32_t b = wave; b < g.beams; b += NT / 64) {
-        const uint32_t row = row0 + b;
+        const uint32_t row = row0 + b, stats = g.parts * kWaves;
+        const Stat *stat = g.stat + (uint64_t)row * stats;
+        Stat v{-kInf, 0, 0.0};
+        if (lane < stats) v = stat[lane];
         const float sc = g.scores[row], w = g.weights ? g.weights[row] : 1.0f;
         const bool ended = g.finished && g.finished[row];
         uint32_t k = 0;
@@ -288,11 +454,12 @@ __global__ __launch_bounds__(NT) void k_beam_pick(BeamArgs g)
         if (there && !bad) {
             k = 2;
             if (!ended) {
-                for (uint32_t i = lane; i < g.parts; i += 64) top = fmaxf(top, g.stat[(uint64_t)row * g.parts + i].top);
+                top = v.top;
+                for (uint32_t i = lane + 64; i < stats; i += 64) top = fmaxf(top, stat[i].top);
                 top = wave_max(top);
                 double s = 0.0;
-                for (uint32_t i = lane; i < g.parts; i += 64) {
-                    const Stat v = g.stat[(uint64_t)row * g.parts + i];
+                for (uint32_t i = lane; i < stats; i += 64) {
+                    if (i >= 64) v = stat[i];
                     s += v.top == -kInf ? v.sum : v.sum * exp(((double)v.top - (double)top) * g.scale);
                 }
                 s = wave_sum(s);
@@ -309,46 +476,53 @@ __global__ __launch_bounds__(NT) void k_beam_pick(BeamArgs g)
             if (bad) report(g.err, ZX_E_CORRUPT);
         }
     }
+    if (tid == 0) count = 0;
     __syncthreads();
-    // entries: the parts' candidates of all rows, then one for each finished beam
-    const uint32_t each = g.parts * g.n_out, all = g.beams * each;
-    const Cand *cand = g.cand + (uint64_t)row0 * each;
-    auto entry = [&](uint32_t e, Best &o) {
-        const bool part = e < all;
-        const uint32_t b = part ? e / each : e - all;
-        if (kind[b] != (part ? 1u : 2u)) return false;
-        if (part) {
-            const Cand v = cand[e];
-            if (v.x == -kInf) return false;
-            o.total = base[b] + ((double)v.x - tops[b]) * g.scale;       // (score - ln sum) + s (x - top): no large logit swallows the rest
-            o.place = (uint64_t)b << 32 | v.token;
-        } else {
-            o.total = base[b];
-            o.place = (uint64_t)b << 32 | (uint32_t)g.end;
-        }
+    auto value = [&](uint32_t list, Cand v, Best &o) {
+        const uint32_t b = list / g.parts;
+        if (kind[b] != 1 || v.x == -kInf) return false;
+        o.total = base[b] + ((double)v.x - tops[b]) * g.scale;       // (score - ln sum) + s (x - top): no large logit swallows the rest
+        o.place = (uint64_t)b << 32 | v.token;
         o.key = ordered(o.total * weight[b] + 0.0);
         return true;
     };
-    uint64_t mine = 0;
-    for (uint32_t e = tid; e < all + g.beams; e += NT) {
+    auto entry = [&](uint32_t list, uint32_t nth, Best &o) { return value(list, cand[(uint64_t)list * g.n_out + nth], o); };
+    Best own;
+    const bool have = tid < entries && value(tid / g.depth, mine, own);
+    uint64_t key = have ? own.key : 0;
+    for (uint32_t e = tid + NT; e < entries; e += NT) {
         Best v;
-        if (entry(e, v) && v.key > mine) mine = v.key;
+        if (entry(e / g.depth, e % g.depth, v) && v.key > key) key = v.key;
     }
     // n_out keys of one wave at least reach the edge (or it is zero), so n_out of the group do
-    const uint32_t hi = nth_largest((uint32_t)(mine >> 32), g.n_out);
+    const uint32_t key_hi = (uint32_t)(key >> 32);
+    const uint32_t hi = nth_largest(key_hi, wave_reduce(key_hi, [](uint32_t a, uint32_t b) { return a > b ? a : b; }), g.n_out);
     if (lane == 0) edge_hi[wave] = hi;
-    if (tid == 0) count = 0;
     __syncthreads();
     uint32_t h = 0;
     for (int i = 0; i < NT / 64; ++i) h = edge_hi[i] > h ? edge_hi[i] : h;
     uint64_t ek = (uint64_t)h << 32, ep = ~0ull;
     uint32_t n;
     for (uint32_t round = 0;; ++round) {
-        for (uint32_t e = tid; e < all + g.beams; e += NT) {
-            Best v;
-            if (!entry(e, v) || better(ek, ep, v.key, v.place)) continue;
+        auto enter = [&](const Best &v) {
+            if (better(ek, ep, v.key, v.place)) return false;
             const uint32_t to = atomicAdd(&count, 1u);
             if (to < kList) list[to] = v;
+            return true;
+        };
+        for (uint32_t e = tid; e < entries; e += NT) {
+            const uint32_t l = e / g.depth, nth = e % g.depth;
+            Best v = own;
+            if (!(e == tid ? have : entry(l, nth, v)) || !enter(v) || nth + 1 < g.depth) continue;
+            for (uint32_t i = g.depth; i < g.n_out; ++i)
+                if (!entry(l, i, v) || !enter(v)) break;
+        }
+        if (tid < g.beams && kind[tid] == 2) {   // finished: one candidate
+            Best v;
+            v.total = base[tid];
+            v.place = (uint64_t)tid << 32 | (uint32_t)g.end;
+            v.key = ordered(v.total * weight[tid] + 0.0);
+            enter(v);
         }
         __syncthreads();
         n = count;
@@ -356,6 +530,7 @@ __global__ __launch_bounds__(NT) void k_beam_pick(BeamArgs g)
         for (uint32_t i = tid; i < some; i += NT) {
             const Best v = list[i];
             uint32_t r = 0;
+#pragma unroll 8
             for (uint32_t j = 0; j < some; ++j) r += better(list[j].key, list[j].place, v.key, v.place);
             if (n > kList) {
                 if (r == g.n_out - 1) {          // more than fit: another round from the n_out-th of those that did on
@@ -372,7 +547,7 @@ __global__ __launch_bounds__(NT) void k_beam_pick(BeamArgs g)
             }
         }
         __syncthreads();
-        if (n <= kList || round > all / 512) break;          // (each round leaves out kList - n_out at least)
+        if (n <= kList || round > lists) break;          // (each round leaves out kList - n_out at least)
         ek = edge_key;
         ep = edge_place;
         if (tid == 0) count = 0;
@@ -387,34 +562,42 @@ __global__ __launch_bounds__(NT) void k_beam_pick(BeamArgs g)
     }
 }
 
-// Logits a lane holds: as many as leave the card about 1024 waves, up to 64 (32 in 32 bits: the same bytes).
-inline uint32_t lane_logits(int type, uint64_t rows, uint32_t vocab)
+template <int TY, bool MASK>
+void launch_parts(const BeamArgs &g, uint32_t pieces, uint32_t wgs, hipStream_t stream)
 {
-    uint32_t e = type == F32 ? 32 : 64;
-    while (e > 8 && rows * ((vocab + 64ull * e - 1) / (64ull * e)) < 1024) e >>= 1;
-    return e;
+    if (pieces == 1) hipLaunchKernelGGL((k_beam_parts<TY, 1, MASK>), dim3(wgs), dim3(kThreads), 0, stream, g);
+    else hipLaunchKernelGGL((k_beam_parts<TY, 4, MASK>), dim3(wgs), dim3(kThreads), 0, stream, g);
 }
-
 template <int TY>
-void launch_parts(const BeamArgs &g, uint32_t e, uint32_t wgs, hipStream_t stream)
+void launch_parts(const BeamArgs &g, uint32_t pieces, uint32_t wgs, hipStream_t stream)
 {
-    if (e == 8) hipLaunchKernelGGL((k_beam_parts<TY, 8>), dim3(wgs), dim3(256), 0, stream, g);
-    else if (e == 16) hipLaunchKernelGGL((k_beam_parts<TY, 16>), dim3(wgs), dim3(256), 0, stream, g);
-    else if (e == 32) hipLaunchKernelGGL((k_beam_parts<TY, 32>), dim3(wgs), dim3(256), 0, stream, g);
-    else if constexpr (TY != F32) hipLaunchKernelGGL((k_beam_parts<TY, 64>), dim3(wgs), dim3(256), 0, stream, g);
+    if (g.allowed) launch_parts<TY, true>(g, pieces, wgs, stream);
+    else launch_parts<TY, false>(g, pieces, wgs, stream);
 }
 
-// ZX_OK, and how the rows are split, where the sizes can be served.
-inline zx_status plan(int type, uint32_t groups, uint32_t beams, uint32_t vocab, uint32_t n_out, uint32_t &e, uint32_t &parts)
+// How rows are split.
+struct Split {
+    uint32_t pieces, tiles, parts;               // pieces of a tile a thread, tiles of a part, parts of a row
+};
+
+// ZX_OK and the split, where the sizes can be served.
+inline zx_status plan(int type, uint32_t groups, uint32_t beams, uint32_t vocab, uint32_t n_out, Split &o)
 {
     if (type != ZX_LOGITS_BF16 && type != ZX_LOGITS_F16 && type != ZX_LOGITS_F32) return ZX_E_UNSUPPORTED;
     if (beams == 0 || beams > kMostBeams || n_out == 0 || n_out > kMostOut || vocab == 0) return ZX_E_INVAL;
     if (vocab > kMostVocab) return ZX_E_LIMIT;
     const uint64_t rows = (uint64_t)groups * beams;
-    e = lane_logits(type, rows, vocab);
-    parts = (uint32_t)((vocab + 64ull * e - 1) / (64ull * e));
+    const uint32_t piece = kThreads * (type == F32 ? 4 : 8);
+    auto up = [](uint64_t a, uint64_t b) { return (a + b - 1) / b; };
+    o.pieces = rows * up(vocab, 4 * piece) < 256 ? 1 : 4;
+    const uint64_t row_tiles = up(vocab, o.pieces * piece);
+    uint64_t tiles = up(rows * row_tiles, 1024);
+    if (tiles > kMostTiles) tiles = kMostTiles;
+    if (tiles == 0) tiles = 1;
+    o.parts = (uint32_t)up(row_tiles, tiles);
+    o.tiles = (uint32_t)up(row_tiles, o.parts);
     // a launch counts its threads in 32 bits
-    if (rows > 0x7FFFFFFFull || rows * parts > (1ull << 26) - 4) return ZX_E_LIMIT;
+    if (rows > 0x7FFFFFFFull || rows * o.parts >= 1ull << 24) return ZX_E_LIMIT;
     return ZX_OK;
 }
 
@@ -424,9 +607,9 @@ static_assert(zxb::BF16 == ZX_LOGITS_BF16 && zxb::F16 == ZX_LOGITS_F16 && zxb::F
 
 extern "C" size_t zx_beam_select_workspace_bytes(int32_t type, uint32_t n_groups, uint32_t beams, uint32_t vocab, uint32_t n_out)
 {
-    uint32_t e, parts;
-    if (zxb::plan(type, n_groups, beams, vocab, n_out, e, parts) != ZX_OK) return 0;
-    return (size_t)n_groups * beams * parts * (sizeof(zxb::Stat) + n_out * sizeof(zxb::Cand));
+    zxb::Split sp;
+    if (zxb::plan(type, n_groups, beams, vocab, n_out, sp) != ZX_OK) return 0;
+    return (size_t)n_groups * beams * sp.parts * (zxb::kWaves * sizeof(zxb::Stat) + n_out * sizeof(zxb::Cand));
 }
 
 extern "C" zx_status zx_beam_select(const zx_beam_logits *in, const float *scores, const float *weights, const uint8_t *finished,
@@ -436,8 +619,8 @@ extern "C" zx_status zx_beam_select(const zx_beam_logits *in, const float *score
 {
     using namespace zxb;
     if (!in) return ZX_E_INVAL;
-    uint32_t e, parts;
-    const zx_status st = plan(in->type, in->n_groups, in->beams, in->vocab, n_out, e, parts);
+    Split sp;
+    const zx_status st = plan(in->type, in->n_groups, in->beams, in->vocab, n_out, sp);
     if (st != ZX_OK) return st;
     if (in->n_groups == 0) return ZX_OK;
     const uintptr_t width = in->type == ZX_LOGITS_F32 ? 4 : 2;
@@ -456,7 +639,7 @@ extern "C" zx_status zx_beam_select(const zx_beam_logits *in, const float *score
     g.finished = finished;
     g.allowed = allowed;
     g.stat = static_cast<Stat *>(workspace);
-    g.cand = reinterpret_cast<Cand *>(g.stat + rows * parts);
+    g.cand = reinterpret_cast<Cand *>(g.stat + rows * sp.parts * kWaves);
     g.out_scores = out_scores;
     g.parents = parents;
     g.tokens = tokens;
@@ -467,14 +650,17 @@ extern "C" zx_status zx_beam_select(const zx_beam_logits *in, const float *score
     g.beams = in->beams;
     g.vocab = in->vocab;
     g.n_out = n_out;
-    g.parts = parts;
+    g.parts = sp.parts;
+    g.tiles = sp.tiles;
     g.words = (in->vocab + 31) / 32;
     g.end = end;
-    const uint32_t wgs = (uint32_t)((rows * parts + 3) / 4);
-    if (in->type == ZX_LOGITS_BF16) launch_parts<BF16>(g, e, wgs, stream);
-    else if (in->type == ZX_LOGITS_F16) launch_parts<F16>(g, e, wgs, stream);
-    else launch_parts<F32>(g, e, wgs, stream);
-    if ((uint64_t)in->beams * parts * n_out > 4096) hipLaunchKernelGGL((k_beam_pick<1024>), dim3(in->n_groups), dim3(1024), 0, stream, g);
+    const uint32_t wgs = (uint32_t)(rows * sp.parts);
+    if (in->type == ZX_LOGITS_BF16) launch_parts<BF16>(g, sp.pieces, wgs, stream);
+    else if (in->type == ZX_LOGITS_F16) launch_parts<F16>(g, sp.pieces, wgs, stream);
+    else launch_parts<F32>(g, sp.pieces, wgs, stream);
+    const uint32_t lists = in->beams * sp.parts, threads = lists > 512 || in->beams > 4 ? 1024 : 256;
+    g.depth = lists >= threads ? 1 : threads / lists < n_out ? threads / lists : n_out;
+    if (threads == 1024) hipLaunchKernelGGL((k_beam_pick<1024>), dim3(in->n_groups), dim3(1024), 0, stream, g);
     else hipLaunchKernelGGL((k_beam_pick<256>), dim3(in->n_groups), dim3(256), 0, stream, g);
     return hipGetLastError() == hipSuccess ? ZX_OK : ZX_E_HIP;
 }

