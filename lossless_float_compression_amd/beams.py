@@ -29,6 +29,17 @@ class Beams(NamedTuple):
 
 
 _bound = None
+_needs = {}                              # workspace sizes, by the sizes that decide them
+_MOST_NEEDS = 256
+_makers = {}                             # by device: what allocates floats, words, flags and bytes there
+
+
+def _like_what(index: int, device: torch.device):
+    """Functions of a size that allocate float32, int32, bool and uint8 tensors (an empty tensor's own is the quickest way)."""
+    m = _makers.get(index)
+    if m is None:
+        m = _makers[index] = tuple(torch.empty(0, dtype=t, device=device).new_empty for t in (torch.float32, torch.int32, torch.bool, torch.uint8))
+    return m
 
 
 def _lib():
@@ -47,7 +58,7 @@ def _lib():
 
 
 def _like(t: torch.Tensor, name: str, dtype: torch.dtype, shape, index: int) -> torch.Tensor:
-    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or tuple(t.shape) != tuple(shape) or t.get_device() != index or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype is not dtype or t.shape != shape or t.get_device() != index or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor {list(shape)} on cuda:{index}")
     return t
 
@@ -88,25 +99,29 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: Optional[int]
     if sv != 1 and V > 1:
         raise ValueError("logits: neighbouring tokens must lie side by side")
     _like(scores, "scores", torch.float32, (G, K), index)
+    pw = pf = pa = None
     if weights is not None:
-        _like(weights, "weights", torch.float32, (G, K), index)
-    if finished is not None:
-        _like(finished, "finished", torch.bool, (G, K), index)
-        if end is None:
+        pw = _like(weights, "weights", torch.float32, (G, K), index).data_ptr()
+    if end is None:
+        end = -1
+        if finished is not None:
             raise ValueError("finished needs end")
-    if end is not None and not 0 <= end < V:
+    elif not 0 <= end < V:
         raise ValueError("end must be a token")
+    if finished is not None:
+        pf = _like(finished, "finished", torch.bool, (G, K), index).data_ptr()
     if allowed is not None:
-        _like(allowed, "allowed", torch.int32, (G, K, (V + 31) // 32), index)
+        pa = _like(allowed, "allowed", torch.int32, (G, K, (V + 31) // 32), index).data_ptr()
     if not (0.0 < scale <= 1e30):
         raise ValueError("scale must be positive")
     if logits.requires_grad or scores.requires_grad or _forward._current_level >= 0:
         for t, name in ((logits, "logits"), (scores, "scores"), (weights, "weights")):
             if t is not None:
                 _no_gradient(t, name)
+    f32, i32, flags, raw = _like_what(index, device)
     if out is None:
-        out = Beams(torch.empty((G, M), dtype=torch.float32, device=device), torch.empty((G, M), dtype=torch.int32, device=device),
-                    torch.empty((G, M), dtype=torch.int32, device=device), torch.empty((G, M), dtype=torch.bool, device=device))
+        size = (G, M)
+        out = Beams(f32(size), i32(size), i32(size), flags(size))
     else:
         for i, (t, name, dt) in enumerate(zip(out, Beams._fields, (torch.float32, torch.int32, torch.int32, torch.bool))):
             _like(t, "out." + name, dt, (G, M), index)
@@ -119,31 +134,40 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: Optional[int]
     e = None if err is None else _int32(err, "err", index).data_ptr()
     if G == 0:
         return out
-    L = _lib()
-    c = zx_beam_logits(logits.data_ptr(), sg if G > 1 else 0, sk if K > 1 else 0, _LOGITS[logits.dtype], G, K, V)
-    need = L.zx_beam_select_workspace_bytes(c.type, G, K, V, M)
-    ws = torch.empty(need, dtype=torch.uint8, device=device)
-    ptr = lambda t: None if t is None else t.data_ptr()   # noqa: E731
-    st = L.zx_beam_select(C.byref(c), scores.data_ptr(), ptr(weights), ptr(finished), -1 if end is None else int(end), ptr(allowed), scale, M,
-                          out.scores.data_ptr(), out.parents.data_ptr(), out.tokens.data_ptr(), out.finished.data_ptr(), ws.data_ptr(), need,
-                          e, _zx._raw_stream(device))
+    L = _bound or _lib()
+    kind = _LOGITS[logits.dtype]
+    key = (kind, G, K, V, M)
+    need = _needs.get(key)
+    if need is None:
+        if len(_needs) >= _MOST_NEEDS:
+            _needs.clear()
+        need = _needs[key] = L.zx_beam_select_workspace_bytes(*key)
+    st = L.zx_beam_select(C.byref(zx_beam_logits(logits.data_ptr(), sg if G > 1 else 0, sk if K > 1 else 0, kind, G, K, V)), scores.data_ptr(),
+                          pw, pf, end, pa, scale, M, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(),
+                          raw(need).data_ptr(), need, e, _zx._raw_stream(device))
     if st != 0:
         raise _zx.ZxError("zx_beam_select", st)
     return out
 
 
-def _part(t: torch.Tensor, name: str, shape, index: int, written: bool = False) -> zx_rows:
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or tuple(t.shape) != tuple(shape) or t.get_device() != index:
+def _part(t: torch.Tensor, name: str, shape, index: int, written: bool = False):
+    """The rows, and the first byte that they reach and the one behind the last."""
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != index:
         raise ValueError(f"{name} must be a bfloat16 tensor {list(shape)} on cuda:{index}")
     if t.requires_grad or _forward._current_level >= 0:
         _no_gradient(t, name)
+    n, h, d = shape
     s0, s1, s2 = t.stride()
-    s0, s1 = s0 if shape[0] > 1 else 0, s1 if shape[1] > 1 else 0
-    if s2 != 1 or s0 % 8 or s1 % 8 or t.data_ptr() % 16:
+    p = t.data_ptr()
+    if n < 2:
+        s0 = 0
+    if h < 2:
+        s1 = 0
+    if s2 != 1 or s0 % 8 or s1 % 8 or p % 16:
         raise ValueError(f"{name}: channels must be contiguous, and the start and the other strides multiples of 16 bytes")
-    if written and not _apart(shape[:2], (s0, s1), shape[2]):
+    if written and not _apart((n, h), (s0, s1), d):
         raise ValueError(f"{name}: rows that are written must not overlap")
-    return zx_rows(t.data_ptr(), s0, s1)
+    return zx_rows(p, s0, s1), p, p + 2 * ((n - 1) * s0 + (h - 1) * s1 + d) if n else p
 
 
 def merge_attention(outs: Sequence[torch.Tensor], lses: Sequence[torch.Tensor], out: Optional[torch.Tensor] = None,
@@ -164,29 +188,35 @@ def merge_attention(outs: Sequence[torch.Tensor], lses: Sequence[torch.Tensor], 
     shape, index, device = f.shape, f.get_device(), f.device
     if _away(index, stream):
         return _elsewhere(device, stream, (*outs, *lses, out, lse), lambda s: merge_attention(outs, lses, out, lse, s))
-    parts = [_part(t, f"outs[{i}]", shape, index) for i, t in enumerate(outs)]
-    for i, t in enumerate(lses):
-        _like(t, f"lses[{i}]", torch.float32, shape[:2], index)
+    n, heads, d = shape
+    parts = [_part(t, "a part", shape, index) for t in outs]
+    rows = shape[:2]
+    where = [_like(t, "an lse", torch.float32, rows, index).data_ptr() for t in lses]
+    size = 4 * n * heads
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=device)
-        o = zx_rows(out.data_ptr(), shape[1] * shape[2], shape[2])
+        out = f.new_empty(shape)
+        o = zx_rows(out.data_ptr(), heads * d, d)
     else:
-        o = _part(out, "out", shape, index, True)
-        if any(_meets(out, t) for t in lses) or any(_meets(out, t) and not (t.data_ptr() == out.data_ptr() and t.stride() == out.stride())
-                                                    for t in outs):
+        o, p, q = _part(out, "out", shape, index, True)
+        if any(p < x + size and x < q for x in where) or any(p < y and x < q and not (
+                x == p and r.token_stride == o.token_stride and r.head_stride == o.head_stride) for r, x, y in parts):
             raise ValueError("out shares memory with a part and is not that part")
+        if lse is not None and _meets(out, lse):
+            raise ValueError("out and lse share memory")
+    pl = None
     if lse is not None:
-        _like(lse, "lse", torch.float32, shape[:2], index)
-        if any(_meets(lse, t) for t in (*outs, out)) or any(_meets(lse, t) and t.data_ptr() != lse.data_ptr() for t in lses):
+        pl = _like(lse, "lse", torch.float32, rows, index).data_ptr()
+        if any(pl < y and x < pl + size for _, x, y in parts) or any(pl != x and pl < x + size and x < pl + size for x in where):
             raise ValueError("lse shares memory with a part and is not that part's")
-    for t in (*lses, lse):
-        if t is not None and (t.requires_grad or _forward._current_level >= 0):
-            _no_gradient(t, "an lse")
-    if shape[0] == 0:
+    if _forward._current_level >= 0 or any(t.requires_grad for t in lses) or (lse is not None and lse.requires_grad):
+        for t in (*lses, lse):
+            if t is not None:
+                _no_gradient(t, "an lse")
+    if n == 0:
         return out
-    n = len(outs)
-    st = _lib().zx_attention_merge((zx_rows * n)(*parts), (C.c_void_p * n)(*[t.data_ptr() for t in lses]), n, shape[0], shape[1], shape[2],
-                                   C.byref(o), None if lse is None else lse.data_ptr(), _zx._raw_stream(device))
+    k = len(parts)
+    st = (_bound or _lib()).zx_attention_merge((zx_rows * k)(*[r for r, _, _ in parts]), (C.c_void_p * k)(*where), k, n, heads, d, C.byref(o), pl,
+                                               _zx._raw_stream(device))
     if st != 0:
         raise _zx.ZxError("zx_attention_merge", st)
     return out

@@ -103,6 +103,23 @@ def _meets(a: torch.Tensor, b: torch.Tensor) -> bool:
     return p < s and r < q
 
 
+def _words(t: torch.Tensor) -> Tuple[int, int]:
+    """`_span` of a contiguous int32 tensor."""
+    p = t.data_ptr()
+    return p, p + 4 * t.numel()
+
+
+def _all_apart(spans: list) -> None:
+    """Refuse stretches of memory that meet."""
+    spans.sort()
+    end = 0
+    for p, q in spans:
+        if p < end and p < q:
+            raise ValueError("the tensors that are read and written must not share memory")
+        if q > end:
+            end = q
+
+
 class PageCopies:
     """A list of copies to be made, on the device: `count` (int32 [1]) says how many of the rows of `pairs` (int32 [cap, 3]: source
     page, destination page, tokens from the page's start) are meant.  Allocated here, or given."""
@@ -121,6 +138,7 @@ class PageCopies:
         if pairs.shape != (cap, 3) or count.shape != (1,) or pairs.device != count.device or _meets(pairs, count):
             raise ValueError(f"pairs must be [{cap}, 3] and count [1], on one device and apart")
         self.cap, self.pairs, self.count, self.device = int(cap), pairs, count, pairs.device
+        self._spans = (_words(pairs), _words(count))
         self._c = zx_page_copies(pairs.data_ptr(), count.data_ptr(), self.cap, 0)
         self._ref = C.byref(self._c)
 
@@ -149,23 +167,26 @@ class PagePool:
         self._index = refs.get_device()
         self._c = zx_page_pool(self.n_pages, self.page_tokens, refs.data_ptr())
         self._ref = C.byref(self._c)
-        self._bytes = torch.empty(0, dtype=torch.uint8, device=self.device)
+        self._bytes = torch.empty(0, dtype=torch.uint8, device=self.device)     # what workspaces are allocated like
+        self._own = _words(refs)
+        self._needs = {}                         # workspace sizes, by the number of rows
 
     # ---- argument checks
-    def _rows(self, table: torch.Tensor, held: torch.Tensor, *apart: Optional[torch.Tensor]) -> zx_page_rows:
+    def _rows(self, table: torch.Tensor, held: torch.Tensor, err: Optional[torch.Tensor], *apart) -> Tuple[zx_page_rows, Optional[int]]:
+        """The rows, and err's address; `apart`: spans of what else is read or written."""
         _int32(table, "table", self._index)
         _int32(held, "held", self._index)
-        if table.dim() != 2 or held.shape != (table.shape[0],):
+        shape = table.shape
+        if len(shape) != 2 or held.shape != shape[:1]:
             raise ValueError("table must be [rows, width] and held [rows]")
-        written = (table, held, self.refs)
-        for i, t in enumerate(written):
-            for u in (*written[i + 1:], *apart):
-                if u is not None and _meets(t, u):
-                    raise ValueError("table, held, refs and what else is read or written must not share memory")
-        return zx_page_rows(table.data_ptr(), held.data_ptr(), table.shape[0], table.shape[1])
-
-    def _err(self, err: Optional[torch.Tensor]):
-        return None if err is None else _int32(err, "err", self._index).data_ptr()
+        spans = [_words(table), _words(held), self._own, *apart]
+        e = None
+        if err is not None:
+            spans.append(_words(_int32(err, "err", self._index)))
+            e = err.data_ptr()
+        rows = zx_page_rows(spans[0][0], spans[1][0], *shape)
+        _all_apart(spans)
+        return rows, e
 
     def _list(self, copies: Optional[PageCopies], least: int) -> PageCopies:
         if copies is None:
@@ -175,7 +196,8 @@ class PagePool:
         return copies
 
     def _enqueue(self, name: str, *args) -> None:
-        st = getattr(_lib(), name)(*args, _zx._raw_stream(self.device))
+        # (a workspace that is let go here is handed out again on this stream only, behind the call)
+        st = getattr(_bound or _lib(), name)(*args, _zx._raw_stream(self.device))
         if st != 0:
             raise _zx.ZxError(name, st)
 
@@ -187,10 +209,10 @@ class PagePool:
         if _away(self._index, stream):
             return _elsewhere(self.device, stream, (table, held, parents, err, self.refs), lambda s: self.fork(table, held, parents, err, s))
         _int32(parents, "parents", self._index)
-        rows = self._rows(table, held, parents, err)
+        rows, e = self._rows(table, held, err, _words(parents))
         if parents.dim() != 2 or parents.numel() != rows.n_seqs or not 0 < parents.shape[1] <= MOST_SEQS:
             raise ValueError(f"parents must be [groups, beams] for the table's {rows.n_seqs} rows, of up to {MOST_SEQS} beams")
-        self._enqueue("zx_pages_fork", self._ref, C.byref(rows), parents.shape[1], parents.data_ptr(), self._err(err))
+        self._enqueue("zx_pages_fork", self._ref, C.byref(rows), parents.shape[1], parents.data_ptr(), e)
 
     def trim(self, table: torch.Tensor, held: torch.Tensor, keep: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None,
              stream=None) -> None:
@@ -198,10 +220,10 @@ class PagePool:
         them.  A row that has no more than that stays as it is."""
         if _away(self._index, stream):
             return _elsewhere(self.device, stream, (table, held, keep, err, self.refs), lambda s: self.trim(table, held, keep, err, s))
-        rows = self._rows(table, held, keep, err)
-        if keep is not None and _int32(keep, "keep", self._index).shape != (rows.n_seqs,):
-            raise ValueError(f"keep must be [{rows.n_seqs}]")
-        self._enqueue("zx_pages_trim", self._ref, C.byref(rows), None if keep is None else keep.data_ptr(), self._err(err))
+        if keep is not None and _int32(keep, "keep", self._index).shape != held.shape:
+            raise ValueError("keep must be [rows]")
+        rows, e = self._rows(table, held, err, *(() if keep is None else (_words(keep),)))
+        self._enqueue("zx_pages_trim", self._ref, C.byref(rows), None if keep is None else keep.data_ptr(), e)
 
     def extend(self, batch: PagedBatch, held: torch.Tensor, copies: Optional[PageCopies] = None, err: Optional[torch.Tensor] = None,
                stream=None) -> PageCopies:
@@ -223,12 +245,13 @@ class PagePool:
         if batch.n_seqs > MOST_SEQS:
             raise ValueError(f"a batch of up to {MOST_SEQS} sequences")
         copies = self._list(copies, batch.n_seqs)
-        rows = self._rows(batch.page_table, held, batch.q_start, batch.kv_len, copies.pairs, copies.count, err)
-        L = _lib()
-        need = L.zx_pages_extend_workspace_bytes(self._ref, batch.n_seqs)
-        ws = self._bytes.new_empty(need)
-        self._enqueue("zx_pages_extend", self._ref, C.byref(rows), batch.q_start.data_ptr(), batch._c.max_q, batch._c.max_kv,
-                      batch.kv_len.data_ptr(), copies._ref, ws.data_ptr(), need, self._err(err))
+        c = batch._c
+        rows, e = self._rows(batch.page_table, held, err, *copies._spans, _words(batch.q_start), _words(batch.kv_len))
+        need = self._needs.get(c.n_seqs)
+        if need is None:
+            need = self._needs[c.n_seqs] = _lib().zx_pages_extend_workspace_bytes(self._ref, c.n_seqs)
+        self._enqueue("zx_pages_extend", self._ref, C.byref(rows), c.q_start, c.max_q, c.max_kv, c.kv_len, copies._ref,
+                      self._bytes.new_empty(need).data_ptr(), need, e)
         return copies
 
     def compact(self, table: Optional[torch.Tensor] = None, held: Optional[torch.Tensor] = None, copies: Optional[PageCopies] = None,
@@ -247,14 +270,19 @@ class PagePool:
             remap = torch.empty(self.n_pages, dtype=torch.int32, device=self.device)
         elif _int32(remap, "remap", self._index).shape != (self.n_pages,):
             raise ValueError(f"remap must be [{self.n_pages}]")
-        apart = (remap, copies.pairs, copies.count, err)
-        rows = zx_page_rows(None, None, 0, 0) if table is None else self._rows(table, held, *apart)
-        if any(_meets(self.refs, t) for t in apart if t is not None) or _meets(remap, copies.pairs) or _meets(remap, copies.count):
-            raise ValueError("refs, remap and copies must not share memory")
-        L = _lib()
-        need = L.zx_pages_compact_workspace_bytes(self._ref)
-        ws = self._bytes.new_empty(need)
-        self._enqueue("zx_pages_compact", self._ref, C.byref(rows), remap.data_ptr(), copies._ref, ws.data_ptr(), need, self._err(err))
+        spans = (*copies._spans, _words(remap))
+        if table is None:
+            rows, e = zx_page_rows(None, None, 0, 0), None
+            if err is not None:
+                e = _int32(err, "err", self._index).data_ptr()
+                spans += (_words(err),)
+            _all_apart([self._own, *spans])
+        else:
+            rows, e = self._rows(table, held, err, *spans)
+        need = self._needs.get(None)
+        if need is None:
+            need = self._needs[None] = _lib().zx_pages_compact_workspace_bytes(self._ref)
+        self._enqueue("zx_pages_compact", self._ref, C.byref(rows), remap.data_ptr(), copies._ref, self._bytes.new_empty(need).data_ptr(), need, e)
         return copies, remap
 
 
