@@ -185,7 +185,7 @@ extern "C" zx_status zx_paged_copy(const zx_paged_cache *caches, uint32_t n_cach
         g.kv_items = ceil_div((uint64_t)o.heads << (o.log_page + g.log_row), share);
         g.bound_items = f.block_tokens ? ceil_div((uint64_t)o.heads << (o.log_page - o.log_block + g.log_bound), share) : 0;
         const uint64_t items = (uint64_t)copies->cap * n * (2ull * g.kv_items + g.bound_items);
-        hipLaunchKernelGGL(k_paged_copy, dim3((uint32_t)(items < 2048 ? items : 2048)), dim3(kThreads), 0, stream, g);
+        hipLaunchKernelGGL(k_paged_copy, dim3((uint32_t)(items < 8192 ? items : 8192)), dim3(kThreads), 0, stream, g);
     }
     return hipGetLastError() == hipSuccess ? ZX_OK : ZX_E_HIP;
 }

@@ -18,9 +18,9 @@ using zxp::div_up;
 
 constexpr uint32_t kMostPages = 1u << 23;
 constexpr uint32_t kMostSeqs = 2048;             // of one call that gives out pages, and beams of a group
-constexpr uint32_t kSegment = 4096;              // pages whose free ones a workgroup counts
-constexpr uint32_t kThreads = 256;
-constexpr uint32_t kEach = kSegment / kThreads;
+constexpr uint32_t kThreads = 1024;
+constexpr uint32_t kEach = 4;                    // pages of a thread
+constexpr uint32_t kSegment = kThreads * kEach;  // pages whose free ones a workgroup counts
 
 struct Pool {
     int32_t *refs;
@@ -36,21 +36,41 @@ struct Rows {
 
 __device__ __forceinline__ uint32_t pages_of(const Pool &p, int32_t tokens) { return ((uint32_t)tokens + (1u << p.log_page) - 1u) >> p.log_page; }
 
-// Sum over the workgroup, and the sum over the threads ahead of this one.
-template <int NT>
-__device__ __forceinline__ uint32_t block_scan(uint32_t v, uint32_t *sums, uint32_t &total)
+// Sums over the workgroup of two numbers, and over the threads ahead of this one.  `sums` is free again at the next barrier.
+struct Two {
+    uint32_t a, b;
+};
+__device__ __forceinline__ Two block_scan(Two v, Two (&sums)[kThreads / 64], Two &total)
 {
-    uint32_t wave_total;
-    uint32_t ex = zxk::wave_excl_scan(v, wave_total);
+    Two w;
+    Two ex{zxk::wave_excl_scan(v.a, w.a), zxk::wave_excl_scan(v.b, w.b)};
     __syncthreads();
-    if ((threadIdx.x & 63u) == 63u) sums[threadIdx.x >> 6] = wave_total;
+    if ((threadIdx.x & 63u) == 63u) sums[threadIdx.x >> 6] = w;
     __syncthreads();
-    total = 0;
-    for (int i = 0; i < NT / 64; ++i) {
-        if (i < (int)(threadIdx.x >> 6)) ex += sums[i];
-        total += sums[i];
+    total = Two{0, 0};
+#pragma unroll
+    for (uint32_t i = 0; i < kThreads / 64; ++i) {
+        const Two s = sums[i];
+        if (i < threadIdx.x >> 6) {
+            ex.a += s.a;
+            ex.b += s.b;
+        }
+        total.a += s.a;
+        total.b += s.b;
     }
     return ex;
+}
+
+// Bit i: page `first` + i is free, of a thread's kEach.
+__device__ __forceinline__ uint32_t free_bits(const Pool &p, uint32_t first)
+{
+    int32_t r[kEach];
+#pragma unroll
+    for (uint32_t i = 0; i < kEach; ++i) r[i] = first + i < p.n_pages ? p.refs[first + i] : 1;
+    uint32_t m = 0;
+#pragma unroll
+    for (uint32_t i = 0; i < kEach; ++i) m |= (uint32_t)(r[i] <= 0) << i;
+    return m;
 }
 
 // ---------------------------------------------------------------- rows go on from other rows
@@ -90,18 +110,31 @@ __global__ __launch_bounds__(1024) void k_pages_fork(ForkArgs g)
     __shared__ uint32_t bad, cols;
     int32_t *held = lds, *parent = held + g.beams, *children = parent + g.beams, *strip = children + g.beams;
     const uint32_t group = blockIdx.y, tid = threadIdx.x, ls = g.log_strip, ns = 1u << ls;
+    int32_t *table = g.r.table + (uint64_t)group * g.beams * g.r.width;
+    int32_t x[4];                                // four entries of a thread under way at once, the first beside the lengths
+    auto read = [&](uint32_t c0, uint32_t i0, auto in) {
+#pragma unroll
+        for (uint32_t u = 0; u < 4; ++u) {
+            const uint32_t i = i0 + u * blockDim.x, r = i >> ls, c = c0 + (i & (ns - 1));
+            x[u] = 0;
+            if (r < g.beams && in(r, c)) x[u] = table[(uint64_t)r * g.r.width + c];
+        }
+    };
+    const uint32_t first = blockIdx.x * ns;
+    read(first, tid, [&](uint32_t, uint32_t c) { return c < g.r.width; });
     if (!load_group(g, group, held, parent, &bad, &cols)) return;
     for (uint32_t i = tid; i < g.beams; i += blockDim.x) children[i] = 0;
     __syncthreads();
     for (uint32_t i = tid; i < g.beams; i += blockDim.x)
         if (parent[i] >= 0) atomicAdd(&children[parent[i]], 1);
-    int32_t *table = g.r.table + (uint64_t)group * g.beams * g.r.width;
-    for (uint32_t c0 = blockIdx.x * ns; c0 < cols; c0 += gridDim.x * ns) {
+    for (uint32_t c0 = first; c0 < cols; c0 += gridDim.x * ns) {
         const uint32_t nc = cols - c0 < ns ? cols - c0 : ns;
         __syncthreads();
-        for (uint32_t i = tid; i < g.beams << ls; i += blockDim.x) {
-            const uint32_t r = i >> ls, c = i & (ns - 1);
-            if (c < nc && c0 + c < pages_of(g.p, held[r])) strip[i] = table[(uint64_t)r * g.r.width + c0 + c];
+        for (uint32_t i0 = tid; i0 < g.beams << ls; i0 += 4 * blockDim.x) {
+            if (c0 != first || i0 != tid) read(c0, i0, [&](uint32_t r, uint32_t c) { return c < pages_of(g.p, held[r]); });
+#pragma unroll
+            for (uint32_t u = 0; u < 4; ++u)
+                if (i0 + u * blockDim.x < g.beams << ls) strip[i0 + u * blockDim.x] = x[u];
         }
         __syncthreads();
         for (uint32_t i = tid; i < g.beams << ls; i += blockDim.x) {
@@ -141,7 +174,7 @@ __global__ __launch_bounds__(1024) void k_pages_fork(ForkArgs g)
 }
 
 // The lengths, where several workgroups of a group had to read them.
-__global__ __launch_bounds__(kThreads) void k_pages_fork_held(ForkArgs g)
+__global__ __launch_bounds__(256) void k_pages_fork_held(ForkArgs g)
 {
     extern __shared__ int32_t lds[];
     __shared__ uint32_t bad, cols;
@@ -153,7 +186,7 @@ __global__ __launch_bounds__(kThreads) void k_pages_fork_held(ForkArgs g)
 
 // ---------------------------------------------------------------- rows give pages back
 
-__global__ __launch_bounds__(kThreads) void k_pages_trim(Pool p, Rows r, const int32_t *keep)
+__global__ __launch_bounds__(1024) void k_pages_trim(Pool p, Rows r, const int32_t *keep)
 {
     const uint32_t s = blockIdx.x;
     const int32_t held = r.held[s], want = keep ? keep[s] : 0;
@@ -164,7 +197,7 @@ __global__ __launch_bounds__(kThreads) void k_pages_trim(Pool p, Rows r, const i
     if (want >= held) return;
     const uint32_t first = pages_of(p, want), end = pages_of(p, held);
     const int32_t *row = r.table + (uint64_t)s * r.width;
-    for (uint32_t c = first + threadIdx.x; c < end; c += kThreads) {
+    for (uint32_t c = first + threadIdx.x; c < end; c += blockDim.x) {
         const uint32_t page = (uint32_t)row[c];
         if (page >= p.n_pages) report(p.err, ZX_E_CORRUPT);
         else if (atomicAdd(&p.refs[page], -1) <= 0) report(p.err, ZX_E_CORRUPT);
@@ -183,7 +216,7 @@ struct Need {
     int32_t held, kv;                            // lengths after the call
     uint32_t old, left;                          // bit 31 of old: this sequence sets that page's count to `left`
 };
-constexpr uint32_t kFlag = 1u << 31;
+constexpr uint32_t kFlag = 1u << 31, kPairBits = 12;
 
 struct ExtendArgs {
     Pool p;
@@ -197,152 +230,136 @@ struct ExtendArgs {
     uint32_t n_segments, log_slots;
 };
 
-__device__ __forceinline__ uint32_t free_in_segment(const Pool &p, uint32_t seg, uint32_t *sums)
-{
-    uint32_t n = 0;
-    const uint32_t p0 = seg * kSegment + threadIdx.x;
-#pragma unroll
-    for (uint32_t i = 0; i < kEach; ++i) {
-        const uint32_t page = p0 + i * kThreads;
-        n += page < p.n_pages && p.refs[page] <= 0;
-    }
-    uint32_t total;
-    (void)block_scan<(int)kThreads>(n, sums, total);
-    return total;
-}
-
-// Free pages counted by segments; and, by workgroup 0, what every sequence needs.  A sequence that goes on in a page which
-// others hold too may not write there: it gets a page of its own and a copy of what it has, unless all that hold the page go on
+// What every sequence needs, by one workgroup.  A sequence that goes on in a page which others hold too
+// may not write there: it gets a page of its own and a copy of what it has, unless all that hold the page go on
 // in this call, when the first of them keeps it.  How many go on in a page, and who is first, is counted in a
 // hash table in LDS; neither depends on the order of entry.
-__global__ __launch_bounds__(kThreads) void k_pages_need(ExtendArgs g)
+__device__ __forceinline__ void find_needs(const ExtendArgs &g, uint32_t *slots, Two (&sums)[kThreads / 64])
 {
-    extern __shared__ uint32_t slots[];          // [slot][3]: page + 1, sequences that write it, the first of them
-    __shared__ uint32_t sums[kThreads / 64];
-    __shared__ unsigned long long wanted;
+    // slots: [slot][3]: page + 1, sequences that write it, the first of them
     const uint32_t tid = threadIdx.x;
-    if (blockIdx.x > 0) {
-        const uint32_t seg = blockIdx.x - 1, n = free_in_segment(g.p, seg, sums);
-        if (tid == 0) g.counted[seg] = n;
-        return;
+    Two total;
+    constexpr uint32_t kSeqs = kMostSeqs / kThreads;         // sequences of a thread, side by side
+    const uint32_t T = 1u << g.p.log_page, per = div_up(g.r.n, kThreads), s0 = tid * per;
+    struct Seq {
+        int32_t nq, held;
+        uint32_t page, refs;                     // refs > 0 where it goes on in a page that has tokens
+        bool ok;
+    } v[kSeqs];
+#pragma unroll
+    for (uint32_t i = 0; i < kSeqs; ++i) {
+        const uint32_t s = s0 + i;
+        v[i] = Seq{0, 0, 0, 0, false};
+        if (i >= per || s >= g.r.n) continue;
+        const int32_t q0 = g.q_start[s], q1 = g.q_start[s + 1], held = g.r.held[s];
+        v[i].held = held;
+        // (differences in 64 bits: lengths that are nonsense must not wrap into sense)
+        const int64_t nq = (int64_t)q1 - q0, all = nq + held;
+        if (q0 < 0 || nq < 0 || nq > (int64_t)g.max_q || held < 0 || all > (int64_t)g.r.cap) continue;
+        v[i].nq = (int32_t)nq;
+        v[i].ok = true;
+        if (nq > 0 && (uint32_t)held & (T - 1)) {
+            v[i].page = (uint32_t)g.r.table[(uint64_t)s * g.r.width + ((uint32_t)held >> g.p.log_page)];
+            const int32_t refs = v[i].page < g.p.n_pages ? g.p.refs[v[i].page] : 0;
+            if (refs <= 0) v[i].ok = false;      // no page, or one that nobody is said to hold
+            else v[i].refs = (uint32_t)refs;
+        }
     }
     const uint32_t n_slots = 1u << g.log_slots, mask = n_slots - 1;
     for (uint32_t i = tid; i < n_slots; i += kThreads) {
         slots[3 * i] = slots[3 * i + 1] = 0;
         slots[3 * i + 2] = 0xFFFFFFFFu;
     }
-    if (tid == 0) wanted = 0;
     __syncthreads();
-    auto slot_of = [&](uint32_t page) { return (page * 0x9E3779B1u) >> (32 - g.log_slots); };
-    const uint32_t T = 1u << g.p.log_page;
-    struct Seq {
-        int32_t nq, held;
-        uint32_t page, refs;                     // refs > 0 where it goes on in a page that has tokens
-        bool ok;
-    };
-    auto load = [&](uint32_t s) {
-        Seq v{0, 0, 0, 0, false};
-        const int32_t q0 = g.q_start[s], q1 = g.q_start[s + 1], held = g.r.held[s];
-        // (differences in 64 bits: lengths that are nonsense must not wrap into sense)
-        const int64_t nq = (int64_t)q1 - q0, all = nq + held;
-        if (q0 < 0 || nq < 0 || nq > (int64_t)g.max_q || held < 0 || all > (int64_t)g.r.cap) return v;
-        v.nq = (int32_t)nq;
-        v.held = held;
-        v.ok = true;
-        if (nq > 0 && held % (int32_t)T) {
-            v.page = (uint32_t)g.r.table[(uint64_t)s * g.r.width + ((uint32_t)held >> g.p.log_page)];
-            const int32_t refs = v.page < g.p.n_pages ? g.p.refs[v.page] : 0;
-            if (refs <= 0) v.ok = false;         // no page, or one that nobody is said to hold
-            else v.refs = (uint32_t)refs;
-        }
-        return v;
-    };
-    for (uint32_t s = tid; s < g.r.n; s += kThreads) {
-        const Seq v = load(s);
-        if (!v.ok) report(g.p.err, ZX_E_CORRUPT);
-        if (!v.ok || v.refs == 0) continue;
-        uint32_t i = slot_of(v.page);
+    uint32_t slot[kSeqs];
+#pragma unroll
+    for (uint32_t i = 0; i < kSeqs; ++i) {
+        slot[i] = 0;
+        if (i >= per || s0 + i >= g.r.n) continue;
+        if (!v[i].ok) report(g.p.err, ZX_E_CORRUPT);
+        if (!v[i].ok || v[i].refs == 0) continue;
+        uint32_t j = (v[i].page * 0x9E3779B1u) >> (32 - g.log_slots);
         for (;;) {                               // (twice as many slots as sequences: one is free)
-            const uint32_t was = atomicCAS(&slots[3 * i], 0u, v.page + 1);
-            if (was == 0 || was == v.page + 1) break;
-            i = (i + 1) & mask;
+            const uint32_t was = atomicCAS(&slots[3 * j], 0u, v[i].page + 1);
+            if (was == 0 || was == v[i].page + 1) break;
+            j = (j + 1) & mask;
         }
-        atomicAdd(&slots[3 * i + 1], 1u);
-        atomicMin(&slots[3 * i + 2], s);
+        atomicAdd(&slots[3 * j + 1], 1u);
+        atomicMin(&slots[3 * j + 2], s0 + i);
+        slot[i] = j;
     }
     __syncthreads();
-    uint32_t taken = 0, copied = 0;              // by the sequences ahead
-    for (uint32_t s0 = 0; s0 < g.r.n; s0 += kThreads) {
-        const uint32_t s = s0 + tid;
-        Seq v{0, 0, 0, 0, false};
-        if (s < g.r.n) v = load(s);
-        uint32_t slot = 0;
-        if (v.ok && v.refs > 0) {
-            slot = slot_of(v.page);
-            while (slots[3 * slot] != v.page + 1 && slots[3 * slot] != 0) slot = (slot + 1) & mask;
-            if (slots[3 * slot] == 0) v.ok = false;          // (only if the table is written meanwhile)
+    Need d[kSeqs];
+    uint32_t n[kSeqs];
+    Two mine{0, 0};
+#pragma unroll
+    for (uint32_t i = 0; i < kSeqs; ++i) {
+        d[i] = Need{};
+        n[i] = 0;
+        if (!v[i].ok) {
+            d[i].held = v[i].held;               // left out: it stays as it is
+            continue;
         }
-        Need d{};
-        uint32_t n = 0;
-        bool copy = false;
-        if (v.ok) {
-            d.held = d.kv = v.held + v.nq;
-            d.first = pages_of(g.p, v.held);
-            if (v.refs > 0) {
-                const uint32_t writers = slots[3 * slot + 1];
-                const bool leads = slots[3 * slot + 2] == s;
-                copy = !(leads && writers >= v.refs);
-                d.old = v.page;
-                if (leads) {
-                    d.old |= kFlag;
-                    d.left = writers >= v.refs ? 1 : v.refs - writers;
-                }
-                d.tokens = (uint32_t)v.held & (T - 1);
-                if (copy) --d.first;
+        d[i].held = d[i].kv = v[i].held + v[i].nq;
+        d[i].first = pages_of(g.p, v[i].held);
+        if (v[i].refs > 0) {
+            const uint32_t writers = slots[3 * slot[i] + 1];
+            const bool leads = slots[3 * slot[i] + 2] == s0 + i;
+            d[i].old = v[i].page;
+            if (leads) {
+                d[i].old |= kFlag;
+                d[i].left = writers >= v[i].refs ? 1 : v[i].refs - writers;
             }
-            n = v.nq > 0 ? pages_of(g.p, d.held) - d.first : 0;
-        } else if (s < g.r.n) {
-            d.held = g.r.held[s];                // left out: it stays as it is
+            d[i].tokens = (uint32_t)v[i].held & (T - 1);
+            if (!(leads && writers >= v[i].refs)) {
+                d[i].pair = kFlag;
+                --d[i].first;
+            }
         }
-        // sums are only used where all is no more than the pool: a sequence's part is cut to what makes it more
-        const uint32_t most = kMostPages + 1;
-        uint32_t total, pairs;
-        const uint32_t ahead = block_scan<(int)kThreads>(n < most ? n : most, sums, total);
-        const uint32_t nth = block_scan<(int)kThreads>(copy ? 1u : 0u, sums, pairs);
-        d.before = taken + ahead;
-        d.pair = copy ? kFlag | (copied + nth) : 0;
-        if (s < g.r.n) g.need[s] = d;
-        if (tid == 0) wanted += total;           // (256 * (2^23 + 1) fits 32 bits; the sum of eight such may not)
-        taken += total;
-        copied += pairs;
+        n[i] = v[i].nq > 0 ? pages_of(g.p, d[i].held) - d[i].first : 0;
+        if (n[i] > g.p.n_pages) n[i] = g.p.n_pages + 1;
+        mine.a += n[i];
+        mine.b += (d[i].pair ? 1u : 0u) + (n[i] >> 15 << kPairBits);
+    }
+    // 2048 times 2^23 pages would not fit 32 bits.  Beside the pairs go the parts' sums in units of 2^15 pages, which do (2^19 above
+    // 12 bits), and where these are no more than the pool, the whole sum is below 2^23 + 2048 * 2^15
+    const Two ahead = block_scan(mine, sums, total);
+    uint32_t before = ahead.a, pair = ahead.b & ((1u << kPairBits) - 1u);
+#pragma unroll
+    for (uint32_t i = 0; i < kSeqs; ++i) {
+        if (i >= per || s0 + i >= g.r.n) continue;
+        d[i].before = before;
+        if (d[i].pair) d[i].pair = kFlag | pair++;
+        before += n[i];
+        g.need[s0 + i] = d[i];
     }
     if (tid == 0) {
-        g.total[0] = wanted;
-        g.total[1] = copied;
+        g.total[0] = (uint64_t)(total.b >> kPairBits) << 15 > g.p.n_pages ? 0xFFFFFFFFu : total.a;
+        g.total[1] = total.b & ((1u << kPairBits) - 1u);
     }
 }
 
-// Each workgroup gives out the free pages of its segment: the r-th free page of the pool to the sequence whose part holds r.
-__global__ __launch_bounds__(kThreads) void k_pages_give(ExtendArgs g)
+// A workgroup gives out the free pages of its segment: the r-th free page of the pool to the sequence whose part holds r.
+__device__ __forceinline__ void give_pages(const ExtendArgs &g, uint32_t seg, uint32_t is_free, uint32_t *before, Two (&sums)[kThreads / 64])
 {
-    __shared__ uint32_t sums[kThreads / 64];
-    __shared__ uint32_t before[kMostSeqs];
-    const uint32_t tid = threadIdx.x, seg = blockIdx.x;
-    const uint64_t wanted = g.total[0];
-    uint32_t ahead = 0, all = 0, mine = 0;
-    for (uint32_t i = tid; i < g.n_segments; i += kThreads) {
-        const uint32_t n = g.counted[i];
-        all += n;
-        if (i < seg) mine += n;
-    }
-    uint32_t unused, total;
-    unused = block_scan<(int)kThreads>(all, sums, total);
-    unused = block_scan<(int)kThreads>(mine, sums, ahead);
-    (void)unused;
-    const bool enough = wanted <= total;
+    const uint32_t tid = threadIdx.x, p0 = seg * kSegment + tid * kEach;
+    const uint32_t wanted = (uint32_t)g.total[0], pairs = (uint32_t)g.total[1];
+    Two n{0, 0}, total;
+    if (g.n_segments == 1)
+        n.a = (uint32_t)__builtin_popcount(is_free);
+    else
+        for (uint32_t i = tid; i < g.n_segments; i += kThreads) {
+            const uint32_t c = g.counted[i];
+            n.a += c;
+            if (i < seg) n.b += c;
+        }
+    for (uint32_t s = tid; s < g.r.n; s += kThreads) before[s] = g.need[s].before;
+    (void)block_scan(n, sums, total);
+    const bool enough = wanted <= total.a;
+    const uint32_t ahead = total.b;
     if (seg == 0) {
         if (!enough && tid == 0) report(g.p.err, ZX_E_NOSPACE);
-        if (tid == 0) *g.count = enough ? (int32_t)g.total[1] : 0;
+        if (tid == 0) *g.count = enough ? (int32_t)pairs : 0;
         for (uint32_t s = tid; s < g.r.n; s += kThreads) {
             const Need d = g.need[s];
             g.kv_len[s] = enough ? d.kv : 0;
@@ -352,34 +369,63 @@ __global__ __launch_bounds__(kThreads) void k_pages_give(ExtendArgs g)
             if (d.old & kFlag) g.p.refs[d.old & ~kFlag] = (int32_t)d.left;
         }
     }
-    if (!enough || wanted <= ahead || g.counted[seg] == 0) return;
-    for (uint32_t s = tid; s < g.r.n; s += kThreads) before[s] = g.need[s].before;
-    // a thread's kEach pages lie side by side, so ranks ascend with the page
-    const uint32_t p0 = seg * kSegment + tid * kEach;
-    uint32_t is_free = 0;
-#pragma unroll
-    for (uint32_t i = 0; i < kEach; ++i)
-        if (p0 + i < g.p.n_pages && g.p.refs[p0 + i] <= 0) is_free |= 1u << i;
-    uint32_t r = ahead + block_scan<(int)kThreads>((uint32_t)__builtin_popcount(is_free), sums, total);
+    if (!enough || wanted <= ahead) return;
+    uint32_t r = ahead + block_scan(Two{(uint32_t)__builtin_popcount(is_free), 0}, sums, total).a;
+    if (!is_free || r >= wanted) return;
+    uint32_t lo = 0, hi = g.r.n;                 // the last sequence with before <= r
+    while (hi - lo > 1) {
+        const uint32_t m = (lo + hi) / 2;
+        if (before[m] <= r) lo = m;
+        else hi = m;
+    }
+    Need d = g.need[lo];
     for (; is_free && r < wanted; is_free &= is_free - 1, ++r) {
-        const uint32_t page = p0 + (uint32_t)__builtin_ctz(is_free);
-        uint32_t lo = 0, hi = g.r.n;             // the last sequence with before <= r
-        while (hi - lo > 1) {
-            const uint32_t m = (lo + hi) / 2;
-            if (before[m] <= r) lo = m;
-            else hi = m;
+        if (lo + 1 < g.r.n && before[lo + 1] <= r) {         // on to the next one that takes any
+            while (lo + 1 < g.r.n && before[lo + 1] <= r) ++lo;
+            d = g.need[lo];
         }
-        const Need d = g.need[lo];
-        const uint32_t at = d.first + (r - d.before);
-        g.r.table[(uint64_t)lo * g.r.width + at] = (int32_t)page;
-        g.p.refs[page] = 1;
+        const uint32_t page = p0 + (uint32_t)__builtin_ctz(is_free), at = d.first + (r - d.before);
+        int32_t *entry = g.r.table + (uint64_t)lo * g.r.width + at;
         if ((d.pair & kFlag) && at == d.first) {
             int32_t *pr = g.pairs + 3 * (uint64_t)(d.pair & ~kFlag);
             pr[0] = (int32_t)(d.old & ~kFlag);
             pr[1] = (int32_t)page;
             pr[2] = (int32_t)d.tokens;
         }
+        *entry = (int32_t)page;
+        g.p.refs[page] = 1;
     }
+}
+
+__global__ __launch_bounds__(kThreads) void k_pages_need(ExtendArgs g)
+{
+    extern __shared__ uint32_t slots[];
+    __shared__ Two sums[kThreads / 64];
+    if (blockIdx.x == 0) return find_needs(g, slots, sums);
+    const uint32_t seg = blockIdx.x - 1;
+    Two total;
+    (void)block_scan(Two{(uint32_t)__builtin_popcount(free_bits(g.p, seg * kSegment + threadIdx.x * kEach)), 0}, sums, total);
+    if (threadIdx.x == 0) g.counted[seg] = total.a;
+}
+
+__global__ __launch_bounds__(kThreads) void k_pages_give(ExtendArgs g)
+{
+    __shared__ Two sums[kThreads / 64];
+    __shared__ uint32_t before[kMostSeqs];
+    // a thread's pages lie side by side, so ranks ascend with the page
+    give_pages(g, blockIdx.x, free_bits(g.p, blockIdx.x * kSegment + threadIdx.x * kEach), before, sums);
+}
+
+// The whole of it by one workgroup, for pools of one segment: 1 x 4 rows 3.0 + 3.4 us in two launches.
+__global__ __launch_bounds__(kThreads) void k_pages_extend(ExtendArgs g)
+{
+    extern __shared__ uint32_t slots[];
+    __shared__ Two sums[kThreads / 64];
+    __shared__ uint32_t before[kMostSeqs];
+    const uint32_t is_free = free_bits(g.p, threadIdx.x * kEach);
+    find_needs(g, slots, sums);
+    __syncthreads();                             // (what it wrote to memory is read by this workgroup alone)
+    give_pages(g, 0, is_free, before, sums);
 }
 
 // ---------------------------------------------------------------- pages in use are brought together
@@ -394,40 +440,44 @@ struct CompactArgs {
 
 __global__ __launch_bounds__(kThreads) void k_pages_count(CompactArgs g)
 {
-    __shared__ uint32_t sums[kThreads / 64];
-    const uint32_t n = free_in_segment(g.p, blockIdx.x, sums);
-    if (threadIdx.x == 0) g.counted[blockIdx.x] = n;
+    __shared__ Two sums[kThreads / 64];
+    Two total;
+    (void)block_scan(Two{(uint32_t)__builtin_popcount(free_bits(g.p, blockIdx.x * kSegment + threadIdx.x * kEach)), 0}, sums, total);
+    if (threadIdx.x == 0) g.counted[blockIdx.x] = total.a;
 }
 
 // With L pages in use, those of them at L or behind go into the free ones ahead of L, in order: the j-th such page into the
 // j-th hole.  There are as many of the one as of the other.
-__global__ __launch_bounds__(kThreads) void k_pages_pair(CompactArgs g)
+__device__ __forceinline__ void pair_pages(const CompactArgs &g, uint32_t seg, Two (&sums)[kThreads / 64])
 {
-    __shared__ uint32_t sums[kThreads / 64];
-    const uint32_t tid = threadIdx.x, seg = blockIdx.x;
-    uint32_t all = 0, ahead = 0, total, mine = 0;
-    for (uint32_t i = tid; i < g.n_segments; i += kThreads) {
-        const uint32_t n = g.counted[i];
-        all += n;
-        if (i < seg) mine += n;
-    }
-    (void)block_scan<(int)kThreads>(all, sums, total);
-    (void)block_scan<(int)kThreads>(mine, sums, ahead);
-    const uint32_t L = g.p.n_pages - total;      // pages in use
-    // holes: free pages ahead of L
+    const uint32_t tid = threadIdx.x;
+    const uint32_t p0 = seg * kSegment + tid * kEach, is_free = free_bits(g.p, p0);
+    Two n{0, 0}, total;
+    if (g.n_segments == 1)
+        n.a = (uint32_t)__builtin_popcount(is_free);
+    else
+        for (uint32_t i = tid; i < g.n_segments; i += kThreads) {
+            const uint32_t c = g.counted[i];
+            n.a += c;
+            if (i < seg) n.b += c;
+        }
+    (void)block_scan(n, sums, total);
+    const uint32_t ahead = total.b, L = g.p.n_pages - total.a;       // free pages of the segments ahead; pages in use
+    // holes: free pages ahead of L, of whole segments and of the one that L lies in
     const uint32_t ls = L / kSegment;
-    uint32_t n = 0, holes;
-    for (uint32_t i = tid; i < ls && i < g.n_segments; i += kThreads) n += g.counted[i];
-    for (uint32_t i = ls * kSegment + tid; i < L; i += kThreads) n += g.p.refs[i] <= 0;
-    (void)block_scan<(int)kThreads>(n, sums, holes);
+    uint32_t holes = 0;
+    if (g.n_segments > 1)
+        for (uint32_t i = tid; i < ls; i += kThreads) holes += g.counted[i];
+    const uint32_t pl = ls * kSegment + tid * kEach;
+    if (pl < L) {
+        const uint32_t m = L - pl < kEach ? (1u << (L - pl)) - 1u : (1u << kEach) - 1u;
+        holes += (uint32_t)__builtin_popcount((ls == seg ? is_free : free_bits(g.p, pl)) & m);
+    }
+    uint32_t f = block_scan(Two{(uint32_t)__builtin_popcount(is_free), holes}, sums, total).a + ahead;        // free pages ahead
+    holes = total.b;
     if (seg == 0 && tid == 0) *g.count = (int32_t)holes;
     const uint32_t most = g.p.n_pages / 2;       // (never more, unless refs is written meanwhile)
-    const uint32_t p0 = seg * kSegment + tid * kEach;
-    uint32_t is_free = 0;
 #pragma unroll
-    for (uint32_t i = 0; i < kEach; ++i)
-        if (p0 + i < g.p.n_pages && g.p.refs[p0 + i] <= 0) is_free |= 1u << i;
-    uint32_t f = ahead + block_scan<(int)kThreads>((uint32_t)__builtin_popcount(is_free), sums, total);    // free pages ahead
     for (uint32_t i = 0; i < kEach; ++i) {
         const uint32_t page = p0 + i;
         if (page >= g.p.n_pages) break;
@@ -447,29 +497,29 @@ __global__ __launch_bounds__(kThreads) void k_pages_pair(CompactArgs g)
     }
 }
 
-// The pairs' counts and new places; and the tables, whose entries find their new place through nth and the pairs.
-__global__ __launch_bounds__(kThreads) void k_pages_move(CompactArgs g, uint32_t for_pairs, uint32_t per_row)
+// The pairs' counts and new places, shared by `of` workgroups.
+__device__ __forceinline__ void move_counts(const CompactArgs &g, uint32_t nth, uint32_t of)
 {
-    if (blockIdx.x < for_pairs) {
-        const uint32_t said = (uint32_t)*g.count, n = said < g.p.n_pages / 2 ? said : g.p.n_pages / 2;
-        for (uint32_t j = blockIdx.x * kThreads + threadIdx.x; j < n; j += for_pairs * kThreads) {
-            const uint32_t from = (uint32_t)g.pairs[3 * (uint64_t)j], to = (uint32_t)g.pairs[3 * (uint64_t)j + 1];
-            if (from >= g.p.n_pages || to >= g.p.n_pages) continue;
-            g.remap[from] = (int32_t)to;
-            g.p.refs[to] = g.p.refs[from];
-            g.p.refs[from] = 0;
-        }
-        return;
+    const uint32_t said = (uint32_t)*g.count, n = said < g.p.n_pages / 2 ? said : g.p.n_pages / 2;
+    for (uint32_t j = nth * blockDim.x + threadIdx.x; j < n; j += of * blockDim.x) {
+        const uint32_t from = (uint32_t)g.pairs[3 * (uint64_t)j], to = (uint32_t)g.pairs[3 * (uint64_t)j + 1];
+        if (from >= g.p.n_pages || to >= g.p.n_pages) continue;
+        g.remap[from] = (int32_t)to;
+        g.p.refs[to] = g.p.refs[from];
+        g.p.refs[from] = 0;
     }
-    const uint32_t item = blockIdx.x - for_pairs, s = item / per_row;
+}
+// Entries c, c + step ... of a row of the table find their new place through nth and the pairs.
+__device__ __forceinline__ void move_row(const CompactArgs &g, uint32_t s, uint32_t c, uint32_t step)
+{
     const int32_t held = g.r.held[s];
     if (held < 0 || held > g.r.cap) {
-        if (threadIdx.x == 0) report(g.p.err, ZX_E_CORRUPT);
+        if (c == 0) report(g.p.err, ZX_E_CORRUPT);
         return;
     }
     const uint32_t n = pages_of(g.p, held);
     int32_t *row = g.r.table + (uint64_t)s * g.r.width;
-    for (uint32_t c = (item % per_row) * kThreads + threadIdx.x; c < n; c += per_row * kThreads) {
+    for (; c < n; c += step) {
         const uint32_t page = (uint32_t)row[c];
         if (page >= g.p.n_pages) {
             report(g.p.err, ZX_E_CORRUPT);
@@ -479,6 +529,30 @@ __global__ __launch_bounds__(kThreads) void k_pages_move(CompactArgs g, uint32_t
         if (j >= 0) row[c] = g.pairs[3 * (uint64_t)j + 1];
         else if (g.remap[page] < 0) report(g.p.err, ZX_E_CORRUPT);       // a page that nobody is said to hold
     }
+}
+
+__global__ __launch_bounds__(kThreads) void k_pages_pair(CompactArgs g)
+{
+    __shared__ Two sums[kThreads / 64];
+    pair_pages(g, blockIdx.x, sums);
+}
+
+constexpr uint32_t kMoveThreads = 256;
+__global__ __launch_bounds__(kMoveThreads) void k_pages_move(CompactArgs g, uint32_t for_pairs, uint32_t per_row)
+{
+    if (blockIdx.x < for_pairs) return move_counts(g, blockIdx.x, for_pairs);
+    const uint32_t item = blockIdx.x - for_pairs;
+    move_row(g, item / per_row, (item % per_row) * kMoveThreads + threadIdx.x, per_row * kMoveThreads);
+}
+
+// The whole of it by one workgroup, for pools of one segment and tables of up to 16384 entries; a wave takes a row at a time.
+__global__ __launch_bounds__(kThreads) void k_pages_compact(CompactArgs g)
+{
+    __shared__ Two sums[kThreads / 64];
+    pair_pages(g, 0, sums);
+    __syncthreads();                             // (what it wrote to memory is read by this workgroup alone)
+    move_counts(g, 0, 1);
+    for (uint32_t s = threadIdx.x / 64; s < g.r.n; s += kThreads / 64) move_row(g, s, threadIdx.x & 63u, 64);
 }
 
 // ---- host side
@@ -522,17 +596,18 @@ extern "C" zx_status zx_pages_fork(const zx_page_pool *pool, const zx_page_rows 
     g.parents = parents;
     g.beams = beams;
     const uint32_t groups = rows->n_seqs / beams;
-    // 32 KB of table entries at a time, four columns at least
+    // 16 KB of table entries at a time, four columns at least
+    const uint32_t width = rows->table_width;
     g.log_strip = 10;
-    while (g.log_strip > 2 && ((uint64_t)beams << g.log_strip) > 8192) --g.log_strip;
-    const uint32_t n_strips = ceil_div(rows->table_width, 1u << g.log_strip);
-    // several workgroups a group, and a launch more for the lengths, where there are few groups and many strips
-    uint32_t wgs = 1;
-    while (wgs * 4 <= n_strips && wgs * groups < 256) wgs *= 2;
+    while (g.log_strip > 2 && (((uint64_t)beams << g.log_strip) > 4096 || 1u << (g.log_strip - 1) >= width)) --g.log_strip;
+    // a group with more than two strips is shared by workgroups, about 2048 in all; the lengths are then written by a launch of
+    // their own, behind those that read them
+    const uint32_t n_strips = ceil_div(width, 1u << g.log_strip), fair = 1 + 2047 / groups;
+    const uint32_t wgs = n_strips <= 2 ? 1 : n_strips < fair ? n_strips : fair;
     g.write_held = wgs == 1;
-    const uint32_t lds = (3 * beams + (beams << g.log_strip)) * 4;
-    hipLaunchKernelGGL(k_pages_fork, dim3(wgs, groups), dim3(1024), lds, stream, g);
-    if (wgs > 1) hipLaunchKernelGGL(k_pages_fork_held, dim3(groups), dim3(kThreads), 2 * beams * 4, stream, g);
+    const uint32_t lds = (3 * beams + (beams << g.log_strip)) * 4, threads = beams << g.log_strip <= 1024 ? 256 : 1024;
+    hipLaunchKernelGGL(k_pages_fork, dim3(wgs, groups), dim3(threads), lds, stream, g);
+    if (wgs > 1) hipLaunchKernelGGL(k_pages_fork_held, dim3(groups), dim3(256), 2 * beams * 4, stream, g);
     return launched();
 }
 
@@ -544,7 +619,7 @@ extern "C" zx_status zx_pages_trim(const zx_page_pool *pool, const zx_page_rows 
     zx_status st = make_pool(pool, err, p);
     if (st == ZX_OK) st = make_rows(rows, pool, r);
     if (st != ZX_OK || rows->n_seqs == 0) return st;
-    hipLaunchKernelGGL(k_pages_trim, dim3(r.n), dim3(kThreads), 0, stream, p, r, keep);
+    hipLaunchKernelGGL(k_pages_trim, dim3(r.n), dim3(r.n <= 256 && r.width > 512 ? 1024 : 256), 0, stream, p, r, keep);
     return launched();
 }
 
@@ -578,8 +653,13 @@ extern "C" zx_status zx_pages_extend(const zx_page_pool *pool, const zx_page_row
     g.counted = reinterpret_cast<uint32_t *>(g.need + rows->n_seqs);
     g.log_slots = 6;
     while ((1u << g.log_slots) < 2 * rows->n_seqs) ++g.log_slots;
-    hipLaunchKernelGGL(k_pages_need, dim3(1 + g.n_segments), dim3(kThreads), (3u << g.log_slots) * 4, stream, g);
-    hipLaunchKernelGGL(k_pages_give, dim3(g.n_segments), dim3(kThreads), 0, stream, g);
+    const uint32_t lds = (3u << g.log_slots) * 4;
+    if (g.n_segments == 1) {
+        hipLaunchKernelGGL(k_pages_extend, dim3(1), dim3(kThreads), lds, stream, g);
+    } else {
+        hipLaunchKernelGGL(k_pages_need, dim3(1 + g.n_segments), dim3(kThreads), lds, stream, g);
+        hipLaunchKernelGGL(k_pages_give, dim3(g.n_segments), dim3(kThreads), 0, stream, g);
+    }
     return launched();
 }
 
@@ -604,12 +684,16 @@ extern "C" zx_status zx_pages_compact(const zx_page_pool *pool, const zx_page_ro
     g.nth = static_cast<int32_t *>(workspace);
     g.counted = reinterpret_cast<uint32_t *>(g.nth + pool->n_pages);
     g.n_segments = ceil_div(pool->n_pages, kSegment);
+    if (g.n_segments == 1 && (uint64_t)rows->n_seqs * rows->table_width <= 16384) {
+        hipLaunchKernelGGL(k_pages_compact, dim3(1), dim3(kThreads), 0, stream, g);
+        return launched();
+    }
     hipLaunchKernelGGL(k_pages_count, dim3(g.n_segments), dim3(kThreads), 0, stream, g);
     hipLaunchKernelGGL(k_pages_pair, dim3(g.n_segments), dim3(kThreads), 0, stream, g);
     // workgroups for the pairs, and for each row of the table
-    const uint32_t pairs = ceil_div(pool->n_pages / 2 + 1, kThreads), for_pairs = pairs < 256 ? pairs : 256;
-    const uint32_t most = ceil_div(rows->table_width, kThreads);
+    const uint32_t pairs = ceil_div(pool->n_pages / 2 + 1, kMoveThreads), for_pairs = pairs < 256 ? pairs : 256;
+    const uint32_t most = ceil_div(rows->table_width, kMoveThreads);
     const uint32_t fair = rows->n_seqs ? 1 + 1024 / rows->n_seqs : 1, per_row = most == 0 ? 1 : most < fair ? most : fair;
-    hipLaunchKernelGGL(k_pages_move, dim3(for_pairs + rows->n_seqs * per_row), dim3(kThreads), 0, stream, g, for_pairs, per_row);
+    hipLaunchKernelGGL(k_pages_move, dim3(for_pairs + rows->n_seqs * per_row), dim3(kMoveThreads), 0, stream, g, for_pairs, per_row);
     return launched();
 }
