@@ -159,6 +159,8 @@ def _part(t: torch.Tensor, name: str, shape, index: int, written: bool = False):
     n, h, d = shape
     s0, s1, s2 = t.stride()
     p = t.data_ptr()
+    if s2 == 1 and s1 == d and s0 == h * d and p % 16 == 0:          # (meets all that is asked for below)
+        return zx_rows(p, s0, s1), p, p + 2 * n * s0
     if n < 2:
         s0 = 0
     if h < 2:
@@ -179,8 +181,8 @@ def merge_attention(outs: Sequence[torch.Tensor], lses: Sequence[torch.Tensor], 
 
     A part whose lse is -inf is not looked at; a row where all are is zero.  out and lse may be one of outs and of lses.
     stream: a torch stream to run on after the work already enqueued on the current one."""
-    outs, lses = list(outs), list(lses)
-    if not 0 < len(outs) <= 16 or len(lses) != len(outs):
+    k = len(outs)
+    if not 0 < k <= 16 or len(lses) != k:
         raise ValueError("1 to 16 parts, each with its lse")
     f = outs[0]
     if not isinstance(f, torch.Tensor) or f.dim() != 3 or f.shape[2] not in (64, 128, 256) or f.shape[1] == 0 or not f.is_cuda:
@@ -189,10 +191,14 @@ def merge_attention(outs: Sequence[torch.Tensor], lses: Sequence[torch.Tensor], 
     if _away(index, stream):
         return _elsewhere(device, stream, (*outs, *lses, out, lse), lambda s: merge_attention(outs, lses, out, lse, s))
     n, heads, d = shape
-    parts = [_part(t, "a part", shape, index) for t in outs]
     rows = shape[:2]
-    where = [_like(t, "an lse", torch.float32, rows, index).data_ptr() for t in lses]
     size = 4 * n * heads
+    parts, where, follow = [], [], _forward._current_level >= 0
+    for t, l in zip(outs, lses):
+        parts.append(_part(t, "a part", shape, index))
+        where.append(_like(l, "an lse", torch.float32, rows, index).data_ptr())
+        if follow or l.requires_grad:
+            _no_gradient(l, "an lse")
     if out is None:
         out = f.new_empty(shape)
         o = zx_rows(out.data_ptr(), heads * d, d)
@@ -206,15 +212,13 @@ def merge_attention(outs: Sequence[torch.Tensor], lses: Sequence[torch.Tensor], 
     pl = None
     if lse is not None:
         pl = _like(lse, "lse", torch.float32, rows, index).data_ptr()
-        if any(pl < y and x < pl + size for _, x, y in parts) or any(pl != x and pl < x + size and x < pl + size for x in where):
-            raise ValueError("lse shares memory with a part and is not that part's")
-    if _forward._current_level >= 0 or any(t.requires_grad for t in lses) or (lse is not None and lse.requires_grad):
-        for t in (*lses, lse):
-            if t is not None:
-                _no_gradient(t, "an lse")
+        if follow or lse.requires_grad:
+            _no_gradient(lse, "lse")
+        for (_, x, y), z in zip(parts, where):
+            if pl < y and x < pl + size or pl != z and pl < z + size and z < pl + size:
+                raise ValueError("lse shares memory with a part and is not that part's")
     if n == 0:
         return out
-    k = len(parts)
     st = (_bound or _lib()).zx_attention_merge((zx_rows * k)(*[r for r, _, _ in parts]), (C.c_void_p * k)(*where), k, n, heads, d, C.byref(o), pl,
                                                _zx._raw_stream(device))
     if st != 0:

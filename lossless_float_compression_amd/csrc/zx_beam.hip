@@ -94,21 +94,77 @@ __device__ __forceinline__ uint32_t wave_reduce(uint32_t x, F f)
     return (uint32_t)__builtin_amdgcn_readfirstlane((int)f((uint32_t)s[0], (uint32_t)s[1]));
 }
 
-// A value that n at least of the wave's keys reach (n <= 64), and few more: the n-th largest itself, or, as soon as exactly
-// n keys reach it, a smaller one.  Found bit by bit from the first one in which any two keys differ; `top` is the largest key.
-__device__ __forceinline__ uint32_t nth_largest(uint32_t key, uint32_t top, uint32_t n)
+constexpr int kLevels = 4;
+template <int NT>
+struct EdgeRoom {
+    uint32_t low[NT / 64], high[NT / 64], keys[NT / 64], bins[kLevels][256];
+};
+
+// A value that n at least of the workgroup's keys reach (0 is no key), and few more: 1 where there are fewer than n keys.  From the
+// first bit in which any two keys differ on, eight bits at a time are counted, and what follows the bin that
+// the n-th largest key lies in is looked at only if that bin holds many.
+template <int NT>
+__device__ __forceinline__ uint32_t block_edge(uint32_t key, uint32_t n, EdgeRoom<NT> &m)
 {
-    const uint32_t low = wave_reduce(key, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
-    if (low == top) return top;
-    const int first = 31 - __builtin_clz(low ^ top);
-    uint32_t t = top & ~((2u << first) - 1u);
-    for (int bit = first; bit >= 0; --bit) {
-        const uint32_t u = t | (1u << bit);
-        const uint32_t c = (uint32_t)__popcll(__ballot(key >= u));
-        if (c >= n) t = u;
-        if (c == n) break;
+    const uint32_t tid = threadIdx.x, lane = tid & 63u;
+    const uint32_t wl = wave_reduce(key ? key : 0xFFFFFFFFu, [](uint32_t a, uint32_t b) { return a < b ? a : b; });
+    const uint32_t wh = wave_reduce(key, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+    const uint64_t some_keys = __ballot(key != 0);
+    if (lane == 0) {
+        m.keys[tid >> 6] = (uint32_t)__popcll(some_keys);
+        m.low[tid >> 6] = wl;
+        m.high[tid >> 6] = wh;
     }
-    return t;
+    for (uint32_t i = tid; i < kLevels * 256; i += NT) (&m.bins[0][0])[i] = 0;
+    __syncthreads();
+    uint32_t low = m.low[0], high = m.high[0], keys = m.keys[0];
+#pragma unroll
+    for (int i = 1; i < NT / 64; ++i) {
+        keys += m.keys[i];
+        low = m.low[i] < low ? m.low[i] : low;
+        high = m.high[i] > high ? m.high[i] : high;
+    }
+    if (keys < n) return 1u;
+    if (low == high) return high;
+    uint32_t width = 32u - (uint32_t)__builtin_clz(low ^ high);      // bits below what all keys share
+    uint32_t base = low & ~(uint32_t)((1ull << width) - 1ull);
+    for (int level = 0;; ++level) {
+        const uint32_t shift = width > 8 ? width - 8 : 0;
+        const bool in = key >= base && (uint64_t)(key - base) >> width == 0 && key;
+        if (in && key - base >> shift) atomicAdd(&m.bins[level][(key - base) >> shift], 1u);         // (bin 0 is what is left)
+        __syncthreads();
+        uint32_t c[4], all;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) c[i] = m.bins[level][4 * lane + i];
+        const uint32_t ahead = zxk::wave_excl_scan(c[0] + c[1] + c[2] + c[3], all);
+        uint32_t from = all - ahead;             // keys in the lane's bins and higher ones
+        int mine = -1;
+        uint32_t reach = 0, above = 0;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            if (from >= n) {
+                mine = i;
+                reach = from;
+                above = from - c[i];
+            }
+            from -= c[i];
+        }
+        const uint64_t some = __ballot(mine >= 0);
+        if (some) {
+            const int l = 63 - __builtin_clzll(some);
+            const uint32_t bin = 4u * (uint32_t)l + (uint32_t)__builtin_amdgcn_readlane(mine, l);
+            reach = (uint32_t)__builtin_amdgcn_readlane((int)reach, l);
+            above = (uint32_t)__builtin_amdgcn_readlane((int)above, l);
+            base += bin << shift;
+            // (bin 0 has not been counted)
+            if (bin && reach <= n + n / 2 + 4) return base;
+        } else {
+            above = all;
+        }
+        if (shift == 0 || level + 1 == kLevels) return base ? base : 1u;
+        n -= above < n ? above : n - 1;
+        width = shift;
+    }
 }
 
 template <int TY>
@@ -257,7 +313,8 @@ __global__ __launch_bounds__(kThreads) void k_beam_parts(BeamArgs g)
     typedef typename Key<TY>::T K;
     __shared__ float tile_top[kMostTiles][kThreads];
     __shared__ K room[kRoom];
-    __shared__ uint32_t hits[kHits], edges[kWaves], n_hits, n_room;
+    __shared__ uint32_t hits[kHits], n_hits, n_room;
+    __shared__ EdgeRoom<kThreads> edges;
     __shared__ K edge_key;
     const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
     const uint32_t row = blockIdx.x / g.parts, part = blockIdx.x - row * g.parts;
@@ -319,20 +376,14 @@ __global__ __launch_bounds__(kThreads) void k_beam_parts(BeamArgs g)
         work(tile + 1, b);
     }
     const float all = wave_max(top), from = all == -kInf ? 0.0f : all;
-    const uint32_t mine = nth_largest(ordered(top), ordered(all), g.n_out);
-    if (lane == 0) edges[wave] = mine;
     const double total = wave_sum((double)(sum * __builtin_amdgcn_exp2f((top - from) * c)));
     if (lane == 0) {
         Stat &o = g.stat[(uint64_t)blockIdx.x * kWaves + wave];
         o.top = all;
         o.sum = total;
     }
-    __syncthreads();
-    // n_out logits of one wave at least reach its edge, so n_out of the part reach the highest; they are hardly more
-    uint32_t high = edges[0];
-#pragma unroll
-    for (uint32_t i = 1; i < kWaves; ++i) high = edges[i] > high ? edges[i] : high;
-    const float edge = fmaxf(unordered(high), kLowest);
+    // n_out threads' maxima at least reach the edge, or all that there are; hardly more logits do
+    const float edge = fmaxf(unordered(block_edge(top > -kInf ? ordered(top) : 0u, g.n_out, edges)), kLowest);
     auto take = [&](const float (&y)[N], uint32_t place, K ek) {     // a piece's logits from the edge on, with keys from ek on
         uint32_t yes = 0;
 #pragma unroll
@@ -429,7 +480,8 @@ __global__ __launch_bounds__(NT) void k_beam_pick(BeamArgs g)
     __shared__ Best list[kList];
     __shared__ double base[kMostBeams], tops[kMostBeams], weight[kMostBeams];
     __shared__ uint32_t kind[kMostBeams];        // 0: no candidates, 1: the parts', 2: finished
-    __shared__ uint32_t count, edge_hi[NT / 64];
+    __shared__ uint32_t count, few, survivors[kList];
+    __shared__ EdgeRoom<NT> edges;
     __shared__ uint64_t edge_key, edge_place;
     const uint32_t tid = threadIdx.x, lane = tid & 63u, wave = tid >> 6;
     const uint32_t row0 = blockIdx.x * g.beams;
@@ -494,14 +546,8 @@ __global__ __launch_bounds__(NT) void k_beam_pick(BeamArgs g)
         Best v;
         if (entry(e / g.depth, e % g.depth, v) && v.key > key) key = v.key;
     }
-    // n_out keys of one wave at least reach the edge (or it is zero), so n_out of the group do
-    const uint32_t key_hi = (uint32_t)(key >> 32);
-    const uint32_t hi = nth_largest(key_hi, wave_reduce(key_hi, [](uint32_t a, uint32_t b) { return a > b ? a : b; }), g.n_out);
-    if (lane == 0) edge_hi[wave] = hi;
-    __syncthreads();
-    uint32_t h = 0;
-    for (int i = 0; i < NT / 64; ++i) h = edge_hi[i] > h ? edge_hi[i] : h;
-    uint64_t ek = (uint64_t)h << 32, ep = ~0ull;
+    // n_out threads' keys at least reach the edge, or all that there are
+    uint64_t ek = (uint64_t)block_edge((uint32_t)(key >> 32), g.n_out, edges) << 32, ep = ~0ull;
     uint32_t n;
     for (uint32_t round = 0;; ++round) {
         auto enter = [&](const Best &v) {
@@ -514,8 +560,16 @@ __global__ __launch_bounds__(NT) void k_beam_pick(BeamArgs g)
             const uint32_t l = e / g.depth, nth = e % g.depth;
             Best v = own;
             if (!(e == tid ? have : entry(l, nth, v)) || !enter(v) || nth + 1 < g.depth) continue;
-            for (uint32_t i = g.depth; i < g.n_out; ++i)
-                if (!entry(l, i, v) || !enter(v)) break;
+            // eight further ones under way at once
+            for (uint32_t i = g.depth; i < g.n_out; i += 8) {
+                Cand more[8];
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j) more[j] = cand[(uint64_t)l * g.n_out + (i + j < g.n_out ? i + j : g.n_out - 1)];
+                bool on = true;
+#pragma unroll
+                for (uint32_t j = 0; j < 8; ++j) on = on && i + j < g.n_out && value(l, more[j], v) && enter(v);
+                if (!on) break;
+            }
         }
         if (tid < g.beams && kind[tid] == 2) {   // finished: one candidate
             Best v;
@@ -527,23 +581,49 @@ __global__ __launch_bounds__(NT) void k_beam_pick(BeamArgs g)
         __syncthreads();
         n = count;
         const uint32_t some = n < kList ? n : kList;
-        for (uint32_t i = tid; i < some; i += NT) {
-            const Best v = list[i];
+        auto rank_of = [&](const Best &v, uint32_t of, auto at) {
             uint32_t r = 0;
 #pragma unroll 8
-            for (uint32_t j = 0; j < some; ++j) r += better(list[j].key, list[j].place, v.key, v.place);
-            if (n > kList) {
-                if (r == g.n_out - 1) {          // more than fit: another round from the n_out-th of those that did on
-                    edge_key = v.key;
-                    edge_place = v.place;
+            for (uint32_t j = 0; j < of; ++j) {
+                const Best &o = list[at(j)];
+                r += better(o.key, o.place, v.key, v.place);
+            }
+            return r;
+        };
+        auto put = [&](const Best &v, uint32_t r) {
+            if (r >= g.n_out) return;
+            const uint64_t to = (uint64_t)blockIdx.x * g.n_out + r;
+            const uint32_t b = (uint32_t)(v.place >> 32), t = (uint32_t)v.place;
+            g.out_scores[to] = (float)v.total;
+            g.parents[to] = (int32_t)b;
+            g.tokens[to] = (int32_t)t;
+            g.out_finished[to] = kind[b] == 2 || (g.end >= 0 && t == (uint32_t)g.end);
+        };
+        if (n > kList) {
+            // more than fit: another round from the n_out-th of those that did on
+            for (uint32_t i = tid; i < some; i += NT)
+                if (rank_of(list[i], some, [](uint32_t j) { return j; }) == g.n_out - 1) {
+                    edge_key = list[i].key;
+                    edge_place = list[i].place;
                 }
-            } else if (r < g.n_out) {
-                const uint64_t to = (uint64_t)blockIdx.x * g.n_out + r;
-                const uint32_t b = (uint32_t)(v.place >> 32), t = (uint32_t)v.place;
-                g.out_scores[to] = (float)v.total;
-                g.parents[to] = (int32_t)b;
-                g.tokens[to] = (int32_t)t;
-                g.out_finished[to] = kind[b] == 2 || (g.end >= 0 && t == (uint32_t)g.end);
+        } else if (n <= 2 * g.n_out + 64) {
+            for (uint32_t i = tid; i < n; i += NT) put(list[i], rank_of(list[i], n, [](uint32_t j) { return j; }));
+        } else {
+            // many: an edge among them first
+            uint32_t top = 0;
+            for (uint32_t i = tid; i < n; i += NT) {
+                const uint32_t k = (uint32_t)(list[i].key >> 32);
+                top = k > top ? k : top;
+            }
+            if (tid == 0) few = 0;
+            const uint32_t e = block_edge(top, g.n_out, edges);
+            for (uint32_t i = tid; i < n; i += NT)
+                if ((uint32_t)(list[i].key >> 32) >= e) survivors[atomicAdd(&few, 1u)] = i;
+            __syncthreads();
+            const uint32_t left = few;
+            for (uint32_t i = tid; i < left; i += NT) {
+                const Best &v = list[survivors[i]];
+                put(v, rank_of(v, left, [&](uint32_t j) { return survivors[j]; }));
             }
         }
         __syncthreads();

@@ -80,7 +80,7 @@ struct ForkArgs {
     Rows r;
     const int32_t *parents;
     uint32_t beams, log_strip;                   // columns that a workgroup holds at a time
-    int32_t write_held;                          // one workgroup a group: it writes the lengths too
+    uint32_t share;                              // workgroups of a group; a single one writes the lengths too
 };
 
 // The lengths and parents of a group into LDS, and the most pages that a row has; whether all are in range.
@@ -109,7 +109,7 @@ __global__ __launch_bounds__(1024) void k_pages_fork(ForkArgs g)
     extern __shared__ int32_t lds[];
     __shared__ uint32_t bad, cols;
     int32_t *held = lds, *parent = held + g.beams, *children = parent + g.beams, *strip = children + g.beams;
-    const uint32_t group = blockIdx.y, tid = threadIdx.x, ls = g.log_strip, ns = 1u << ls;
+    const uint32_t group = blockIdx.x / g.share, nth = blockIdx.x % g.share, tid = threadIdx.x, ls = g.log_strip, ns = 1u << ls;
     int32_t *table = g.r.table + (uint64_t)group * g.beams * g.r.width;
     int32_t x[4];                                // four entries of a thread under way at once, the first beside the lengths
     auto read = [&](uint32_t c0, uint32_t i0, auto in) {
@@ -120,14 +120,14 @@ __global__ __launch_bounds__(1024) void k_pages_fork(ForkArgs g)
             if (r < g.beams && in(r, c)) x[u] = table[(uint64_t)r * g.r.width + c];
         }
     };
-    const uint32_t first = blockIdx.x * ns;
+    const uint32_t first = nth * ns;
     read(first, tid, [&](uint32_t, uint32_t c) { return c < g.r.width; });
     if (!load_group(g, group, held, parent, &bad, &cols)) return;
     for (uint32_t i = tid; i < g.beams; i += blockDim.x) children[i] = 0;
     __syncthreads();
     for (uint32_t i = tid; i < g.beams; i += blockDim.x)
         if (parent[i] >= 0) atomicAdd(&children[parent[i]], 1);
-    for (uint32_t c0 = first; c0 < cols; c0 += gridDim.x * ns) {
+    for (uint32_t c0 = first; c0 < cols; c0 += g.share * ns) {
         const uint32_t nc = cols - c0 < ns ? cols - c0 : ns;
         __syncthreads();
         for (uint32_t i0 = tid; i0 < g.beams << ls; i0 += 4 * blockDim.x) {
@@ -168,7 +168,7 @@ __global__ __launch_bounds__(1024) void k_pages_fork(ForkArgs g)
             add();
         }
     }
-    if (g.write_held)
+    if (g.share == 1)
         for (uint32_t i = tid; i < g.beams; i += blockDim.x)
             if (parent[i] != (int32_t)i) g.r.held[(uint64_t)group * g.beams + i] = parent[i] < 0 ? 0 : held[parent[i]];
 }
@@ -603,11 +603,10 @@ extern "C" zx_status zx_pages_fork(const zx_page_pool *pool, const zx_page_rows 
     // a group with more than two strips is shared by workgroups, about 2048 in all; the lengths are then written by a launch of
     // their own, behind those that read them
     const uint32_t n_strips = ceil_div(width, 1u << g.log_strip), fair = 1 + 2047 / groups;
-    const uint32_t wgs = n_strips <= 2 ? 1 : n_strips < fair ? n_strips : fair;
-    g.write_held = wgs == 1;
+    g.share = n_strips <= 2 ? 1 : n_strips < fair ? n_strips : fair;
     const uint32_t lds = (3 * beams + (beams << g.log_strip)) * 4, threads = beams << g.log_strip <= 1024 ? 256 : 1024;
-    hipLaunchKernelGGL(k_pages_fork, dim3(wgs, groups), dim3(threads), lds, stream, g);
-    if (wgs > 1) hipLaunchKernelGGL(k_pages_fork_held, dim3(groups), dim3(256), 2 * beams * 4, stream, g);
+    hipLaunchKernelGGL(k_pages_fork, dim3(groups * g.share), dim3(threads), lds, stream, g);
+    if (g.share > 1) hipLaunchKernelGGL(k_pages_fork_held, dim3(groups), dim3(256), 2 * beams * 4, stream, g);
     return launched();
 }
 

@@ -90,7 +90,7 @@ def _device_of(device) -> torch.device:
 
 
 def _int32(t, name: str, index: Optional[int] = None) -> torch.Tensor:
-    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or not t.is_cuda or not t.is_contiguous():
+    if not isinstance(t, torch.Tensor) or t.dtype is not torch.int32 or not t.is_contiguous() or not t.is_cuda:
         raise ValueError(f"{name} must be a contiguous device int32 tensor")
     if index is not None and t.get_device() != index:
         raise ValueError(f"{name} is on {t.device}, the cache on cuda:{index}")
@@ -558,8 +558,8 @@ class PagedKVCache:
 
     def copy_pages(self, copies, err: Optional[torch.Tensor] = None, stream=None) -> None:
         """Carry a list of page copies out in this cache alone (`PagedLayers` does so in all layers' at once)."""
-        from .pages import PagedLayers
-        PagedLayers([self]).copy_pages(copies, err, stream)
+        from .pages import _copy
+        _copy(self, self._ref, 1, copies, err, stream)
 
     # ---- pages in a slot pool
     def blocks_per_page(self) -> int:

@@ -17,6 +17,7 @@ import ctypes as C
 from typing import Optional, Sequence, Tuple
 
 import torch
+import torch.autograd.forward_ad as _forward
 
 from . import paged as _paged
 from . import zx as _zx
@@ -174,19 +175,22 @@ class PagePool:
     # ---- argument checks
     def _rows(self, table: torch.Tensor, held: torch.Tensor, err: Optional[torch.Tensor], *apart) -> Tuple[zx_page_rows, Optional[int]]:
         """The rows, and err's address; `apart`: spans of what else is read or written."""
-        _int32(table, "table", self._index)
-        _int32(held, "held", self._index)
-        shape = table.shape
-        if len(shape) != 2 or held.shape != shape[:1]:
+        index = self._index
+        _int32(table, "table", index)
+        _int32(held, "held", index)
+        try:
+            n, width = table.shape
+        except ValueError:
+            n = -1
+        if held.shape != (n,):
             raise ValueError("table must be [rows, width] and held [rows]")
-        spans = [_words(table), _words(held), self._own, *apart]
-        e = None
+        t, h, e = table.data_ptr(), held.data_ptr(), None
+        spans = [(t, t + 4 * n * width), (h, h + 4 * n), self._own, *apart]
         if err is not None:
-            spans.append(_words(_int32(err, "err", self._index)))
+            spans.append(_words(_int32(err, "err", index)))
             e = err.data_ptr()
-        rows = zx_page_rows(spans[0][0], spans[1][0], *shape)
         _all_apart(spans)
-        return rows, e
+        return zx_page_rows(t, h, n, width), e
 
     def _list(self, copies: Optional[PageCopies], least: int) -> PageCopies:
         if copies is None:
@@ -318,14 +322,19 @@ class PagedLayers:
         """Carry `copies` out in every cache: the first tokens of a source page's keys and values, bit for bit, over those of the destination
         page, and the bounds of the blocks that they reach into.  A page that is written must be in no other pair.  Pairs with page ids
         or counts of tokens out of range are left out, with 4 in `err` (device int32 word).  stream: as `PagePool`."""
-        if _away(self._index, stream):
-            return _elsewhere(self.device, stream, (copies.pairs, copies.count, err, *self._tensors), lambda s: self.copy_pages(copies, err, s))
-        if copies.device != self.device:
-            raise ValueError(f"the copies are on {copies.device}, the caches on {self.device}")
-        if self._gradients:
-            for t in self._tensors:
-                _paged._no_gradient(t, "a tensor of the caches")
-        e = None if err is None else _int32(err, "err", self._index).data_ptr()
-        st = _lib().zx_paged_copy(self._c, len(self.caches), copies._ref, e, _zx._raw_stream(self.device))
-        if st != 0:
-            raise _zx.ZxError("zx_paged_copy", st)
+        _copy(self, self._c, len(self.caches), copies, err, stream)
+
+
+def _copy(of, structs, n: int, copies: PageCopies, err: Optional[torch.Tensor], stream) -> None:
+    """The copies in the caches of `of` (a PagedLayers or one PagedKVCache), n structs."""
+    if _away(of._index, stream):
+        return _elsewhere(of.device, stream, (copies.pairs, copies.count, err, *of._tensors), lambda s: _copy(of, structs, n, copies, err, s))
+    if copies.device != of.device:
+        raise ValueError(f"the copies are on {copies.device}, the caches on {of.device}")
+    if of._gradients or _forward._current_level >= 0:
+        for t in of._tensors:
+            _paged._no_gradient(t, "a tensor of the caches")
+    e = None if err is None else _int32(err, "err", of._index).data_ptr()
+    st = (_bound or _lib()).zx_paged_copy(structs, n, copies._ref, e, _zx._raw_stream(of.device))
+    if st != 0:
+        raise _zx.ZxError("zx_paged_copy", st)

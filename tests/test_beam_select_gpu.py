@@ -82,7 +82,7 @@ def made(G, K, V, dtype, seed=0, pad=0, start=0, spread=3.0):
 @pytest.mark.parametrize("dtype", TYPES)
 @pytest.mark.parametrize("G,K,V,M", [(1, 1, 1, 1), (1, 1, 1, 5), (2, 3, 1, 4), (1, 4, 3, 8), (3, 2, 31, 64), (1, 1, 64, 64), (2, 5, 513, 10), (1, 4, 4097, 8),
                                      (3, 7, 2047, 13), (1, 64, 700, 64), (5, 3, 50001, 6), (1, 2, 128256, 4), (40, 8, 9001, 16), (700, 2, 999, 3),
-                                     (1, 1, 1 << 20, 64), (150, 8, 8191, 8), (33, 30, 2222, 60)])
+                                     (1, 1, 1 << 20, 64), (150, 8, 8191, 8), (33, 30, 2222, 60), (9000, 2, 5, 3), (1, 3, 70000, 64)])
 def test_sizes(dtype, G, K, V, M):
     x, s = made(G, K, V, dtype, seed=V)
     check(zx.beam_select(x, s, M), x, s, M)

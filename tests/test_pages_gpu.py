@@ -253,6 +253,30 @@ def test_wide_tables(groups, K, W):
     d.trim([h // 3 for h in m.held])
 
 
+@pytest.mark.parametrize("K", (1, 2))
+def test_the_most_rows(K):
+    """65536 rows, as groups of their own and of two."""
+    n, T = 65536, 16
+    g = torch.Generator(device="cuda").manual_seed(K)
+    pool, err = zx.PagePool(2 * n, T), i32([0])
+    perm = torch.randperm(2 * n, generator=g, device="cuda").to(torch.int32).view(n, 2)
+    table, held = perm.clone(), torch.randint(0, 33, (n,), generator=g, device="cuda", dtype=torch.int32)
+    per = (held + T - 1) // T
+    used = torch.arange(2, device="cuda") < per[:, None]
+    pool.refs[table[used].long()] = 1
+    was = held.clone()
+    parents = torch.randint(-1, K, (n // K, K), generator=g, device="cuda", dtype=torch.int32)
+    pool.fork(table, held, parents, err=err)
+    goes = parents.view(-1) >= 0
+    of = (torch.arange(n, device="cuda") // K * K + parents.view(-1).clamp(min=0)).long()
+    assert torch.equal(held, torch.where(goes, was[of], 0))
+    mine = torch.arange(2, device="cuda") < ((held + T - 1) // T)[:, None]
+    assert torch.equal(table, torch.where(mine, perm[of], perm))
+    assert torch.equal(pool.refs.long(), torch.bincount(table[mine].long(), minlength=2 * n))
+    pool.trim(table, held, err=err)
+    assert not bool(pool.refs.any()) and not bool(held.any()) and int(err) == 0
+
+
 def test_rows_beyond_the_limit():
     d = Device(Model(100, 16, 3, 2))
     i = lambda *s: torch.zeros(s, dtype=torch.int32, device="cuda")   # noqa: E731
