@@ -3,14 +3,23 @@
 // With lse_b = ln sum_t exp(s x_bt) over the tokens that beam b may take, candidate (b, t) has the total
 // score_b + s x_bt - lse_b, and the n_out candidates of a group with the largest weight_b * total are taken.
 //
-// Bound by reading the logits once.  k_beam_parts: a wave holds one part of a row in registers, 64 * E logits,
-// so that the part's maximum is known before the first exponential and none is taken twice.  The n_out largest of
-// the part are found without sorting: the n_out-th largest of the 64 lanes' maxima (by bisection of its bits, with
-// ballots) is no larger than the n_out-th largest logit, so only logits from there on can be among them, and
-// hardly more than n_out are; those few are ranked by counting.  k_beam_pick: one workgroup a group joins the
-// parts' sums, turns the parts' candidates into totals, and finds the n_out best of them in the same two steps.
+// Bound by reading the logits once.  k_beam_parts streams a part of a row: each thread keeps its running maximum and its sum of
+// exponentials relative to that, and the maxima of its shares of the part's tiles.  The n_out largest logits of the part are found
+// without sorting it: the n_out-th largest of the threads' maxima is no larger than the n_out-th largest logit,
+// so only logits from there on can be among them, and hardly more than n_out are; the few tiles' shares that hold them are read again
+// (from L2) and the logits ranked by counting.  k_beam_pick: one workgroup a group joins the parts' sums, turns the parts' candidates into totals and
+// finds the n_out best of them the same way.
 //
-// Rounding: a part's sum is taken in 32 bits over a lane's E logits and in 64 bits from there on; totals are
+// 64 x 8 of 128256, BF16, 16 out, a seventh of the beams finished: 29 + 6 us, 111 MB read (3.8 TB/s; without what follows the last tile 27, with
+// no exponentials 27); 256 x 8: 105 us, 5.0 TB/s; in 32 bits 190 us, 5.5 TB/s.  1 x 4 of 32000: 5.4 + 4.6.
+// Tried, in us of k_beam_parts for 64 x 8: a part of 4096 logits held in registers by each wave, which ranks its own 75, then 34 with the maxima of
+// pieces kept and cheaper ranking, 33 with parts of a workgroup (every part pays for its edge and ranking); the next two tiles under way
+// 30.9, tiles of half the size 30.0.
+//
+// Many equal logits at the edge do not fit the list of 256 that are ranked; then the part is read again from a sharper edge on (all logits
+// equal: 64 x 8 of 128256 300 us, 1 x 4 of 32000 60).
+//
+// Rounding: exponentials are summed in 32 bits by a thread (up to 256 logits, four sums) and in 64 bits from there on; totals are
 // formed and compared in 64 bits, since which of two beams is taken must not turn on a rounding.
 #include "zx_common.h"
 
@@ -669,6 +678,8 @@ inline zx_status plan(int type, uint32_t groups, uint32_t beams, uint32_t vocab,
     const uint64_t rows = (uint64_t)groups * beams;
     const uint32_t piece = kThreads * (type == F32 ? 4 : 8);
     auto up = [](uint64_t a, uint64_t b) { return (a + b - 1) / b; };
+    // tiles of four pieces where that makes a workgroup a CU (parts of one such tile each: 7 x 5 of 50001 in 32 bits 7.2 us, of one piece 8.1);
+    // parts as long as leave 1024 workgroups, four a CU (64 x 8 of 128256: 29.6 us; 1280 30.4, 2048 31.0, 4096 34.4, parts of a tile 49.7)
     o.pieces = rows * up(vocab, 4 * piece) < 256 ? 1 : 4;
     const uint64_t row_tiles = up(vocab, o.pieces * piece);
     uint64_t tiles = up(rows * row_tiles, 1024);
@@ -738,6 +749,7 @@ extern "C" zx_status zx_beam_select(const zx_beam_logits *in, const float *score
     if (in->type == ZX_LOGITS_BF16) launch_parts<BF16>(g, sp.pieces, wgs, stream);
     else if (in->type == ZX_LOGITS_F16) launch_parts<F16>(g, sp.pieces, wgs, stream);
     else launch_parts<F32>(g, sp.pieces, wgs, stream);
+    // (more threads where there are more rows' sums to join or more candidates to look at: 64 x 8 6.1 us, with 256 threads 9.4)
     const uint32_t lists = in->beams * sp.parts, threads = lists > 512 || in->beams > 4 ? 1024 : 256;
     g.depth = lists >= threads ? 1 : threads / lists < n_out ? threads / lists : n_out;
     if (threads == 1024) hipLaunchKernelGGL((k_beam_pick<1024>), dim3(in->n_groups), dim3(1024), 0, stream, g);

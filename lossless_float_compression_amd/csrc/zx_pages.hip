@@ -6,8 +6,12 @@
 // arguments alone: counts are added up with atomics on whole numbers, whose order does not show, and ranks come
 // from prefix sums over the pool, which a launch ahead has counted by segments of kSegment pages.
 //
-// Bound by launches (one to three of a few us) for the pools and tables of a serving step; the bytes are the table's entries in
-// use and refs, read and written once.
+// Bound by launches (one or two of 3 to 6 us) for the pools and tables of a serving step: each is a chain of trips to memory, lengths -> table ->
+// counts -> ranks, so what does not depend on each other is read together, and pools of up to 4096 pages are served by one workgroup in
+// one launch.  The bytes are the table's entries in use and refs, read and written once.
+// Four beams over 1000 tokens: fork 4.0 us, extend 5.0; 64 x 8 beams over 32768 tokens in pages of 16 (a million
+// entries): 9.9 + 2.0 and 4.6 + 5.6; 256 sequences, five tokens each: trim 3.0, extend 4.0 + 4.9; 16 prompts of 20000: 4.5, 3.4 + 5.7;
+// 6000 pages brought together: 9.0.
 #include "zx_paged.h"
 
 namespace zxg {
@@ -101,9 +105,8 @@ __device__ __forceinline__ bool load_group(const ForkArgs &g, uint32_t group, in
 }
 
 // Old rows are read into LDS strip by strip, then written where they go on, so rows may trade places.  A page's
-// count changes by (rows that go on from a row that holds it) - 1 for each such row; a thread adds
-// these up down a column as long as neighbouring rows hold the same page there (beams of one prompt mostly
-// do), and most sums are zero.
+// count changes by (rows that go on from a row that holds it) - 1 for each such row; these are added up over
+// neighbouring rows that hold the same page in a column (beams of one prompt mostly do), and most sums are zero.
 __global__ __launch_bounds__(1024) void k_pages_fork(ForkArgs g)
 {
     extern __shared__ int32_t lds[];
@@ -143,29 +146,15 @@ __global__ __launch_bounds__(1024) void k_pages_fork(ForkArgs g)
             if (q >= 0 && q != (int32_t)r && c < nc && c0 + c < pages_of(g.p, held[q]))
                 table[(uint64_t)r * g.r.width + c0 + c] = strip[((uint32_t)q << ls) + c];
         }
-        // columns shared out over the threads, each in runs of up to 64 rows
-        const uint32_t runs = div_up(g.beams, 64);
-        for (uint32_t i = tid; i < runs << ls; i += blockDim.x) {
-            const uint32_t c = i & (ns - 1), r0 = (i >> ls) * 64, r1 = r0 + 64 < g.beams ? r0 + 64 : g.beams;
-            if (c >= nc) continue;
-            uint32_t page = 0xFFFFFFFFu;
-            int32_t sum = 0;
-            auto add = [&] {
-                if (sum == 0) return;
-                if (page >= g.p.n_pages) report(g.p.err, ZX_E_CORRUPT);
-                else if (atomicAdd(&g.p.refs[page], sum) + sum < 0) report(g.p.err, ZX_E_CORRUPT);
-            };
-            for (uint32_t r = r0; r < r1; ++r) {
-                if (c0 + c >= pages_of(g.p, held[r])) continue;
-                const uint32_t is = (uint32_t)strip[(r << ls) + c];
-                if (is != page) {
-                    add();
-                    sum = 0;
-                    page = is;
-                }
-                sum += children[r] - 1;
-            }
-            add();
+        // runs of up to 64 neighbouring rows that hold the same page in a column, one thread each
+        for (uint32_t i = tid; i < g.beams << ls; i += blockDim.x) {
+            const uint32_t r = i >> ls, c = i & (ns - 1), page = (uint32_t)strip[i];
+            auto holds = [&](uint32_t q) { return c0 + c < pages_of(g.p, held[q]) && (uint32_t)strip[(q << ls) + c] == page; };
+            if (!holds(r) || ((r & 63u) && holds(r - 1))) continue;
+            int32_t sum = children[r] - 1;
+            for (uint32_t q = r + 1; q < g.beams && (q & 63u) && holds(q); ++q) sum += children[q] - 1;
+            if (sum == 0) continue;
+            if (page >= g.p.n_pages || atomicAdd(&g.p.refs[page], sum) + sum < 0) report(g.p.err, ZX_E_CORRUPT);
         }
     }
     if (g.share == 1)
@@ -596,10 +585,10 @@ extern "C" zx_status zx_pages_fork(const zx_page_pool *pool, const zx_page_rows 
     g.parents = parents;
     g.beams = beams;
     const uint32_t groups = rows->n_seqs / beams;
-    // 16 KB of table entries at a time, four columns at least
+    // 4 KB of table entries at a time, four columns at least (16 KB: 10.9 us for 64 x 8 rows of 2068 entries, 4 KB: 9.9)
     const uint32_t width = rows->table_width;
     g.log_strip = 10;
-    while (g.log_strip > 2 && (((uint64_t)beams << g.log_strip) > 4096 || 1u << (g.log_strip - 1) >= width)) --g.log_strip;
+    while (g.log_strip > 2 && (((uint64_t)beams << g.log_strip) > 1024 || 1u << (g.log_strip - 1) >= width)) --g.log_strip;
     // a group with more than two strips is shared by workgroups, about 2048 in all; the lengths are then written by a launch of
     // their own, behind those that read them
     const uint32_t n_strips = ceil_div(width, 1u << g.log_strip), fair = 1 + 2047 / groups;

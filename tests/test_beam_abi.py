@@ -164,3 +164,31 @@ def test_what_tensors_reach():
     p = t.data_ptr()
     assert pages._span(t) == (p, p + 96) and pages._span(t[1:3, 2:4]) == (p + 32, p + 64) and len(set(pages._span(t[:0]))) == 1
     assert pages._meets(t[:2], t[1:]) and not pages._meets(t[:2], t[2:]) and not pages._meets(t[:0], t)
+
+
+def test_caches_that_autograd_follows_are_not_copied_in():
+    """By either mode; without one, as they are."""
+    import torch.autograd.forward_ad as forward
+
+    t = torch.zeros((2, 3), dtype=torch.bfloat16)
+    list_ = type("Copies", (), dict(device="cpu", pairs=t, count=t))
+    of = type("Of", (), dict(_index=0, device="elsewhere", _tensors=(t,), _gradients=False))
+    with pytest.MonkeyPatch.context() as m:
+        m.setattr(torch.cuda, "current_device", lambda: 0)
+        with pytest.raises(ValueError, match="the copies are on"):
+            pages._copy(of, None, 1, list_, None, None)
+        of.device = "cpu"
+        with forward.dual_level():
+            of._tensors = (forward.make_dual(t, torch.ones_like(t)),)
+            with pytest.raises(ValueError, match="gradient"):
+                pages._copy(of, None, 1, list_, None, None)
+        of._tensors, of._gradients = (t.clone().requires_grad_(),), True
+        with pytest.raises(ValueError, match="gradient"):
+            pages._copy(of, None, 1, list_, None, None)
+
+
+def test_stretches_that_meet():
+    pages._all_apart([(8, 12), (0, 8), (12, 12), (12, 20), (20, 20)])
+    for bad in ([(0, 8), (4, 12)], [(0, 20), (4, 8)], [(0, 20), (4, 8), (8, 12)], [(4, 8), (4, 8)]):
+        with pytest.raises(ValueError, match="share memory"):
+            pages._all_apart(bad)

@@ -1,9 +1,10 @@
 """The choice of the next beams against its definition in 64 bits.
 
-How far a score may be off.  A part's sum: x - top (2^-24 of itself), times a constant that is rounded (2^-24), rounded (2^-24), so an
-exponential's argument d is off by 3 |d| 2^-24; its exponential by one step more (2^-23); up to 16 are added up in 32 bits one
-after the other, then 4 (19 * 2^-24 of the sum).  Weighted by the probabilities p, sum p |d| = H(p) - ln sum e^d <= ln vocab <= 17: the ln of the sum is off by
-less than (3 * 17 + 2 + 19) 2^-24 = 72 * 2^-24.  What is in 64 bits adds nothing to that; the score itself is rounded to 32 bits (2^-24 of itself)."""
+How far a score may be off.  An exponential's argument (x - top, times a rounded constant, rounded) is off by 3 |d| 2^-24, the
+exponential by one step more (2^-23).  Weighted by the probabilities p, sum p |d| = H(p) - ln sum e^d <= ln vocab <= 17.  A thread adds up in 32 bits:
+ten roundings a tile and two of the rescaled sum, eight tiles at most, each 2^-24 of the sum; so the ln of the sum is off by less than (3 * 17 + 2 + 96) 2^-24.  The
+cases here are held to half of that, 72 * 2^-24 (their sums have one or two tiles a thread, 24 roundings).  What is in 64 bits adds nothing to that; the score
+itself is rounded to 32 bits (2^-24 of itself)."""
 import math
 
 import pytest
