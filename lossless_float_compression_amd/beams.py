@@ -8,7 +8,7 @@ import torch
 import torch.autograd.forward_ad as _forward
 
 from . import zx as _zx
-from .pages import _away, _elsewhere, _meets
+from .pages import _away, _elsewhere, _meets, _stream_of
 from .paged import _apart, _int32, _no_gradient, zx_rows
 
 MOST_BEAMS = 64
@@ -144,7 +144,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: Optional[int]
         need = _needs[key] = L.zx_beam_select_workspace_bytes(*key)
     st = L.zx_beam_select(C.byref(zx_beam_logits(logits.data_ptr(), sg if G > 1 else 0, sk if K > 1 else 0, kind, G, K, V)), scores.data_ptr(),
                           pw, pf, end, pa, scale, M, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(),
-                          raw(need).data_ptr(), need, e, _zx._raw_stream(device))
+                          raw(need).data_ptr(), need, e, _stream_of(index))
     if st != 0:
         raise _zx.ZxError("zx_beam_select", st)
     return out
@@ -220,7 +220,7 @@ def merge_attention(outs: Sequence[torch.Tensor], lses: Sequence[torch.Tensor], 
     if n == 0:
         return out
     st = (_bound or _lib()).zx_attention_merge((zx_rows * k)(*[r for r, _, _ in parts]), (C.c_void_p * k)(*where), k, n, heads, d, C.byref(o), pl,
-                                               _zx._raw_stream(device))
+                                               _stream_of(index))
     if st != 0:
         raise _zx.ZxError("zx_attention_merge", st)
     return out

@@ -67,12 +67,19 @@ def _lib():
     return _bound
 
 
+# the cheap accessors, where this torch build has them
+_device = getattr(torch._C, "_cuda_getDevice", None) or torch.cuda.current_device
+_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _away(index: int, stream) -> bool:
     """Whether a call has to change the current device or stream first (a raw stream handle will not do: memory is
     allocated on the stream that uses it)."""
-    if stream is not None and not isinstance(stream, torch.Stream):
+    if stream is None:
+        return _device() != index
+    if not isinstance(stream, torch.Stream):
         raise ValueError("stream must be a torch stream (torch.cuda.ExternalStream makes one of a raw handle)")
-    return torch.cuda.current_device() != index or (stream is not None and _zx._side_stream(stream) is not None)
+    return _device() != index or _zx._side_stream(stream) is not None
 
 
 def _elsewhere(device: torch.device, stream, tensors, call):
@@ -175,19 +182,21 @@ class PagePool:
     # ---- argument checks
     def _rows(self, table: torch.Tensor, held: torch.Tensor, err: Optional[torch.Tensor], *apart) -> Tuple[zx_page_rows, Optional[int]]:
         """The rows, and err's address; `apart`: spans of what else is read or written."""
-        index = self._index
-        _int32(table, "table", index)
-        _int32(held, "held", index)
+        _int32(table, "table", self._index)
         try:
             n, width = table.shape
         except ValueError:
-            n = -1
-        if held.shape != (n,):
+            n, width = -1, 0
+        return self._rows_at(table.data_ptr(), n, width, held, err, apart)
+
+    def _rows_at(self, t: int, n: int, width: int, held: torch.Tensor, err: Optional[torch.Tensor], apart) -> Tuple[zx_page_rows, Optional[int]]:
+        """The same for a table at an address."""
+        if _int32(held, "held", self._index).shape != (n,):
             raise ValueError("table must be [rows, width] and held [rows]")
-        t, h, e = table.data_ptr(), held.data_ptr(), None
+        h, e = held.data_ptr(), None
         spans = [(t, t + 4 * n * width), (h, h + 4 * n), self._own, *apart]
         if err is not None:
-            spans.append(_words(_int32(err, "err", index)))
+            spans.append(_words(_int32(err, "err", self._index)))
             e = err.data_ptr()
         _all_apart(spans)
         return zx_page_rows(t, h, n, width), e
@@ -198,12 +207,6 @@ class PagePool:
         if copies.device != self.device or copies.cap < least:
             raise ValueError(f"copies must be on {self.device} with room for {least}")
         return copies
-
-    def _enqueue(self, name: str, *args) -> None:
-        # (a workspace that is let go here is handed out again on this stream only, behind the call)
-        st = getattr(_bound or _lib(), name)(*args, _zx._raw_stream(self.device))
-        if st != 0:
-            raise _zx.ZxError(name, st)
 
     # ---- operators
     def fork(self, table: torch.Tensor, held: torch.Tensor, parents: torch.Tensor, err: Optional[torch.Tensor] = None, stream=None) -> None:
@@ -216,7 +219,9 @@ class PagePool:
         rows, e = self._rows(table, held, err, _words(parents))
         if parents.dim() != 2 or parents.numel() != rows.n_seqs or not 0 < parents.shape[1] <= MOST_SEQS:
             raise ValueError(f"parents must be [groups, beams] for the table's {rows.n_seqs} rows, of up to {MOST_SEQS} beams")
-        self._enqueue("zx_pages_fork", self._ref, C.byref(rows), parents.shape[1], parents.data_ptr(), e)
+        st = (_bound or _lib()).zx_pages_fork(self._ref, C.byref(rows), parents.shape[1], parents.data_ptr(), e, _stream_of(self._index))
+        if st != 0:
+            raise _zx.ZxError("zx_pages_fork", st)
 
     def trim(self, table: torch.Tensor, held: torch.Tensor, keep: Optional[torch.Tensor] = None, err: Optional[torch.Tensor] = None,
              stream=None) -> None:
@@ -227,7 +232,9 @@ class PagePool:
         if keep is not None and _int32(keep, "keep", self._index).shape != held.shape:
             raise ValueError("keep must be [rows]")
         rows, e = self._rows(table, held, err, *(() if keep is None else (_words(keep),)))
-        self._enqueue("zx_pages_trim", self._ref, C.byref(rows), None if keep is None else keep.data_ptr(), e)
+        st = (_bound or _lib()).zx_pages_trim(self._ref, C.byref(rows), None if keep is None else keep.data_ptr(), e, _stream_of(self._index))
+        if st != 0:
+            raise _zx.ZxError("zx_pages_trim", st)
 
     def extend(self, batch: PagedBatch, held: torch.Tensor, copies: Optional[PageCopies] = None, err: Optional[torch.Tensor] = None,
                stream=None) -> PageCopies:
@@ -250,12 +257,16 @@ class PagePool:
             raise ValueError(f"a batch of up to {MOST_SEQS} sequences")
         copies = self._list(copies, batch.n_seqs)
         c = batch._c
-        rows, e = self._rows(batch.page_table, held, err, *copies._spans, _words(batch.q_start), _words(batch.kv_len))
-        need = self._needs.get(c.n_seqs)
+        n, q, kv = c.n_seqs, c.q_start, c.kv_len
+        rows, e = self._rows_at(c.page_table or 0, n, c.table_width, held, err, (*copies._spans, (q, q + 4 * n + 4), (kv or 0, (kv or 0) + 4 * n)))
+        need = self._needs.get(n)
         if need is None:
-            need = self._needs[c.n_seqs] = _lib().zx_pages_extend_workspace_bytes(self._ref, c.n_seqs)
-        self._enqueue("zx_pages_extend", self._ref, C.byref(rows), c.q_start, c.max_q, c.max_kv, c.kv_len, copies._ref,
-                      self._bytes.new_empty(need).data_ptr(), need, e)
+            need = self._needs[n] = _lib().zx_pages_extend_workspace_bytes(self._ref, n)
+        # (the workspace is let go here; it is handed out again on this stream only, behind the call)
+        st = (_bound or _lib()).zx_pages_extend(self._ref, C.byref(rows), q, c.max_q, c.max_kv, kv, copies._ref, self._bytes.new_empty(need).data_ptr(),
+                                                need, e, _stream_of(self._index))
+        if st != 0:
+            raise _zx.ZxError("zx_pages_extend", st)
         return copies
 
     def compact(self, table: Optional[torch.Tensor] = None, held: Optional[torch.Tensor] = None, copies: Optional[PageCopies] = None,
@@ -286,7 +297,10 @@ class PagePool:
         need = self._needs.get(None)
         if need is None:
             need = self._needs[None] = _lib().zx_pages_compact_workspace_bytes(self._ref)
-        self._enqueue("zx_pages_compact", self._ref, C.byref(rows), remap.data_ptr(), copies._ref, self._bytes.new_empty(need).data_ptr(), need, e)
+        st = (_bound or _lib()).zx_pages_compact(self._ref, C.byref(rows), remap.data_ptr(), copies._ref, self._bytes.new_empty(need).data_ptr(), need, e,
+                                                 _stream_of(self._index))
+        if st != 0:
+            raise _zx.ZxError("zx_pages_compact", st)
         return copies, remap
 
 
@@ -335,6 +349,6 @@ def _copy(of, structs, n: int, copies: PageCopies, err: Optional[torch.Tensor], 
         for t in of._tensors:
             _paged._no_gradient(t, "a tensor of the caches")
     e = None if err is None else _int32(err, "err", of._index).data_ptr()
-    st = (_bound or _lib()).zx_paged_copy(structs, n, copies._ref, e, _zx._raw_stream(of.device))
+    st = (_bound or _lib()).zx_paged_copy(structs, n, copies._ref, e, _stream_of(of._index))
     if st != 0:
         raise _zx.ZxError("zx_paged_copy", st)

@@ -174,7 +174,7 @@ def test_caches_that_autograd_follows_are_not_copied_in():
     list_ = type("Copies", (), dict(device="cpu", pairs=t, count=t))
     of = type("Of", (), dict(_index=0, device="elsewhere", _tensors=(t,), _gradients=False))
     with pytest.MonkeyPatch.context() as m:
-        m.setattr(torch.cuda, "current_device", lambda: 0)
+        m.setattr(pages, "_device", lambda: 0)
         with pytest.raises(ValueError, match="the copies are on"):
             pages._copy(of, None, 1, list_, None, None)
         of.device = "cpu"
