@@ -2,7 +2,7 @@
 // over parts of a context joined.
 //
 // Both are bound by the bytes: every byte is read once and written once.  Copies: 512 pages of 8 heads x 64 tokens x 128 channels, BF16,
-// in 32 layers 4.9 TB/s read and written, the rate of a large copy; of 31 of the 64 tokens 3.8 (every other 8 KB: the card's
+// in 32 layers 5.2 TB/s read and written (a large copy 4.9 to 5.4); of 31 of the 64 tokens 4.2 (every other 8 KB: the card's
 // channels are not all met).  Joins: 4096 x 32 heads, five parts 36 us, 5.7 TB/s.
 #include "zx_paged.h"
 
@@ -28,7 +28,12 @@ struct CopyArgs {
     uint32_t kv_items, bound_items;              // workgroups' shares of a page's keys (or values) and of its bounds
 };
 
+// Whether a list of so many shares goes past the caches: more than the 256 MB that the last of them holds.  512 pages in 32 layers
+// (4.3 GB) 1736 us through them, 1645 past them; 8 pages in 32 layers, 31 tokens (33 MB), 17.5 and 19.6.
+constexpr uint64_t kManyShares = 16384;
+
 // `n` rows of 2^log_vecs pieces of each head, from piece `first` of them on.
+template <bool PAST>
 __device__ __forceinline__ void copy_rows(const uint8_t *src, uint8_t *dst, int64_t head, uint32_t token, uint32_t n, uint32_t heads,
                                           uint32_t log_vecs, uint32_t first)
 {
@@ -40,11 +45,17 @@ __device__ __forceinline__ void copy_rows(const uint8_t *src, uint8_t *dst, int6
     for (uint32_t i = 0; i < kVecs; ++i) {
         const uint32_t v = first + i * kThreads + threadIdx.x, row = v >> log_vecs, h = row / n, t = row - h * n;
         at[i] = v < all ? (int64_t)h * head + (int64_t)((uint64_t)t * token + ((v & ((1u << log_vecs) - 1)) << 4)) : -1;
-        if (at[i] >= 0) x[i] = *reinterpret_cast<const u4 *>(src + at[i]);
+        if (at[i] < 0) continue;
+        const u4 *from = reinterpret_cast<const u4 *>(src + at[i]);
+        x[i] = PAST ? __builtin_nontemporal_load(from) : *from;
     }
 #pragma unroll
     for (uint32_t i = 0; i < kVecs; ++i)
-        if (at[i] >= 0) *reinterpret_cast<u4 *>(dst + at[i]) = x[i];
+        if (at[i] >= 0) {
+            u4 *to = reinterpret_cast<u4 *>(dst + at[i]);
+            if (PAST) __builtin_nontemporal_store(x[i], to);
+            else *to = x[i];
+        }
 }
 
 // Items: for each pair and cache, shares of its keys, of its values and of its bounds.  A share is kThreads * kVecs
@@ -69,16 +80,32 @@ __global__ __launch_bounds__(kThreads) void k_paged_copy(CopyArgs g)
         if (from == to || n == 0) continue;
         const One &c = g.c[layer];
         constexpr uint32_t kShare = kThreads * kVecs;
-        if (share < g.kv_items)
-            copy_rows(c.k + (int64_t)from * c.k_page, c.k + (int64_t)to * c.k_page, c.k_head, c.k_token, n, g.heads, g.log_row, share * kShare);
-        else if (share < 2 * g.kv_items)
-            copy_rows(c.v + (int64_t)from * c.v_page, c.v + (int64_t)to * c.v_page, c.v_head, c.v_token, n, g.heads, g.log_row,
-                      (share - g.kv_items) * kShare);
-        else {
-            const uint32_t blocks = ((n - 1) >> g.log_block) + 1, row = 16u << g.log_bound;
-            const int64_t head = (int64_t)row << (g.log_page - g.log_block), page = head * g.heads;
-            copy_rows(c.bounds + from * page, c.bounds + to * page, head, row, blocks, g.heads, g.log_bound, (share - 2 * g.kv_items) * kShare);
+        const uint8_t *src;
+        uint8_t *dst;
+        int64_t head;
+        uint32_t token, rows = n, log_vecs = g.log_row, at = share;
+        if (share < g.kv_items) {
+            src = c.k + (int64_t)from * c.k_page;
+            dst = c.k + (int64_t)to * c.k_page;
+            head = c.k_head;
+            token = c.k_token;
+        } else if (share < 2 * g.kv_items) {
+            src = c.v + (int64_t)from * c.v_page;
+            dst = c.v + (int64_t)to * c.v_page;
+            head = c.v_head;
+            token = c.v_token;
+            at -= g.kv_items;
+        } else {
+            rows = ((n - 1) >> g.log_block) + 1;
+            log_vecs = g.log_bound;
+            token = 16u << g.log_bound;
+            head = (int64_t)token << (g.log_page - g.log_block);
+            src = c.bounds + from * (head * g.heads);
+            dst = c.bounds + to * (head * g.heads);
+            at -= 2 * g.kv_items;
         }
+        if (all > kManyShares) copy_rows<true>(src, dst, head, token, rows, g.heads, log_vecs, at * kShare);
+        else copy_rows<false>(src, dst, head, token, rows, g.heads, log_vecs, at * kShare);
     }
 }
 

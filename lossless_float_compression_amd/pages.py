@@ -316,14 +316,13 @@ class PagedLayers:
             if c._key != f._key or c.n_pages != f.n_pages or c.device != f.device:
                 raise ValueError("the caches must have one shape, type and device")
         self.caches, self.device, self._index = caches, f.device, f._index
-        pages = [t for c in caches for t in (c.k, c.v)]
-        steps = [sorted(((st, n) for st, n in zip(t.stride()[:3], t.shape[:3]) if n > 1), reverse=True) for t in pages]
-        order = sorted(range(len(pages)), key=lambda i: pages[i].data_ptr())
-        for at, i in enumerate(order):           # those that begin before this one ends
-            for j in order[at + 1:]:
-                if not _meets(pages[i], pages[j]):
+        pages = sorted(((*_span(t), t) for c in caches for t in (c.k, c.v)), key=lambda x: x[0])
+        steps = lambda t: sorted(((st, n) for st, n in zip(t.stride()[:3], t.shape[:3]) if n > 1), reverse=True)   # noqa: E731
+        for i, (p, q, t) in enumerate(pages):    # against those that begin before this one ends
+            for r, _, u in pages[i + 1:]:
+                if r >= q:
                     break
-                if _meet(steps[i], steps[j], (pages[j].data_ptr() - pages[i].data_ptr()) // pages[i].element_size(), f.head_dim):
+                if _meet(steps(t), steps(u), (r - p) // t.element_size(), f.head_dim):
                     raise ValueError("the caches must have pages of their own")
         bounds = sorted((_span(c.bounds) for c in caches if c.bounds is not None))
         if any(a[1] > b[0] for a, b in zip(bounds, bounds[1:])):
