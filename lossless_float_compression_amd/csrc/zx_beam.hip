@@ -11,7 +11,7 @@
 // finds the n_out best of them the same way.
 //
 // 64 x 8 of 128256, BF16, 16 out, a seventh of the beams finished: 29 + 6 us, 111 MB read (3.8 TB/s; without what follows the last tile 27, with
-// no exponentials 27); 256 x 8: 105 us, 5.0 TB/s; in 32 bits 190 us, 5.5 TB/s.  1 x 4 of 32000: 5.4 + 4.6.
+// no exponentials 27); 256 x 8: 98 us, 5.4 TB/s; in 32 bits 179 us, 5.9 TB/s.  1 x 4 of 32000: 5.4 + 4.6.
 // Tried, in us of k_beam_parts for 64 x 8: a part of 4096 logits held in registers by each wave, which ranks its own 75, then 34 with the maxima of
 // pieces kept and cheaper ranking, 33 with parts of a workgroup (every part pays for its edge and ranking); the next two tiles under way
 // 30.9, tiles of half the size 30.0.
@@ -28,6 +28,7 @@ namespace zxb {
 using zxk::report;
 
 typedef uint32_t u4 __attribute__((ext_vector_type(4)));
+typedef u4 u4_anywhere __attribute__((aligned(2)));  // 16 bytes that begin at any logit
 
 constexpr float kInf = __builtin_huge_valf();
 constexpr float kLowest = -3.4028234663852886e38f;
@@ -213,7 +214,8 @@ __device__ __forceinline__ u4 fetch(const uint8_t *row, uint32_t t, uint32_t voc
 {
     constexpr uint32_t N = Type<TY>::N, W = Type<TY>::W;
     u4 r{0, 0, 0, 0};
-    if (vocab >= N) __builtin_memcpy(&r, row + (uint64_t)(t + N <= vocab ? t : vocab - N) * W, 16);
+    // (a row is read once: past the caches 256 x 8 of 128256 98 us, through them 105)
+    if (vocab >= N) r = __builtin_nontemporal_load(reinterpret_cast<const u4_anywhere *>(row + (uint64_t)(t + N <= vocab ? t : vocab - N) * W));
     return r;
 }
 template <int TY>

@@ -159,3 +159,12 @@ def test_refusals():
         with pytest.raises(ValueError):
             call()
             pytest.fail(f"call {i} was taken")
+
+
+def test_parts_larger_than_the_caches():
+    """More bytes than 256 MB of parts are read another way: the same values."""
+    outs, lses = made(3, 12000, 32, 128)
+    whole = zx.merge_attention(outs, lses)
+    half = [zx.merge_attention([t[i:i + 4000] for t in outs], [t[i:i + 4000].contiguous() for t in lses]) for i in (0, 4000, 8000)]
+    assert torch.equal(whole, torch.cat(half))
+    check(whole[::37], None, [t[::37] for t in outs], [t[::37] for t in lses])
