@@ -495,7 +495,8 @@ zx_status zx_attention_merge(const zx_rows *parts, const float *const *lses, uin
  * less) is free.  A pool's pages may be those of many caches (a model's layers).  Row s of a table holds the pages of its first
  * ceil(held[s] / page_tokens) entries; what stands behind them is neither looked at nor changed, save where pages are given out.
  * Everything is read on the device when the work runs; a row whose length is negative or more than the table has room for
- * is left out, and an entry that is no page is skipped; both set err to ZX_E_CORRUPT.  Calls on one pool are ordered by the caller. */
+ * is left out, and an entry that is no page is skipped; both set err to ZX_E_CORRUPT.  Calls on one pool are ordered by the caller.
+ * The arrays of whole numbers here and below, and the floats that are not rows, need their elements' alignment only. */
 typedef struct zx_page_pool {
     uint32_t n_pages;              /* at most 2^23                                      */
     uint32_t page_tokens;          /* a power of two, 16..4096                          */

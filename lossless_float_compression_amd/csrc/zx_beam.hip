@@ -718,6 +718,8 @@ extern "C" zx_status zx_beam_select(const zx_beam_logits *in, const float *score
     if (in->n_groups == 0) return ZX_OK;
     const uintptr_t width = in->type == ZX_LOGITS_F32 ? 4 : 2;
     if (!in->logits || (uintptr_t)in->logits % width || !scores || !out_scores || !parents || !tokens || !out_finished) return ZX_E_INVAL;
+    if (((uintptr_t)scores | (uintptr_t)weights | (uintptr_t)allowed | (uintptr_t)out_scores | (uintptr_t)parents | (uintptr_t)tokens | (uintptr_t)err) & 3u)
+        return ZX_E_INVAL;
     if (!(scale > 0.0) || !(scale <= 1e30) || end < -1 || (end >= 0 && (uint32_t)end >= in->vocab) || (finished && end < 0)) return ZX_E_INVAL;
     if (in->group_stride > (1ull << 40) || in->beam_stride > (1ull << 40)) return ZX_E_INVAL;
     const uint64_t rows = (uint64_t)in->n_groups * in->beams;

@@ -183,6 +183,7 @@ extern "C" zx_status zx_paged_copy(const zx_paged_cache *caches, uint32_t n_cach
     using namespace zxp;
     if (n_caches == 0) return ZX_OK;
     if (!caches || !copies || !copies->count || (copies->cap && !copies->pairs)) return ZX_E_INVAL;
+    if (((uintptr_t)copies->count | (uintptr_t)copies->pairs | (uintptr_t)err) & 3u) return ZX_E_INVAL;
     if (n_caches > 65536) return ZX_E_LIMIT;
     const zx_paged_cache &f = caches[0];
     for (uint32_t i = 0; i < n_caches; ++i) {
@@ -234,9 +235,10 @@ extern "C" zx_status zx_attention_merge(const zx_rows *parts, const float *const
     zx_status st = make_rows(out, g.out);
     for (uint32_t i = 0; i < n_parts && st == ZX_OK; ++i) {
         st = make_rows(&parts[i], g.part[i]);
-        if (!lses[i]) st = ZX_E_INVAL;
+        if (!lses[i] || ((uintptr_t)lses[i] & 3u)) st = ZX_E_INVAL;
         g.lse[i] = lses[i];
     }
+    if (st == ZX_OK && ((uintptr_t)out_lse & 3u)) st = ZX_E_INVAL;
     if (st != ZX_OK) return st;
     if (n_tokens == 0) return ZX_OK;
     g.out_lse = out_lse;

@@ -545,9 +545,11 @@ __global__ __launch_bounds__(kThreads) void k_pages_compact(CompactArgs g)
 }
 
 // ---- host side
+inline bool al4(const void *p) { return ((uintptr_t)p & 3u) == 0; }
+
 zx_status make_pool(const zx_page_pool *p, uint32_t *err, Pool &o)
 {
-    if (!p || !p->refs || p->n_pages == 0 || !zxp::pow2_in(p->page_tokens, 16, 4096)) return ZX_E_INVAL;
+    if (!p || !p->refs || !al4(p->refs) || !al4(err) || p->n_pages == 0 || !zxp::pow2_in(p->page_tokens, 16, 4096)) return ZX_E_INVAL;
     if (p->n_pages > kMostPages) return ZX_E_LIMIT;
     o = Pool{p->refs, p->n_pages, zxp::log2_of(p->page_tokens), err};
     return ZX_OK;
@@ -556,14 +558,17 @@ zx_status make_pool(const zx_page_pool *p, uint32_t *err, Pool &o)
 zx_status make_rows(const zx_page_rows *r, const zx_page_pool *p, Rows &o)
 {
     if (!r) return ZX_E_INVAL;
-    if (r->n_seqs && (!r->held || (r->table_width && !r->page_table))) return ZX_E_INVAL;
+    if (r->n_seqs && (!r->held || (r->table_width && !r->page_table) || !al4(r->held) || !al4(r->page_table))) return ZX_E_INVAL;
     const uint64_t room = (uint64_t)r->table_width * p->page_tokens;
     if (room > 0x3FFFFFFFu || r->n_seqs > 65536) return ZX_E_LIMIT;
     o = Rows{r->page_table, r->held, r->n_seqs, r->table_width, (int32_t)room};
     return ZX_OK;
 }
 
-inline bool good_copies(const zx_page_copies *c, uint32_t least) { return c && c->count && c->cap >= least && (c->pairs || least == 0); }
+inline bool good_copies(const zx_page_copies *c, uint32_t least)
+{
+    return c && c->count && c->cap >= least && (c->pairs || least == 0) && al4(c->count) && al4(c->pairs);
+}
 
 inline zx_status launched() { return hipGetLastError() == hipSuccess ? ZX_OK : ZX_E_HIP; }
 
@@ -581,7 +586,7 @@ extern "C" zx_status zx_pages_fork(const zx_page_pool *pool, const zx_page_rows 
     if (beams == 0 || rows->n_seqs % beams) return ZX_E_INVAL;
     if (beams > kMostSeqs) return ZX_E_LIMIT;
     if (rows->n_seqs == 0) return ZX_OK;
-    if (!parents) return ZX_E_INVAL;
+    if (!parents || !al4(parents)) return ZX_E_INVAL;
     g.parents = parents;
     g.beams = beams;
     const uint32_t groups = rows->n_seqs / beams;
@@ -607,6 +612,7 @@ extern "C" zx_status zx_pages_trim(const zx_page_pool *pool, const zx_page_rows 
     zx_status st = make_pool(pool, err, p);
     if (st == ZX_OK) st = make_rows(rows, pool, r);
     if (st != ZX_OK || rows->n_seqs == 0) return st;
+    if (!al4(keep)) return ZX_E_INVAL;
     hipLaunchKernelGGL(k_pages_trim, dim3(r.n), dim3(r.n <= 256 && r.width > 512 ? 1024 : 256), 0, stream, p, r, keep);
     return launched();
 }
@@ -627,7 +633,7 @@ extern "C" zx_status zx_pages_extend(const zx_page_pool *pool, const zx_page_row
     if (st != ZX_OK) return st;
     if (rows->n_seqs > kMostSeqs) return ZX_E_LIMIT;
     if (!good_copies(copies, rows->n_seqs)) return ZX_E_INVAL;
-    if (rows->n_seqs && (!q_start || !kv_len)) return ZX_E_INVAL;
+    if (rows->n_seqs && (!q_start || !kv_len || !al4(q_start) || !al4(kv_len))) return ZX_E_INVAL;
     if (!workspace || ((uintptr_t)workspace & 15u) || ws_bytes < zx_pages_extend_workspace_bytes(pool, rows->n_seqs)) return ZX_E_INVAL;
     if ((uint32_t)g.r.cap > max_kv) g.r.cap = (int32_t)max_kv;
     g.q_start = q_start;
@@ -664,7 +670,7 @@ extern "C" zx_status zx_pages_compact(const zx_page_pool *pool, const zx_page_ro
     zx_status st = make_pool(pool, err, g.p);
     if (st == ZX_OK) st = make_rows(rows, pool, g.r);
     if (st != ZX_OK) return st;
-    if (!remap || !good_copies(copies, pool->n_pages / 2)) return ZX_E_INVAL;
+    if (!remap || !al4(remap) || !good_copies(copies, pool->n_pages / 2)) return ZX_E_INVAL;
     if (!workspace || ((uintptr_t)workspace & 15u) || ws_bytes < zx_pages_compact_workspace_bytes(pool)) return ZX_E_INVAL;
     g.remap = remap;
     g.pairs = copies->pairs;

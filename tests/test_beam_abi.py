@@ -37,7 +37,8 @@ def select(lib, n_out=8, scores=0x1000, weights=None, finished=None, end=-1, all
     (dict(outs=(0x2000, 0x3000, None, 0x5000)), INVAL), (dict(outs=(0x2000, 0x3000, 0x4000, None)), INVAL), (dict(scale=0.0), INVAL), (dict(scale=-1.0), INVAL),
     (dict(scale=math.nan), INVAL), (dict(scale=math.inf), INVAL), (dict(end=-2), INVAL), (dict(end=1000), INVAL), (dict(finished=0x9000), INVAL),
     (dict(group_stride=1 << 41), INVAL), (dict(beam_stride=1 << 41), INVAL), (dict(ws=None), INVAL), (dict(ws=0x10008), INVAL), (dict(ws_bytes=100), INVAL),
-    (dict(n_groups=1 << 30), LIMIT), (dict(n_groups=0), OK)])
+    (dict(n_groups=1 << 30), LIMIT), (dict(n_groups=0), OK), (dict(scores=0x1002), INVAL), (dict(weights=0x1001), INVAL), (dict(allowed=0x1002), INVAL),
+    (dict(outs=(0x2001, 0x3000, 0x4000, 0x5000)), INVAL), (dict(outs=(0x2000, 0x3000, 0x4002, 0x5000)), INVAL)])
 def test_select(lib, kw, want):
     assert select(lib, **kw) == want
 
@@ -64,7 +65,7 @@ def test_merge(lib):
         o = paged.zx_rows(0x20000, 512, 128) if out is None else out
         return lib.zx_attention_merge(r if parts else None, l if lses else None, n, tokens, heads, D, C.byref(o), None, None)
     assert call(tokens=0) == OK
-    for kw in (dict(n=0), dict(n=17), dict(heads=0), dict(heads=65537), dict(D=96), dict(D=0), dict(parts=False), dict(lses=False), dict(lse=None),
+    for kw in (dict(n=0), dict(n=17), dict(heads=0), dict(heads=65537), dict(D=96), dict(D=0), dict(parts=False), dict(lses=False), dict(lse=None), dict(lse=0x8002),
                dict(part=paged.zx_rows(0x10008, 512, 128)), dict(part=paged.zx_rows(None, 512, 128)), dict(part=paged.zx_rows(0x10000, 516, 128)),
                dict(out=paged.zx_rows(0x10000, 512, 1 << 41))):
         assert call(**kw) == INVAL, kw
@@ -92,13 +93,14 @@ def calls(lib, p=None, r=None, c=None):
 
 
 @pytest.mark.parametrize("kw,want", [(dict(n_pages=0), INVAL), (dict(n_pages=(1 << 23) + 1), LIMIT), (dict(page_tokens=8), INVAL), (dict(page_tokens=48), INVAL),
-                                     (dict(page_tokens=8192), INVAL), (dict(refs=None), INVAL)])
+                                     (dict(page_tokens=8192), INVAL), (dict(refs=None), INVAL), (dict(refs=0x1002), INVAL)])
 def test_pools(lib, kw, want):
     for name, got in calls(lib, p=pool(**kw)):
         assert got == want, name
 
 
-@pytest.mark.parametrize("kw,want", [(dict(page_table=None), INVAL), (dict(held=None), INVAL), (dict(n_seqs=65537), LIMIT), (dict(table_width=1 << 26), LIMIT)])
+@pytest.mark.parametrize("kw,want", [(dict(page_table=None), INVAL), (dict(held=None), INVAL), (dict(n_seqs=65537), LIMIT), (dict(table_width=1 << 26), LIMIT),
+                                     (dict(page_table=0x2001), INVAL), (dict(held=0x3002), INVAL)])
 def test_rows(lib, kw, want):
     for name, got in calls(lib, r=rows(**kw)):
         assert got == want, name
@@ -121,6 +123,12 @@ def test_pages(lib):
         a = good()
         a[i] = no
         assert e(*a) == INVAL, i
+    for i in (2, 5):
+        a = good()
+        a[i] = P(0x1002)
+        assert e(*a) == INVAL, i
+    assert f(pool(), rows(), 3, P(18), no, no) == INVAL and lib.zx_pages_trim(pool(), rows(), P(18), no, no) == INVAL
+    assert e(*good(c=copies(pairs=0x4001))) == INVAL and e(*good(c=copies(count=0x5002))) == INVAL
     k, ws = lib.zx_pages_compact, lib.zx_pages_compact_workspace_bytes
     need = ws(pool())
     assert need > 0 and ws(no) == 0
