@@ -114,7 +114,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: Optional[int]
         pa = _like(allowed, "allowed", torch.int32, (G, K, (V + 31) // 32), index).data_ptr()
     if not (0.0 < scale <= 1e30):
         raise ValueError("scale must be positive")
-    if logits.requires_grad or scores.requires_grad or _forward._current_level >= 0:
+    if logits.requires_grad or scores.requires_grad or (weights is not None and weights.requires_grad) or _forward._current_level >= 0:
         for t, name in ((logits, "logits"), (scores, "scores"), (weights, "weights")):
             if t is not None:
                 _no_gradient(t, name)
@@ -185,9 +185,10 @@ def merge_attention(outs: Sequence[torch.Tensor], lses: Sequence[torch.Tensor], 
     if not 0 < k <= 16 or len(lses) != k:
         raise ValueError("1 to 16 parts, each with its lse")
     f = outs[0]
-    if not isinstance(f, torch.Tensor) or f.dim() != 3 or f.shape[2] not in (64, 128, 256) or f.shape[1] == 0 or not f.is_cuda:
+    shape = f.shape if isinstance(f, torch.Tensor) else ()
+    if len(shape) != 3 or shape[2] not in (64, 128, 256) or shape[1] == 0 or not f.is_cuda:
         raise ValueError("outs must be bfloat16 device tensors [tokens, heads, 64, 128 or 256]")
-    shape, index, device = f.shape, f.get_device(), f.device
+    index, device = f.get_device(), f.device
     if _away(index, stream):
         return _elsewhere(device, stream, (*outs, *lses, out, lse), lambda s: merge_attention(outs, lses, out, lse, s))
     n, heads, d = shape

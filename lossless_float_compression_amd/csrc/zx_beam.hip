@@ -141,7 +141,8 @@ __device__ __forceinline__ uint32_t block_edge(uint32_t key, uint32_t n, EdgeRoo
     for (int level = 0;; ++level) {
         const uint32_t shift = width > 8 ? width - 8 : 0;
         const bool in = key >= base && (uint64_t)(key - base) >> width == 0 && key;
-        if (in && key - base >> shift) atomicAdd(&m.bins[level][(key - base) >> shift], 1u);         // (bin 0 is what is left)
+        const uint32_t bin = (key - base) >> shift;
+        if (in && bin) atomicAdd(&m.bins[level][bin], 1u);   // (bin 0 is what is left)
         __syncthreads();
         uint32_t c[4], all;
 #pragma unroll
@@ -162,12 +163,12 @@ __device__ __forceinline__ uint32_t block_edge(uint32_t key, uint32_t n, EdgeRoo
         const uint64_t some = __ballot(mine >= 0);
         if (some) {
             const int l = 63 - __builtin_clzll(some);
-            const uint32_t bin = 4u * (uint32_t)l + (uint32_t)__builtin_amdgcn_readlane(mine, l);
+            const uint32_t nth = 4u * (uint32_t)l + (uint32_t)__builtin_amdgcn_readlane(mine, l);
             reach = (uint32_t)__builtin_amdgcn_readlane((int)reach, l);
             above = (uint32_t)__builtin_amdgcn_readlane((int)above, l);
-            base += bin << shift;
+            base += nth << shift;
             // (bin 0 has not been counted)
-            if (bin && reach <= n + n / 2 + 4) return base;
+            if (nth && reach <= n + n / 2 + 4) return base;
         } else {
             above = all;
         }
