@@ -378,7 +378,8 @@ def test_refusals():
            lambda: zx.beam_select(x, s, allowed=torch.zeros((2, 4, 3), **i32)), lambda: zx.beam_select(x, s, allowed=torch.zeros((2, 4, 4), device="cuda")),
            lambda: zx.beam_select(x, s, out=mk(5)), lambda: zx.beam_select(x, s, 5, out=o), lambda: zx.beam_select(x, s, out=o._replace(tokens=o.parents)),
            lambda: zx.beam_select(x, s, weights=s, out=o._replace(scores=s)), lambda: zx.beam_select(x, s, err=torch.zeros(1, device="cuda")),
-           lambda: zx.beam_select(x.clone().requires_grad_(), s), lambda: zx.beam_select(x, s.clone().requires_grad_()), lambda: zx.beam_select(x, s, weights=s.clone().requires_grad_()),
+           lambda: zx.beam_select(x.clone().requires_grad_(), s), lambda: zx.beam_select(x, s.clone().requires_grad_()),
+           lambda: zx.beam_select(x, s, weights=s.clone().requires_grad_()),
            lambda: zx.beam_select(x, s, stream=0x1000)]
     for i, call in enumerate(bad):
         with pytest.raises(ValueError):
