@@ -142,9 +142,10 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: Optional[int]
         if len(_needs) >= _MOST_NEEDS:
             _needs.clear()
         need = _needs[key] = L.zx_beam_select_workspace_bytes(*key)
+    ws = raw(need)                               # (held until the launches are enqueued: the call lets other threads run)
     st = L.zx_beam_select(C.byref(zx_beam_logits(logits.data_ptr(), sg if G > 1 else 0, sk if K > 1 else 0, kind, G, K, V)), scores.data_ptr(),
                           pw, pf, end, pa, scale, M, out[0].data_ptr(), out[1].data_ptr(), out[2].data_ptr(), out[3].data_ptr(),
-                          raw(need).data_ptr(), need, e, _stream_of(index))
+                          ws.data_ptr(), need, e, _stream_of(index))
     if st != 0:
         raise _zx.ZxError("zx_beam_select", st)
     return out

@@ -262,9 +262,9 @@ class PagePool:
         need = self._needs.get(n)
         if need is None:
             need = self._needs[n] = _lib().zx_pages_extend_workspace_bytes(self._ref, n)
-        # (the workspace is let go here; it is handed out again on this stream only, behind the call)
-        st = (_bound or _lib()).zx_pages_extend(self._ref, C.byref(rows), q, c.max_q, c.max_kv, kv, copies._ref, self._bytes.new_empty(need).data_ptr(),
-                                                need, e, _stream_of(self._index))
+        ws = self._bytes.new_empty(need)         # (held until the launches are enqueued: the call lets other threads run)
+        st = (_bound or _lib()).zx_pages_extend(self._ref, C.byref(rows), q, c.max_q, c.max_kv, kv, copies._ref, ws.data_ptr(), need, e,
+                                                _stream_of(self._index))
         if st != 0:
             raise _zx.ZxError("zx_pages_extend", st)
         return copies
@@ -297,8 +297,8 @@ class PagePool:
         need = self._needs.get(None)
         if need is None:
             need = self._needs[None] = _lib().zx_pages_compact_workspace_bytes(self._ref)
-        st = (_bound or _lib()).zx_pages_compact(self._ref, C.byref(rows), remap.data_ptr(), copies._ref, self._bytes.new_empty(need).data_ptr(), need, e,
-                                                 _stream_of(self._index))
+        ws = self._bytes.new_empty(need)         # (held as in extend)
+        st = (_bound or _lib()).zx_pages_compact(self._ref, C.byref(rows), remap.data_ptr(), copies._ref, ws.data_ptr(), need, e, _stream_of(self._index))
         if st != 0:
             raise _zx.ZxError("zx_pages_compact", st)
         return copies, remap

@@ -1,0 +1,83 @@
+"""What the beam search's bindings do with their arguments and workspaces (CPU): host tensors that say they are the device's, and
+library functions that stand in for the kernels' entry points."""
+import weakref
+
+import pytest
+import torch
+
+import lossless_float_compression_amd as zx
+from lossless_float_compression_amd import beams, pages
+
+
+class Here(torch.Tensor):
+    """A host tensor that passes for one of the current device (index -1)."""
+    is_cuda = True
+
+
+def here(*shape, dtype=torch.int32):
+    return torch.zeros(shape, dtype=dtype).as_subclass(Here)
+
+
+class Spaces:
+    """Allocates workspaces, and knows whether the last one is still there."""
+
+    def __init__(self):
+        self.last = None
+
+    def new_empty(self, n):
+        t = torch.empty(n, dtype=torch.uint8)
+        self.last = weakref.ref(t)
+        return t
+
+    def holds(self, address):
+        t = self.last()
+        return t is not None and t.data_ptr() == address
+
+
+class Library:
+    """Entry points that note whether the workspace that they are given is held while they run."""
+
+    def __init__(self, spaces):
+        self.spaces, self.ran = spaces, []
+
+    def _size(self, *a):
+        return 4096
+
+    zx_beam_select_workspace_bytes = zx_pages_extend_workspace_bytes = zx_pages_compact_workspace_bytes = _size
+
+    def _call(self, name, at):
+        def call(*a):
+            self.ran.append((name, self.spaces.holds(a[at])))
+            return 0
+        return call
+
+    def __getattr__(self, name):
+        return self._call(name, {"zx_beam_select": 12, "zx_pages_extend": 7, "zx_pages_compact": 4}[name])
+
+
+@pytest.fixture
+def library(monkeypatch):
+    spaces = Spaces()
+    lib = Library(spaces)
+    for m in (beams, pages):
+        monkeypatch.setattr(m, "_bound", lib)
+        monkeypatch.setattr(m, "_stream_of", lambda index: None)
+    monkeypatch.setattr(beams, "_needs", {})
+    monkeypatch.setattr(pages, "_device", lambda: -1)
+    of = lambda t: torch.empty(0, dtype=t).new_empty                     # noqa: E731
+    monkeypatch.setattr(beams, "_makers", {-1: (of(torch.float32), of(torch.int32), of(torch.bool), spaces.new_empty)})
+    return lib
+
+
+def test_workspaces_are_held_until_the_launches_are_enqueued(library):
+    """An entry point runs without the interpreter's lock: memory let go before it returns can be given to another thread on the same stream,
+    whose launches then come between these."""
+    zx.beam_select(here(2, 4, 100, dtype=torch.bfloat16), here(2, 4, dtype=torch.float32))
+    pool = zx.PagePool(64, 16, refs=here(64))
+    pool._bytes = library.spaces
+    batch = zx.PagedBatch(here(5), here(4), here(4, 8))
+    copies = zx.PageCopies(64, pairs=here(64, 3), count=here(1))
+    pool.extend(batch, here(4), copies=copies)
+    pool.compact(here(4, 8), here(4), copies=copies, remap=here(64))
+    pool.compact(copies=copies, remap=here(64))
+    assert library.ran == [("zx_beam_select", True), ("zx_pages_extend", True), ("zx_pages_compact", True), ("zx_pages_compact", True)]
