@@ -586,7 +586,7 @@ typedef struct zx_beam_logits {    /* logit (g, b, t) at g * group_stride + b * 
  *   finished  u8[n_groups][beams], or NULL: none; needs end >= 0
  *   end       the token that ends a beam, or -1
  *   allowed   u32[n_groups][beams][ceil(vocab / 32)], bit t % 32 of word t / 32 for token t, or NULL: all
- *   scale     positive, at most 1e30 (one over a temperature)
+ *   scale     1e-36 to 1e30 (one over a temperature; smaller ones do not fit the kernel's 32 bits)
  *   n_out     1..64
  *   out_scores, parents, tokens, out_finished   float, int32, int32, u8 [n_groups][n_out]: a candidate's score, its beam
  *             (-1 behind the last candidate, with score -inf and token -1), its token, and whether it is finished: its beam was, or

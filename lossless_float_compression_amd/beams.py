@@ -77,7 +77,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: Optional[int]
     end       the token that ends a beam; None: none does
     allowed   int32 [groups, beams, ceil(vocab / 32)]: bit t % 32 of word t / 32 says whether token t may be taken; the softmax is over
               those that may.  None: all (logits of -inf are never taken)
-    scale     one over a temperature
+    scale     one over a temperature, 1e-36 to 1e30
     out       `Beams` to write into; `out.scores`, `out.finished` may be the `scores` and `finished` given
 
     Returns `Beams`; `finished` says that a candidate's beam was or its token is `end`.  Behind a group's last candidate: score -inf,
@@ -112,8 +112,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: Optional[int]
         pf = _like(finished, "finished", torch.bool, (G, K), index).data_ptr()
     if allowed is not None:
         pa = _like(allowed, "allowed", torch.int32, (G, K, (V + 31) // 32), index).data_ptr()
-    if not (0.0 < scale <= 1e30):
-        raise ValueError("scale must be positive")
+    if not (1e-36 <= scale <= 1e30):
+        raise ValueError("scale must be a number from 1e-36 to 1e30")
     if logits.requires_grad or scores.requires_grad or (weights is not None and weights.requires_grad) or _forward._current_level >= 0:
         for t, name in ((logits, "logits"), (scores, "scores"), (weights, "weights")):
             if t is not None:

@@ -34,6 +34,9 @@ constexpr float kInf = __builtin_huge_valf();
 constexpr float kLowest = -3.4028234663852886e38f;
 constexpr uint32_t kMostOut = 64, kMostBeams = 64;
 constexpr uint32_t kMostVocab = 1u << 24;
+// The scale times log2 e has to be a normal number in 32 bits (zero times -inf is NaN), and where a difference of two logits passes 32 bits
+// (3.4e38; it is -inf then) its exponential has to be nothing: e^-340 here.
+constexpr double kLeastScale = 1e-36;
 
 enum { BF16, F16, F32 };
 
@@ -721,7 +724,7 @@ extern "C" zx_status zx_beam_select(const zx_beam_logits *in, const float *score
     if (!in->logits || (uintptr_t)in->logits % width || !scores || !out_scores || !parents || !tokens || !out_finished) return ZX_E_INVAL;
     if (((uintptr_t)scores | (uintptr_t)weights | (uintptr_t)allowed | (uintptr_t)out_scores | (uintptr_t)parents | (uintptr_t)tokens | (uintptr_t)err) & 3u)
         return ZX_E_INVAL;
-    if (!(scale > 0.0) || !(scale <= 1e30) || end < -1 || (end >= 0 && (uint32_t)end >= in->vocab) || (finished && end < 0)) return ZX_E_INVAL;
+    if (!(scale >= kLeastScale) || !(scale <= 1e30) || end < -1 || (end >= 0 && (uint32_t)end >= in->vocab) || (finished && end < 0)) return ZX_E_INVAL;
     if (in->group_stride > (1ull << 40) || in->beam_stride > (1ull << 40)) return ZX_E_INVAL;
     const uint64_t rows = (uint64_t)in->n_groups * in->beams;
     if (!workspace || ((uintptr_t)workspace & 15u) || ws_bytes < zx_beam_select_workspace_bytes(in->type, in->n_groups, in->beams, in->vocab, n_out))

@@ -7,6 +7,8 @@ import torch
 
 import lossless_float_compression_amd as zx
 from lossless_float_compression_amd import beams, pages
+from test_beam_launches import select
+from test_paged_launches import ask  # noqa: F401
 
 
 class Here(torch.Tensor):
@@ -81,3 +83,28 @@ def test_workspaces_are_held_until_the_launches_are_enqueued(library):
     pool.compact(here(4, 8), here(4), copies=copies, remap=here(64))
     pool.compact(copies=copies, remap=here(64))
     assert library.ran == [("zx_beam_select", True), ("zx_pages_extend", True), ("zx_pages_compact", True), ("zx_pages_compact", True)]
+
+
+SMALLEST = 1e-36
+
+
+def test_scales_too_small_for_32_bits_are_refused(library):
+    """Below about 1e-45 the factor in 32 bits is zero and zero times minus infinity NaN; below 1e-38 differences of logits that pass
+    32 bits would still matter."""
+    x, s = here(2, 4, 100, dtype=torch.bfloat16), here(2, 4, dtype=torch.float32)
+    for scale in (5e-324, 1e-46, 1e-38, SMALLEST * (1 - 1e-6)):
+        with pytest.raises(ValueError, match="scale"):
+            zx.beam_select(x, s, scale=scale)
+    assert library.ran == []
+    for scale in (SMALLEST, 1e-30, 1e30):
+        zx.beam_select(x, s, scale=scale)
+    assert len(library.ran) == 3
+
+
+def test_the_entry_point_refuses_them_too(ask):  # noqa: F811
+    def one(scale):
+        c = select(0, 2, 4, 1000, 8)
+        c[1][6] = ["c_double", scale]
+        return c
+    got = ask([one(x) for x in (5e-324, 1e-46, 1e-38, SMALLEST * (1 - 1e-6), SMALLEST, 1e30, 1.1e30)])
+    assert [(ret, len(launches)) for ret, launches in got] == [(1, 0)] * 4 + [(0, 2)] * 2 + [(1, 0)]

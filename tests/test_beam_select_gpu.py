@@ -387,3 +387,18 @@ def test_refusals():
             pytest.fail(f"call {i} was taken")
     with torch.no_grad():
         zx.beam_select(x.clone().requires_grad_(), s)
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+def test_the_smallest_scale(dtype):
+    """All that may be taken are equal but for 1e-36 of their logits: logits of -inf and masked tokens have no share, any finite one has."""
+    x, s = made(2, 3, 2501, dtype)
+    x[0, 1, 5:] = -math.inf
+    if dtype is not torch.float16:
+        x[1, 1, ::2], x[1, 1, 1::2] = torch.finfo(dtype).max, -torch.finfo(dtype).max    # e^-680 apart
+    mask = torch.ones((2, 3, 2501), dtype=torch.bool, device="cuda")
+    mask[1, 2, :2400] = False
+    err = torch.zeros(1, dtype=torch.int32, device="cuda")
+    r = zx.beam_select(x, s, 12, allowed=bits_of(mask), scale=1e-36, err=err)
+    assert int(err) == 0
+    check(r, x, s, 12, allowed=bits_of(mask), scale=1e-36)
