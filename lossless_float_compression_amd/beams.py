@@ -12,6 +12,7 @@ from .pages import _away, _elsewhere, _meets, _stream_of
 from .paged import _apart, _int32, _no_gradient, zx_rows
 
 MOST_BEAMS = 64
+MOST_VOCAB = 1 << 24
 _LOGITS = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
 
 
@@ -95,6 +96,8 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: Optional[int]
     M = K if n_out is None else int(n_out)
     if not 0 < K <= MOST_BEAMS or not 0 < M <= MOST_BEAMS or V == 0:
         raise ValueError(f"1 to {MOST_BEAMS} beams, 1 to {MOST_BEAMS} candidates and a vocabulary, please")
+    if V > MOST_VOCAB or G > 0x7FFFFFFF // K:                # (counts are passed on in 32 bits)
+        raise ValueError("up to 2^24 tokens, and fewer than 2^31 beams in all")
     sg, sk, sv = logits.stride()
     if sv != 1 and V > 1:
         raise ValueError("logits: neighbouring tokens must lie side by side")

@@ -108,3 +108,13 @@ def test_the_entry_point_refuses_them_too(ask):  # noqa: F811
         return c
     got = ask([one(x) for x in (5e-324, 1e-46, 1e-38, SMALLEST * (1 - 1e-6), SMALLEST, 1e30, 1.1e30)])
     assert [(ret, len(launches)) for ret, launches in got] == [(1, 0)] * 4 + [(0, 2)] * 2 + [(1, 0)]
+
+
+@pytest.mark.parametrize("shape", [(1, 1, (1 << 24) + 1), (1, 1, (1 << 32) + 5), (1 << 31, 1, 1), ((1 << 32) + 2, 1, 1)])
+def test_sizes_past_32_bits_are_refused(library, shape):
+    """A count passed on in 32 bits would be taken for what is left of it."""
+    x = torch.empty(shape, dtype=torch.bfloat16, device="meta").as_subclass(Here)
+    s = torch.empty(shape[:2], device="meta").as_subclass(Here)
+    with pytest.raises(ValueError, match="2\\^24 tokens"):
+        zx.beam_select(x, s)
+    assert library.ran == []
