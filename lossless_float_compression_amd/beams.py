@@ -9,7 +9,7 @@ import torch.autograd.forward_ad as _forward
 
 from . import zx as _zx
 from .pages import _away, _elsewhere, _meets, _stream_of
-from .paged import _apart, _int32, _no_gradient, zx_rows
+from .paged import _apart, _int32, _meet, _no_gradient, zx_rows
 
 MOST_BEAMS = 64
 MOST_VOCAB = 1 << 24
@@ -176,6 +176,13 @@ def _part(t: torch.Tensor, name: str, shape, index: int, written: bool = False):
     return zx_rows(p, s0, s1), p, p + 2 * ((n - 1) * s0 + (h - 1) * s1 + d) if n else p
 
 
+def _shared(o: zx_rows, r: zx_rows, shape) -> bool:
+    """Whether rows that are written may share memory with a part's whose span they meet (parts may lie between each other's rows)."""
+    n, h, d = shape
+    steps = lambda x: sorted(((st, k) for st, k in ((x.token_stride, n), (x.head_stride, h)) if k > 1), reverse=True)   # noqa: E731
+    return not _apart((n, h), (r.token_stride, r.head_stride), d) or _meet(steps(o), steps(r), (r.p - o.p) // 2, d)
+
+
 def merge_attention(outs: Sequence[torch.Tensor], lses: Sequence[torch.Tensor], out: Optional[torch.Tensor] = None,
                     lse: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
     """Attention over parts of a context joined: outs[i] (bf16 [tokens, heads, 64, 128 or 256]) and lses[i] (float32 [tokens, heads]) are
@@ -210,7 +217,7 @@ def merge_attention(outs: Sequence[torch.Tensor], lses: Sequence[torch.Tensor], 
     else:
         o, p, q = _part(out, "out", shape, index, True)
         if any(p < x + size and x < q for x in where) or any(p < y and x < q and not (
-                x == p and r.token_stride == o.token_stride and r.head_stride == o.head_stride) for r, x, y in parts):
+                x == p and r.token_stride == o.token_stride and r.head_stride == o.head_stride) and _shared(o, r, shape) for r, x, y in parts):
             raise ValueError("out shares memory with a part and is not that part")
         if lse is not None and _meets(out, lse):
             raise ValueError("out and lse share memory")

@@ -49,12 +49,12 @@ class Library:
 
     def _call(self, name, at):
         def call(*a):
-            self.ran.append((name, self.spaces.holds(a[at])))
+            self.ran.append((name, at is None or self.spaces.holds(a[at])))
             return 0
         return call
 
     def __getattr__(self, name):
-        return self._call(name, {"zx_beam_select": 12, "zx_pages_extend": 7, "zx_pages_compact": 4}[name])
+        return self._call(name, {"zx_beam_select": 12, "zx_pages_extend": 7, "zx_pages_compact": 4, "zx_attention_merge": None}[name])
 
 
 @pytest.fixture
@@ -118,3 +118,29 @@ def test_sizes_past_32_bits_are_refused(library, shape):
     with pytest.raises(ValueError, match="2\\^24 tokens"):
         zx.beam_select(x, s)
     assert library.ran == []
+
+
+def test_joined_in_place_among_interleaved_parts(library):
+    """Parts side by side in one tensor, [token, part, head, channel] and others: one of them may be written. What shares
+    memory with another part is refused all the same."""
+    bf = dict(dtype=torch.bfloat16)
+    lses = [here(5, 4, dtype=torch.float32) for _ in range(3)]
+    layouts = (here(5, 3, 4, 64, **bf).unbind(1), here(5, 4, 3, 64, **bf).unbind(2), here(5, 4, 192, **bf).split(64, 2), here(3, 5, 4, 64, **bf).unbind(0),
+               [t.transpose(0, 1) for t in here(3, 4, 5, 64, **bf).unbind(0)])
+    for outs in layouts:
+        for i in range(3):
+            assert zx.merge_attention(outs, lses, out=outs[i]) is outs[i]
+        spare = here(5, 4, 64, **bf)
+        assert zx.merge_attention([outs[0], spare], lses[:2], out=outs[2]) is outs[2]        # beside them
+        assert zx.merge_attention([outs[0], outs[1], outs[1]], lses, out=outs[1]) is outs[1]
+    assert len(library.ran) == 25
+    one = here(8, 4, 64, **bf)
+    wide = here(5, 3, 4, 64, **bf)
+    flat = here(5 * 4 * 64 + 64, **bf)
+    bad = [([one[:5], one[3:]], one[:5]), ([one[1:6], one[:5]], one[:5]), ([wide[:, 0], wide[:, 1, :1].expand(5, 4, 64)], wide[:, 1]),
+           ([wide[:, 0], wide[:1, 1].expand(5, 4, 64)], wide[:, 1]), ([flat[:1280].view(5, 4, 64)], flat[8:1288].view(5, 4, 64)),
+           ([one[:5]], one[:5].flatten()[:1280].view(4, 5, 64).transpose(0, 1))]
+    for i, (outs, out) in enumerate(bad):
+        with pytest.raises(ValueError, match="shares memory"):
+            zx.merge_attention(outs, lses[:len(outs)], out=out)
+            pytest.fail(f"call {i} was taken")

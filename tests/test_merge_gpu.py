@@ -168,3 +168,26 @@ def test_parts_larger_than_the_caches():
     half = [zx.merge_attention([t[i:i + 4000] for t in outs], [t[i:i + 4000].contiguous() for t in lses]) for i in (0, 4000, 8000)]
     assert torch.equal(whole, torch.cat(half))
     check(whole[::37], None, [t[::37] for t in outs], [t[::37] for t in lses])
+
+
+@pytest.mark.parametrize("layout", ("parts ahead of heads", "parts behind heads", "parts side by side"))
+def test_in_place_among_interleaved_parts(layout):
+    """The parts in one tensor, one of them written: the others stay."""
+    outs, lses = made(3, 50, 4, 64)
+    if layout == "parts ahead of heads":
+        big = torch.stack(outs, 1)
+        mine = big.unbind(1)
+    elif layout == "parts behind heads":
+        big = torch.stack(outs, 2)
+        mine = big.unbind(2)
+    else:
+        big = torch.cat(outs, 2)
+        mine = big.split(64, 2)
+    want = zx.merge_attention(outs, lses)
+    check(want, None, outs, lses)
+    for i in range(3):
+        before = [t.clone() for t in mine]
+        assert torch.equal(zx.merge_attention(mine, lses, out=mine[i]), want)
+        for j in range(3):
+            assert torch.equal(mine[j].view(torch.int16), (want if j == i else before[j]).view(torch.int16))
+        mine[i].copy_(before[i])
