@@ -184,3 +184,36 @@ def test_refusals():
     # layers that lie between each other's pages are apart
     mixed = torch.zeros((4, 3, 2, 16, 64), dtype=torch.bfloat16, device="cuda")
     zx.PagedLayers([zx.PagedKVCache(4, 2, 64, 16, k=mixed[:, 0], v=mixed[:, 1]), b])
+
+
+PAST = 16384                             # shares of 16 KB of a list from which on it is carried out past the caches
+
+
+@pytest.mark.parametrize("layout", ("heads", "tokens", "side"))
+@pytest.mark.parametrize("dtype", (zx.BF16, zx.FP8_E4M3FN))
+@pytest.mark.parametrize("past", (False, True))
+@pytest.mark.parametrize("H,D,T,C,layers", [(1, 64, 16, None, 1), (2, 128, 64, 16, 2), (5, 64, 512, 64, 3), (3, 256, 32, 32, 1)])
+def test_long_lists(H, D, T, C, layers, past, dtype, layout):
+    """The longest list that goes through the caches and the shortest that goes past them: any number of tokens of each page, nothing else written."""
+    ceil = lambda a: -(-a // 16384)                                      # noqa: E731
+    per = layers * (2 * ceil(H * T * D * (2 if dtype == zx.BF16 else 1)) + (ceil(H * (T // C) * D * 4) if C else 0))
+    n = PAST // per + past
+    assert (n * per > PAST) == past
+    g = torch.Generator(device="cuda").manual_seed(n)
+    caches = [cache(2 * n + 3, H, D, T, dtype, C, g, layout) for _ in range(layers)]
+    perm = torch.randperm(2 * n + 3, generator=g, device="cuda").to(torch.int32)
+    src, dst = perm[:n], perm[n:2 * n]
+    some = torch.randint(0, T + 1, (n,), generator=g, device="cuda", dtype=torch.int32)
+    some[:3] = torch.tensor([T, 0, 1], dtype=torch.int32)
+    want = [pages(c) for c in caches]
+    for w in want:
+        for x, unit in zip(w, (1, 1, C)):
+            if x is not None:
+                m = (some + (unit - 1)) // unit
+                take = (torch.arange(x.shape[2], device="cuda") < m[:, None]).view(-1, 1, x.shape[2], *[1] * (x.dim() - 3))
+                x[dst.long()] = torch.where(take, x[src.long()], x[dst.long()])
+    err = i32([0])
+    zx.PagedLayers(caches).copy_pages(zx.PageCopies(n, pairs=torch.stack((src, dst, some), 1).contiguous(), count=i32([n])), err=err)
+    for c, w in zip(caches, want):
+        same(c, w)
+    assert int(err) == 0
