@@ -567,7 +567,8 @@ zx_status zx_paged_copy(const zx_paged_cache *caches, uint32_t n_caches, const z
  * Beam b of group g has scored score[g][b] so far.  With x its logits, s the scale and lse = ln sum_t e^(s x_t) over the tokens
  * that it may take, candidate (b, t) scores score[g][b] + s x_t - lse; a beam that is finished has the one candidate (b, end), which scores
  * score[g][b].  Of each group the n_out candidates with the largest weight[g][b] * score are taken, the best
- * first; of equal ones that of the earlier beam, then the earlier token.  Logits of -inf and tokens that `allowed` leaves out (whatever
+ * first; of equal ones that of the earlier beam, then (scores that only 64 bits do not tell apart) the larger logit, then the earlier
+ * token.  Logits of -inf and tokens that `allowed` leaves out (whatever
  * their logits are) are no candidates; a beam with score -inf is not there.  Beams with a NaN or +inf among their logits or as
  * score, or with a weight that is not positive and finite, have no candidates and set err to ZX_E_CORRUPT. */
 typedef enum { ZX_LOGITS_BF16 = 0, ZX_LOGITS_F16 = 1, ZX_LOGITS_F32 = 2 } zx_logit_type;

@@ -69,7 +69,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: Optional[int]
                 scale: float = 1.0, out: Optional[Beams] = None, err: Optional[torch.Tensor] = None, stream=None) -> Beams:
     """The n_out (1..64; default: as many as there are) best next beams of each group: beam b that has scored scores[g, b] goes on with token
     t for scores[g, b] + ln softmax(scale * logits[g, b])[t], and the candidates with the largest weights[g, b] times that are
-    taken (equal ones: the earlier beam, then the earlier token).
+    taken (equal ones: the earlier beam, then the larger logit, which scores in 64 bits may not show, then the earlier token).
 
     logits    bf16, fp16 or fp32 [groups, beams, vocab] (up to 64 beams, 2^24 tokens), any strides with neighbouring tokens
     scores    float32 [groups, beams]; -inf: the beam is not there (a search begins with all but one of them so)

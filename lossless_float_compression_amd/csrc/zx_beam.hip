@@ -482,10 +482,19 @@ __global__ __launch_bounds__(kThreads) void k_beam_parts(BeamArgs g)
 
 struct Best {
     uint64_t key;                                // orders like weight * total
-    uint64_t place;                              // beam << 32 | token
+    uint64_t place;                              // place_of
     double total;
 };
 constexpr uint32_t kList = 1024;
+
+// The order among equal totals: the earlier beam, then the larger logit (in 64 bits the totals of unlike ones may be equal), then the earlier token.
+// So a part's candidates, which are sorted by logit and token, are in this order too: whatever reaches an edge, all ahead of it do.
+constexpr uint32_t kTokenBits = 24, kBeamShift = 32 + kTokenBits;
+static_assert(kMostVocab <= 1u << kTokenBits && kMostBeams <= 1u << (64 - kBeamShift), "places fit 64 bits");
+__device__ __forceinline__ uint64_t place_of(uint32_t beam, float x, uint32_t token)
+{
+    return (uint64_t)beam << kBeamShift | (uint64_t)(0xFFFFFFFFu - ordered(x)) << kTokenBits | token;
+}
 
 __device__ __forceinline__ bool better(uint64_t ka, uint64_t pa, uint64_t kb, uint64_t pb) { return ka > kb || (ka == kb && pa < pb); }
 
@@ -549,7 +558,7 @@ __global__ __launch_bounds__(NT) void k_beam_pick(BeamArgs g)
         const uint32_t b = list / g.parts;
         if (kind[b] != 1 || v.x == -kInf) return false;
         o.total = base[b] + ((double)v.x - tops[b]) * g.scale;       // (score - ln sum) + s (x - top): no large logit swallows the rest
-        o.place = (uint64_t)b << 32 | v.token;
+        o.place = place_of(b, v.x, v.token);
         o.key = ordered(o.total * weight[b] + 0.0);
         return true;
     };
@@ -589,7 +598,7 @@ __global__ __launch_bounds__(NT) void k_beam_pick(BeamArgs g)
         if (tid < g.beams && kind[tid] == 2) {   // finished: one candidate
             Best v;
             v.total = base[tid];
-            v.place = (uint64_t)tid << 32 | (uint32_t)g.end;
+            v.place = place_of(tid, 0.0f, (uint32_t)g.end);
             v.key = ordered(v.total * weight[tid] + 0.0);
             enter(v);
         }
@@ -608,7 +617,7 @@ __global__ __launch_bounds__(NT) void k_beam_pick(BeamArgs g)
         auto put = [&](const Best &v, uint32_t r) {
             if (r >= g.n_out) return;
             const uint64_t to = (uint64_t)blockIdx.x * g.n_out + r;
-            const uint32_t b = (uint32_t)(v.place >> 32), t = (uint32_t)v.place;
+            const uint32_t b = (uint32_t)(v.place >> kBeamShift), t = (uint32_t)v.place & ((1u << kTokenBits) - 1u);
             g.out_scores[to] = (float)v.total;
             g.parents[to] = (int32_t)b;
             g.tokens[to] = (int32_t)t;

@@ -194,3 +194,15 @@ def test_graph(dtype):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(r, want))
         check(r, x, s, M)
+
+
+@pytest.mark.parametrize("scale,spread", [(1e-30, 3.0), (1.0, 1e-25)])
+@pytest.mark.parametrize("shape", [(2, 64, 6000, 64), (1, 3, 70000, 64), (300, 4, 700, 8), (5, 40, 20000, 33), (64, 8, 64128, 16)])
+@pytest.mark.parametrize("dtype", (torch.bfloat16, torch.float32))
+def test_scores_that_are_equal_in_64_bits(dtype, shape, scale, spread):
+    """Logits differ, scores do not: the earlier beam, then the larger logit; as many candidates as there are, though none of them stands out."""
+    G, K, V, M = shape
+    x, _ = made(G, K, V, dtype, seed=V, spread=spread)
+    s = torch.zeros((G, K), device="cuda")
+    s[::2, 0] = -1.0
+    check(zx.beam_select(x, s, M, scale=scale), x, s, M, scale=scale, exact=True)
