@@ -567,8 +567,8 @@ zx_status zx_paged_copy(const zx_paged_cache *caches, uint32_t n_caches, const z
  * Beam b of group g has scored score[g][b] so far.  With x its logits, s the scale and lse = ln sum_t e^(s x_t) over the tokens
  * that it may take, candidate (b, t) scores score[g][b] + s x_t - lse; a beam that is finished has the one candidate (b, end), which scores
  * score[g][b].  Of each group the n_out candidates with the largest weight[g][b] * score are taken, the best
- * first; of equal ones that of the earlier beam, then (scores that only 64 bits do not tell apart) the larger logit, then the earlier
- * token.  Logits of -inf and tokens that `allowed` leaves out (whatever
+ * first; of equal ones that of the earlier beam, then (where 64 bits do not tell the scores apart) that of the larger logit, then the
+ * earlier token.  Logits of -inf and tokens that `allowed` leaves out (whatever
  * their logits are) are no candidates; a beam with score -inf is not there.  Beams with a NaN or +inf among their logits or as
  * score, or with a weight that is not positive and finite, have no candidates and set err to ZX_E_CORRUPT. */
 typedef enum { ZX_LOGITS_BF16 = 0, ZX_LOGITS_F16 = 1, ZX_LOGITS_F32 = 2 } zx_logit_type;
@@ -593,7 +593,8 @@ typedef struct zx_beam_logits {    /* logit (g, b, t) at g * group_stride + b * 
  *             (-1 behind the last candidate, with score -inf and token -1), its token, and whether it is finished: its beam was, or
  *             its token is `end`
  *   workspace zx_beam_select_workspace_bytes(...) bytes, 16-byte aligned; its contents do not matter
- * Exponentials are summed in 32 bits over a few dozen logits and in 64 bits from there on; scores are formed and compared in 64 bits. */
+ * Exponentials are taken in 32 bits and summed in 32 bits over up to 256 logits (128 of FP32), in 64 bits from there on; scores are formed
+ * and compared in 64 bits, so what they are off by is lse's error (below 1e-5; beams closer than that may change places). */
 size_t zx_beam_select_workspace_bytes(int32_t type, uint32_t n_groups, uint32_t beams, uint32_t vocab, uint32_t n_out);
 zx_status zx_beam_select(const zx_beam_logits *in, const float *scores, const float *weights, const uint8_t *finished, int32_t end,
                          const uint32_t *allowed, double scale, uint32_t n_out, float *out_scores, int32_t *parents, int32_t *tokens,

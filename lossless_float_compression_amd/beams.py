@@ -83,7 +83,7 @@ def beam_select(logits: torch.Tensor, scores: torch.Tensor, n_out: Optional[int]
 
     Returns `Beams`; `finished` says that a candidate's beam was or its token is `end`.  Behind a group's last candidate: score -inf,
     parent and token -1, which `PagePool.fork` takes for an empty row.  Beams with NaN or +inf logits or scores, or weights that are not positive
-    numbers, are left out, with 4 in `err` (device int32 word).  Scores are formed and compared in 64 bits.  stream: a torch stream to run on
+    numbers, are left out, with 4 in `err` (device int32 word).  Scores are formed and compared in 64 bits, sums of exponentials begin in 32.  stream: a torch stream to run on
     after the work already enqueued on the current one."""
     if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dtype not in _LOGITS or logits.dim() != 3:
         raise ValueError("logits must be a bfloat16, float16 or float32 device tensor [groups, beams, vocab]")

@@ -10,17 +10,18 @@
 // (from L2) and the logits ranked by counting.  k_beam_pick: one workgroup a group joins the parts' sums, turns the parts' candidates into totals and
 // finds the n_out best of them the same way.
 //
-// 64 x 8 of 128256, BF16, 16 out, a seventh of the beams finished: 29 + 6 us, 111 MB read (3.8 TB/s; without what follows the last tile 27, with
-// no exponentials 27); 256 x 8: 98 us, 5.4 TB/s; in 32 bits 179 us, 5.9 TB/s.  1 x 4 of 32000: 5.4 + 4.6.
+// 64 x 8 of 128256, BF16, 16 out, a seventh of the beams finished: 28 + 6 us, 3.9 TB/s of the 111 MB that it needs (119 MB are read: the first
+// tile of a part is under way before its row's score and flag can leave it out; without what follows the last tile 27, with no exponentials 27); 256 x 8: 98 us, 5.4 TB/s; in 32 bits 179 us, 5.9 TB/s.  1 x 4 of 32000: 5.3 + 4.6.
 // Tried, in us of k_beam_parts for 64 x 8: a part of 4096 logits held in registers by each wave, which ranks its own 75, then 34 with the maxima of
 // pieces kept and cheaper ranking, 33 with parts of a workgroup (every part pays for its edge and ranking); the next two tiles under way
 // 30.9, tiles of half the size 30.0.
 //
 // Many equal logits at the edge do not fit the list of 256 that are ranked; then the part is read again from a sharper edge on (all logits
-// equal: 64 x 8 of 128256 300 us, 1 x 4 of 32000 60).
+// equal, whole calls: 64 x 8 of 128256 330 us, 1 x 4 of 32000 42).
 //
-// Rounding: exponentials are summed in 32 bits by a thread (up to 256 logits, four sums) and in 64 bits from there on; totals are
-// formed and compared in 64 bits, since which of two beams is taken must not turn on a rounding.
+// Rounding: exponentials are taken and summed in 32 bits by a thread (up to 256 logits, 128 in 32 bits, in four sums) and summed in 64 bits from there
+// on; totals are formed and compared in 64 bits, which adds nothing to the sums' error.  That error (below 1e-5 of a score, 3e-8 measured) is one for all of
+// a beam's candidates: their order is exact, and only beams closer than it may change places.
 #include "zx_common.h"
 
 namespace zxb {
@@ -456,7 +457,7 @@ __global__ __launch_bounds__(kThreads) void k_beam_parts(BeamArgs g)
     };
     if (v > kHits || n > kRoom) {
         // more than there is room for, as many equal logits are: the n_out-th of those that fit is a sharper edge, which
-        // leaves out kRoom - n_out of them at least
+        // leaves out kRoom - n_out of them at least, so the rounds end
         K ek = 0;
         for (;;) {
             __syncthreads();

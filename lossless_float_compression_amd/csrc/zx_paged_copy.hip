@@ -30,8 +30,10 @@ struct CopyArgs {
     uint32_t kv_items, bound_items;              // workgroups' shares of a page's keys (or values) and of its bounds
 };
 
-// Whether a list of so many shares goes past the caches: more than the 256 MB that the last of them holds.  512 pages in 32 layers
-// (4.3 GB) 1736 us through them, 1645 past them; 8 pages in 32 layers, 31 tokens (33 MB), 17.5 and 19.6.
+// Whether a list of so many shares of 16 KB goes past the caches: 256 MB of whole pages, which is what the last of them holds.  Shares are counted
+// by the list's length and the size of a page, whatever part of the pages is copied (the tokens stand on the device), so lists of partly filled pages go past
+// earlier.  512 pages in 32 layers (4.3 GB) 1736 us through them, 1645 past them; 8 pages in 32 layers, 31 tokens (33 MB), 17.5 and 19.6;
+// between these it has not been measured.
 constexpr uint64_t kManyShares = 16384;
 
 // `n` rows of 2^log_vecs pieces of each head, from piece `first` of them on.
